@@ -1,0 +1,250 @@
+"""Thin Python binding of the softmax-attention entry points of libkda.so.
+
+Attention over packed prompts (:func:`prefill`), an 8-bit paged key/value
+cache (:class:`KVCache`, :func:`append`), attention over it for single tokens
+and draft windows (:func:`decode`) and the eviction of its lightest pages
+(:func:`evict`), as declared in ``include/kda_attn.h``.  As in :mod:`kda`,
+functions check shapes, dtypes and devices, pass raw device pointers and the
+current CUDA stream, and raise ``KdaError`` on a negative status; all
+arithmetic runs in the library's kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from .kda import (KdaError, _check, _dtype_code, _need, _ptr, _scratch, _stream_handle,  # noqa: F401
+                  lib)
+
+PAGE_TOKENS = 64
+KDA_DEVERR_PAGE = 256
+MAX_DRAFT = 16
+
+EXPORTED = ("kda_attn_prefill", "kda_cache_append", "kda_attn_decode", "kda_attn_decode_workspace_bytes",
+            "kda_cache_evict")
+
+
+class KdaAttnDims(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class KdaKvCache(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64)]
+
+
+class KVCache(NamedTuple):
+    """The 8-bit cache: pages of 64 positions, one power-of-two scale per page and head."""
+    k_pages: torch.Tensor  # [num_pages, Hkv, 64, d] float8_e4m3fn
+    v_pages: torch.Tensor  # [num_pages, Hkv, d, 64] float8_e4m3fn
+    k_scale: torch.Tensor  # [num_pages, Hkv] fp32
+    v_scale: torch.Tensor  # [num_pages, Hkv] fp32
+
+
+class Evicted(NamedTuple):
+    seq_lens: torch.Tensor     # [B] int32
+    block_table: torch.Tensor  # [B, max_pages] int32
+    weight: torch.Tensor       # [B, max_pages] fp32
+    freed: torch.Tensor        # [B, max_pages] int32, -1 past freed_count
+    freed_count: torch.Tensor  # [B] int32
+
+
+_VP, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_PD, _PC = ctypes.POINTER(KdaAttnDims), ctypes.POINTER(KdaKvCache)
+
+
+def _declare(lib):
+    lib.kda_attn_prefill.argtypes = [_PD, _I32, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _VP, _VP]
+    lib.kda_cache_append.argtypes = [_PD, _PC, _I32, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _I32, _VP, _VP]
+    lib.kda_attn_decode.argtypes = [_PD, _PC, _I32, _I32, _VP, _I64, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP, _SZ,
+                                    _VP, _VP]
+    lib.kda_attn_decode_workspace_bytes.argtypes = [_PD, _I32, _I32, _I32, _I32]
+    lib.kda_cache_evict.argtypes = [_I32, _I32, _I32, _I32, _I32] + [_VP] * 10
+    for name in EXPORTED:
+        getattr(lib, name).restype = ctypes.c_int
+    lib.kda_attn_decode_workspace_bytes.restype = _SZ
+    return lib
+
+
+_lib = _declare(lib())
+
+
+def make_dims(q_heads: int, kv_heads: int, head_dim: int, dtype_code: int, scale: float | None = None) -> KdaAttnDims:
+    return KdaAttnDims(int(q_heads), int(kv_heads), int(head_dim), int(dtype_code),
+                       float(scale) if scale is not None else 0.0)
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype) -> int:
+    """Checks a tensor of token rows that may lie apart (a slice of a fused
+    projection) and returns the distance between tokens in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    H, d = shape[-2], shape[-1]
+    st = t.stride()
+    apart = st[-3]
+    if shape[-3] == 1 and len(shape) == 3 or t.numel() == 0:
+        apart = max(apart, H * d)  # the distance is never used
+    ok = st[-1] == 1 and (H == 1 or st[-2] == d) and apart >= H * d
+    if len(shape) == 4 and shape[0] > 1 and t.numel():
+        if shape[1] == 1:
+            apart = st[0]
+        ok = ok and apart >= H * d and st[0] == shape[1] * apart
+    if not ok:
+        raise ValueError(f"{name} must have contiguous [heads, d] rows at one distance")
+    if (apart * t.element_size()) % 16 or t.data_ptr() % 16:
+        raise ValueError(f"{name}'s rows must start on 16-byte boundaries")
+    return apart
+
+
+def _check_cache(c: KVCache):
+    N, Hkv, page, d = c.k_pages.shape
+    if page != PAGE_TOKENS:
+        raise ValueError(f"k_pages has {page} positions per page, expected {PAGE_TOKENS}")
+    f8 = torch.float8_e4m3fn
+    _need(c.k_pages, "k_pages", (N, Hkv, PAGE_TOKENS, d), f8)
+    _need(c.v_pages, "v_pages", (N, Hkv, d, PAGE_TOKENS), f8)
+    _need(c.k_scale, "k_scale", (N, Hkv), torch.float32)
+    _need(c.v_scale, "v_scale", (N, Hkv), torch.float32)
+    return Hkv, d, KdaKvCache(c.k_pages.data_ptr(), c.v_pages.data_ptr(), c.k_scale.data_ptr(), c.v_scale.data_ptr(), N)
+
+
+def alloc_cache(num_pages: int, kv_heads: int, head_dim: int, device="cuda") -> KVCache:
+    """An empty cache of ``num_pages`` pages of 64 positions."""
+    f8 = torch.float8_e4m3fn
+    return KVCache(torch.zeros((num_pages, kv_heads, PAGE_TOKENS, head_dim), dtype=torch.uint8, device=device).view(f8),
+                   torch.zeros((num_pages, kv_heads, head_dim, PAGE_TOKENS), dtype=torch.uint8, device=device).view(f8),
+                   torch.ones((num_pages, kv_heads), dtype=torch.float32, device=device),
+                   torch.ones((num_pages, kv_heads), dtype=torch.float32, device=device))
+
+
+def prefill(q, k, v, cu_seqlens, out=None, *, lse=None, return_lse=False, scale=None, err_flag=None, stream=None):
+    """Causal attention over packed prompts.
+
+    q: [T, Hq, d]; k, v: [T, Hkv, d], Hq a multiple of Hkv (rows may lie apart,
+    as slices of one projection); cu_seqlens: [n + 1] int32.  Returns out
+    [T, Hq, d], with ``return_lse`` also lse [T, Hq] fp32 (natural log).
+    """
+    T, Hq, d = q.shape
+    Hkv, dt = k.shape[1], q.dtype
+    code = _dtype_code(q)
+    qs, ks, vs = (_rows(q, "q", (T, Hq, d), dt), _rows(k, "k", (T, Hkv, d), dt), _rows(v, "v", (T, Hkv, d), dt))
+    n = cu_seqlens.shape[0] - 1
+    _need(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+    else:
+        _need(out, "out", (T, Hq, d), dt)
+    if lse is None:
+        if return_lse:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    else:
+        _need(lse, "lse", (T, Hq), torch.float32)
+    dims = make_dims(Hq, Hkv, d, code, scale)
+    _check(_lib.kda_attn_prefill(ctypes.byref(dims), n, _ptr(cu_seqlens), T, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
+                                 _ptr(out), _ptr(lse), _ptr(err_flag), _stream_handle(stream)), "kda_attn_prefill")
+    return (out, lse) if return_lse else out
+
+
+def append(cache: KVCache, k, v, cu_seqlens, start_pos, block_table, *, err_flag=None, stream=None):
+    """Quantises packed new tokens into the cache, after the ``start_pos``
+    positions that each sequence holds.
+
+    k, v: [T, Hkv, d]; cu_seqlens: [n + 1] int32; start_pos: [n] int32;
+    block_table: [n, max_pages] int32.
+    """
+    Hkv, d, c = _check_cache(cache)
+    T, dt = k.shape[0], k.dtype
+    code = _dtype_code(k)
+    ks, vs = _rows(k, "k", (T, Hkv, d), dt), _rows(v, "v", (T, Hkv, d), dt)
+    n, width = block_table.shape
+    _need(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32)
+    _need(start_pos, "start_pos", (n,), torch.int32)
+    _need(block_table, "block_table", (n, width), torch.int32)
+    dims = make_dims(Hkv, Hkv, d, code)
+    _check(_lib.kda_cache_append(ctypes.byref(dims), ctypes.byref(c), n, _ptr(cu_seqlens), T, _ptr(k), ks, _ptr(v), vs,
+                                 _ptr(start_pos), _ptr(block_table), width, _ptr(err_flag), _stream_handle(stream)),
+           "kda_cache_append")
+
+
+def decode_workspace_bytes(q_heads, kv_heads, head_dim, dtype_code, batch, draft_len, max_pages, with_weight) -> int:
+    """Bytes of workspace that :func:`decode` needs."""
+    dims = make_dims(q_heads, kv_heads, head_dim, dtype_code)
+    return _lib.kda_attn_decode_workspace_bytes(ctypes.byref(dims), batch, draft_len, max_pages, 1 if with_weight else 0)
+
+
+def decode(q, cache: KVCache, seq_lens, block_table, out=None, *, lse=None, return_lse=False, weight_in=None,
+           weight_out=None, return_weight=False, workspace=None, scale=None, err_flag=None, stream=None):
+    """Attention of each sequence's last D (1..16) tokens, which are in the
+    cache already; token t sees the positions before seq_lens - D + 1 + t.
+
+    q: [B, D, Hq, d]; seq_lens: [B] int32 (0: padding); block_table:
+    [B, max_pages] int32.  Returns out [B, D, Hq, d], then with ``return_lse``
+    lse [B, D, Hq] fp32, then with ``return_weight`` (or ``weight_out``) the
+    page weights [B, max_pages] fp32: ``weight_in`` (zero without it) plus the
+    attention weight that this call's rows gave to each page.
+    """
+    Hkv, d, c = _check_cache(cache)
+    B, D, Hq, _ = q.shape
+    dt = q.dtype
+    code = _dtype_code(q)
+    qs = _rows(q, "q", (B, D, Hq, d), dt)
+    width = block_table.shape[1]
+    _need(seq_lens, "seq_lens", (B,), torch.int32)
+    _need(block_table, "block_table", (B, width), torch.int32)
+    if out is None:
+        out = torch.empty((B, D, Hq, d), dtype=dt, device=q.device)
+    else:
+        _need(out, "out", (B, D, Hq, d), dt)
+    if lse is None:
+        if return_lse:
+            lse = torch.empty((B, D, Hq), dtype=torch.float32, device=q.device)
+    else:
+        _need(lse, "lse", (B, D, Hq), torch.float32)
+    if weight_in is not None:
+        _need(weight_in, "weight_in", (B, width), torch.float32)
+    if weight_out is not None:
+        _need(weight_out, "weight_out", (B, width), torch.float32)
+    elif return_weight or weight_in is not None:
+        weight_out = torch.empty((B, width), dtype=torch.float32, device=q.device)
+    dims = make_dims(Hq, Hkv, d, code, scale)
+    pd = ctypes.byref(dims)
+    if workspace is None:
+        need = _lib.kda_attn_decode_workspace_bytes(pd, B, D, width, 0 if weight_out is None else 1)
+        workspace = _scratch(need, q.device, stream)
+    else:
+        need = workspace.numel() * workspace.element_size()
+    _check(_lib.kda_attn_decode(pd, ctypes.byref(c), B, D, _ptr(q), qs, _ptr(seq_lens), _ptr(block_table), width,
+                                _ptr(out), _ptr(lse), _ptr(weight_in), _ptr(weight_out), _ptr(workspace), need,
+                                _ptr(err_flag), _stream_handle(stream)), "kda_attn_decode")
+    got = (out,) + ((lse,) if return_lse else ()) + ((weight_out,) if weight_out is not None else ())
+    return got if len(got) > 1 else out
+
+
+def evict(seq_lens, block_table, weight, budget: int, sink: int = 1, recent: int = 1, *, in_place=False,
+          err_flag=None, stream=None) -> Evicted:
+    """Drops the lightest pages of sequences that hold more than ``budget``;
+    the first ``sink`` and last ``recent`` pages stay.
+
+    seq_lens: [B] int32; block_table: [B, max_pages] int32; weight:
+    [B, max_pages] fp32.  With ``in_place`` these three are updated.
+    """
+    B, width = block_table.shape
+    _need(seq_lens, "seq_lens", (B,), torch.int32)
+    _need(block_table, "block_table", (B, width), torch.int32)
+    _need(weight, "weight", (B, width), torch.float32)
+    if in_place:
+        lens, table, w = seq_lens, block_table, weight
+    else:
+        lens, table, w = torch.empty_like(seq_lens), torch.empty_like(block_table), torch.empty_like(weight)
+    freed, count = torch.empty_like(block_table), torch.empty_like(seq_lens)
+    _check(_lib.kda_cache_evict(B, width, int(budget), int(sink), int(recent), _ptr(seq_lens), _ptr(block_table),
+                                _ptr(weight), _ptr(lens), _ptr(table), _ptr(w), _ptr(freed), _ptr(count),
+                                _ptr(err_flag), _stream_handle(stream)), "kda_cache_evict")
+    return Evicted(lens, table, w, freed, count)

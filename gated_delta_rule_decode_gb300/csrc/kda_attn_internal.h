@@ -1,0 +1,96 @@
+// Launch interface between the attention entry points (kda_attn_api.cu) and
+// their kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_attn.h"
+
+namespace kda {
+
+constexpr int kPage = KDA_PAGE_TOKENS;
+
+struct AttnPrefillParams {
+    const int32_t *cu_seqlens;
+    int64_t total_tokens;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    void *out;
+    float *lse;
+    int32_t *err_flag;
+    int32_t num_seqs, Hq, Hkv, G;
+    float scale;
+};
+
+struct CacheAppendParams {
+    unsigned char *k_pages, *v_pages;
+    float *k_scale, *v_scale;
+    int64_t num_pages;
+    const int32_t *cu_seqlens;
+    int64_t total_tokens;
+    const void *k, *v;
+    int64_t k_stride, v_stride;
+    const int32_t *start_pos, *block_table;
+    int32_t *err_flag;
+    int32_t num_seqs, Hkv, max_pages;
+};
+
+struct AttnDecodeParams {
+    const unsigned char *k_pages, *v_pages;
+    const float *k_scale, *v_scale;
+    int64_t num_pages;
+    const void *q;
+    int64_t q_stride;
+    const int32_t *seq_lens, *block_table;
+    void *out;
+    float *lse;
+    const float *weight_in;
+    float *weight_out;
+    void *workspace;
+    int32_t *err_flag;
+    int32_t batch, D, Hq, Hkv, G, max_pages;
+    float scale;
+};
+
+struct CacheEvictParams {
+    const int32_t *seq_lens, *block_table;
+    const float *weight;
+    int32_t *seq_lens_out, *block_table_out;
+    float *weight_out;
+    int32_t *freed, *freed_count, *err_flag;
+    int32_t batch, max_pages, budget, sink, recent;
+};
+
+// The packed sequence that owns unit u when sequence s gets the units
+// [cu[s] / per + s, cu[s+1] / per + s + 1): at least ceil(len / per) of them,
+// found by bisection on cu_seqlens alone.  Also gives the unit's index within
+// the sequence.  Reads cu[0..num_seqs] only, whatever the offsets hold.
+__device__ __forceinline__ int seq_of_unit(const int32_t *cu, int num_seqs, int per, int extra, int64_t u,
+                                           int64_t &local) {
+    int a = 0, b = num_seqs - 1;  // last s with its first unit <= u
+    while (a < b) {
+        const int m = (a + b + 1) >> 1;
+        if ((int64_t)(cu[m] / per) + (int64_t)m * extra <= u) a = m; else b = m - 1;
+    }
+    local = u - ((int64_t)(cu[a] / per) + (int64_t)a * extra);
+    return a;
+}
+
+// Token range of sequence s; false (and KDA_DEVERR_SEQLENS) when it is not one.
+__device__ __forceinline__ bool seq_range(const int32_t *cu, int s, int64_t total, int32_t *err, int &lo, int &hi) {
+    lo = cu[s];
+    hi = cu[s + 1];
+    if (lo >= 0 && lo <= hi && (int64_t)hi <= total) return true;
+    if (err) atomicOr(err, KDA_DEVERR_SEQLENS);
+    return false;
+}
+
+cudaError_t launch_attn_prefill(const AttnPrefillParams &p, int d, int dtype, cudaStream_t s);
+cudaError_t launch_cache_append(const CacheAppendParams &p, int d, int dtype, cudaStream_t s);
+size_t attn_decode_workspace_bytes(int Hq, int Hkv, int d, int dtype, int64_t batch, int D, int64_t max_pages,
+                                   bool with_weight);
+cudaError_t launch_attn_decode(const AttnDecodeParams &p, int d, int dtype, cudaStream_t s);
+cudaError_t launch_cache_evict(const CacheEvictParams &p, cudaStream_t s);
+
+}  // namespace kda

@@ -1,0 +1,345 @@
+// The 8-bit paged key/value cache: append (quantisation) and page eviction.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+#include "kda_attn_internal.h"
+#include "kda_check.cuh"
+
+namespace kda {
+namespace {
+
+// ---------------------------------------------------------------- append
+//
+// One CTA per (page that gets new rows, head, keys or values).  The page's
+// new rows (up to 64) are loaded once into registers as 16-byte pieces, a
+// block reduction gives their largest finite magnitude and so the scale, and
+// the rows leave as bytes: keys as they lie, values through a shared tile
+// that turns them into one row of positions per channel.
+//
+// The scale is a power of two, so x / s' is exact and a page whose scale
+// grows re-rounds only what becomes subnormal in e4m3.
+constexpr int kAppendThreads = 128;
+
+__device__ __forceinline__ float pow2_need(float amax) {
+    // smallest e >= -126 with amax <= 1.75 * 2^8 * 2^e
+    const uint32_t b = __float_as_uint(amax);
+    const int x = (int)(b >> 23) - 127;
+    int e = x - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = e < -126 ? -126 : e;
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// 1 / s for a power of two s in 2^-126..2^120.
+__device__ __forceinline__ float pow2_inverse(float s) {
+    const uint32_t e = __float_as_uint(s) >> 23;
+    return __uint_as_float((254u - e) << 23);
+}
+
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a <= 3.402823466e38f ? a : 0.f;  // false for infinities and NaN
+}
+
+__device__ __forceinline__ uint32_t quant2(float a, float b) {
+    // saturates to +-448, keeps NaN, rounds to nearest even
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ unsigned char requant1(unsigned char b, float ratio) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(b, __NV_E4M3);
+    return (unsigned char)__nv_cvt_float_to_fp8(__half2float(__half(h)) * ratio, __NV_SATFINITE, __NV_E4M3);
+}
+
+template <typename T>
+struct Piece;  // 16 bytes of a row as floats
+template <>
+struct Piece<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void get(const uint4 &u, float (&x)[4]) {
+        x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
+        x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+    }
+};
+template <>
+struct Piece<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void get(const uint4 &u, float (&x)[8]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const CacheAppendParams p) {
+    constexpr int N = Piece<T>::N;                  // elements per 16-byte piece
+    constexpr int PR = HD / N;                      // pieces per row
+    constexpr int RS = kAppendThreads / PR;         // rows per step of the block
+    constexpr int STEPS = (kPage + RS - 1) / RS;
+    __shared__ __align__(16) unsigned char tile[HD][kPage + 4];
+    __shared__ float warp_max[kAppendThreads / 32];
+    const int tid = threadIdx.x, h = blockIdx.y;
+    const bool is_v = blockIdx.z != 0;
+
+    int64_t c = 0;
+    const int s = seq_of_unit(p.cu_seqlens, p.num_seqs, kPage, 2, blockIdx.x, c);
+    int t0, t1;
+    if (!seq_range(p.cu_seqlens, s, p.total_tokens, p.err_flag, t0, t1)) return;
+    const int64_t start = p.start_pos[s];
+    if (t1 == t0 || start < 0) return;
+    const int64_t end = start + (t1 - t0);
+    const int64_t page_idx = start / kPage + c;
+    if (page_idx * kPage >= end) return;
+    const int64_t lo = page_idx * kPage > start ? page_idx * kPage : start;
+    const int64_t hi = (page_idx + 1) * kPage < end ? (page_idx + 1) * kPage : end;
+    const int rows = (int)(hi - lo), off = (int)(lo - page_idx * kPage);
+    const int page = page_idx < p.max_pages ? p.block_table[(int64_t)s * p.max_pages + page_idx] : -1;
+    if (page < 0 || page >= p.num_pages) {
+        if (tid == 0 && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
+        return;
+    }
+
+    const int64_t stride = is_v ? p.v_stride : p.k_stride;
+    const T *src = static_cast<const T *>(is_v ? p.v : p.k) + ((int64_t)t0 + (lo - start)) * stride + (int64_t)h * HD;
+    const int r0 = tid / PR, piece = tid % PR;
+    uint4 raw[STEPS];
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int r = r0 + i * RS;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (r < rows) raw[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)r * stride + piece * N);
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        float x[N];
+        Piece<T>::get(raw[i], x);
+#pragma unroll
+        for (int j = 0; j < N; ++j) amax = fmaxf(amax, finite_abs(x[j]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+    if ((tid & 31) == 0) warp_max[tid >> 5] = amax;
+    float *scale = (is_v ? p.v_scale : p.k_scale) + (int64_t)page * p.Hkv + h;
+    const float old = off > 0 ? *scale : 0.f;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, warp_max[w]);
+    const float now = fmaxf(old, pow2_need(amax));
+    const float inv = pow2_inverse(now);
+    const int64_t base = ((int64_t)page * p.Hkv + h) * (int64_t)(HD * kPage);
+    unsigned char *dst = (is_v ? p.v_pages : p.k_pages) + base;
+
+    if (off > 0 && now > old) {  // the page's earlier rows take the new scale
+        const float ratio = old * inv;
+        for (int i = tid; i < off * HD; i += kAppendThreads) {
+            unsigned char *b = is_v ? dst + (i / off) * kPage + i % off : dst + i;
+            *b = requant1(*b, ratio);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int r = r0 + i * RS;
+        if (r >= rows) continue;
+        float x[N];
+        Piece<T>::get(raw[i], x);
+        uint32_t w[N / 4];
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j)
+            w[j] = quant2(x[4 * j] * inv, x[4 * j + 1] * inv) | (quant2(x[4 * j + 2] * inv, x[4 * j + 3] * inv) << 16);
+        if (!is_v) {
+            uint32_t *o = reinterpret_cast<uint32_t *>(dst + (off + r) * HD + piece * N);
+            if constexpr (N == 8) *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+            else *o = w[0];
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) tile[piece * N + j][off + r] = (unsigned char)(w[j / 4] >> (8 * (j % 4)));
+        }
+    }
+    if (tid == 0) *scale = now;
+    if (!is_v) return;
+    __syncthreads();
+    // words of four positions that are all new, single bytes at the two ends
+    const int last = off + rows;
+    const int w0 = off / 4, nw = (last + 3) / 4 - w0;
+    for (int i = tid; i < HD * nw; i += kAppendThreads) {
+        const int ch = i / nw, pos = 4 * (w0 + i % nw);
+        if (pos >= off && pos + 4 <= last) {
+            *reinterpret_cast<uint32_t *>(dst + ch * kPage + pos) = *reinterpret_cast<const uint32_t *>(&tile[ch][pos]);
+        } else {
+            for (int j = pos; j < pos + 4; ++j)
+                if (j >= off && j < last) dst[ch * kPage + j] = tile[ch][j];
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_append(const CacheAppendParams &p, int d, cudaStream_t st) {
+    // units of seq_of_unit: cu / 64 + 2 s, so every sequence has its pages
+    const int64_t units = p.total_tokens / kPage + 2 * (int64_t)p.num_seqs;
+    if (units > 0x7fffffff) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)units, (unsigned)p.Hkv, 2);
+    if (d == 128) append_kernel<T, 128><<<grid, kAppendThreads, 0, st>>>(p);
+    else if (d == 64) append_kernel<T, 64><<<grid, kAppendThreads, 0, st>>>(p);
+    else append_kernel<T, 32><<<grid, kAppendThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- evict
+//
+// One CTA per sequence.  The E = P - budget lightest pages of the middle go:
+// a radix selection over the weights as ordered integers (8 bits a pass, the
+// histogram in shared memory) finds the weight t of the last page to go and
+// how many of the pages that weigh exactly t go with the lighter ones; of
+// those the higher indices go.  Then one pass in index order closes the rows
+// up.  An entry never moves to a higher index, and a chunk is read before
+// anything of it is written, so the rows may be updated in place.
+constexpr int kEvictThreads = 512;
+
+__device__ __forceinline__ uint32_t weight_key(float w) {
+    if (!(w == w)) return 0;  // NaN below everything
+    const uint32_t b = __float_as_uint(w == 0.f ? 0.f : w);  // -0 as 0
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kEvictThreads) evict_kernel(const CacheEvictParams p) {
+    constexpr int W = kEvictThreads / 32;
+    __shared__ uint32_t hist[256];
+    __shared__ uint32_t s_prefix, s_left;
+    __shared__ int warp_a[W], warp_b[W];
+    const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row = (int64_t)n * p.max_pages;
+    const int32_t *table = p.block_table + row;
+    const float *weight = p.weight + row;
+    const int len = p.seq_lens[n];
+    const int64_t held = len > 0 ? ((int64_t)len + kPage - 1) / kPage : 0;
+    const bool bad = held > p.max_pages;
+    if (bad && tid == 0 && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
+    const int P = bad ? 0 : (int)held;
+    const int E = P > p.budget ? P - p.budget : 0;
+    const int lo = p.sink, hi = P - p.recent;  // the pages that may go (E > 0: lo < hi)
+
+    uint32_t prefix = 0, equal_go = 0;
+    if (E > 0) {
+        uint32_t left = E;
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            for (int i = tid; i < 256; i += kEvictThreads) hist[i] = 0;
+            __syncthreads();
+            const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
+            for (int i = lo + tid; i < hi; i += kEvictThreads) {
+                const uint32_t key = weight_key(weight[i]);
+                if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+            }
+            __syncthreads();
+            if (warp == 0) {  // the bin in which the running count reaches `left`
+                uint32_t c[8], sum = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum += c[j] = hist[lane * 8 + j];
+                uint32_t incl = sum;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t t = __shfl_up_sync(~0u, incl, o);
+                    if (lane >= o) incl += t;
+                }
+                uint32_t before = incl - sum;
+                if (before < left && incl >= left) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (before < left && before + c[j] >= left) {
+                            s_prefix = prefix | ((uint32_t)(lane * 8 + j) << shift);
+                            s_left = left - before;
+                        }
+                        before += c[j];
+                    }
+                }
+            }
+            __syncthreads();
+            prefix = s_prefix;
+            left = s_left;
+        }
+        equal_go = left;  // pages of weight `prefix` that go: the last ones of them
+    }
+    // how many pages weigh exactly `prefix`
+    int equal = 0;
+    if (E > 0) {
+        for (int i = lo + tid; i < hi; i += kEvictThreads) equal += weight_key(weight[i]) == prefix;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) equal += __shfl_xor_sync(~0u, equal, o);
+        if (lane == 0) warp_a[warp] = equal;
+        __syncthreads();
+        equal = 0;
+        for (int w = 0; w < W; ++w) equal += warp_a[w];
+        __syncthreads();
+    }
+    const int equal_stay = equal - (int)equal_go;
+
+    int gone = 0, seen_equal = 0;  // before this chunk
+    for (int base = 0; base < p.max_pages; base += kEvictThreads) {
+        const int i = base + tid;
+        const bool in = i < p.max_pages;
+        const int32_t id = in ? table[i] : -1;
+        const float wt = in ? weight[i] : 0.f;
+        const bool open = E > 0 && in && i >= lo && i < hi;
+        const uint32_t key = weight_key(wt);
+        const bool eq = open && key == prefix;
+        // rank among the pages of weight `prefix`
+        const unsigned me = __ballot_sync(~0u, eq);
+        if (lane == 0) warp_a[warp] = __popc(me);
+        __syncthreads();
+        int before = seen_equal, all = 0;
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) before += warp_a[w];
+            all += warp_a[w];
+        }
+        before += __popc(me & ((1u << lane) - 1u));
+        seen_equal += all;
+        const bool go = open && (key < prefix || (eq && before >= equal_stay));
+        const unsigned mg = __ballot_sync(~0u, go);
+        if (lane == 0) warp_b[warp] = __popc(mg);
+        __syncthreads();  // also: every entry of the chunk is read
+        int at = gone, total = 0;
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) at += warp_b[w];
+            total += warp_b[w];
+        }
+        at += __popc(mg & ((1u << lane) - 1u));
+        if (in) {
+            if (go) {
+                p.freed[row + at] = id;
+            } else {
+                p.block_table_out[row + i - at] = id;
+                p.weight_out[row + i - at] = wt;
+            }
+        }
+        gone += total;
+    }
+    __syncthreads();
+    for (int i = tid; i < p.max_pages; i += kEvictThreads) {
+        if (i >= p.max_pages - E) {
+            p.block_table_out[row + i] = -1;
+            p.weight_out[row + i] = 0.f;
+        }
+        if (i >= E) p.freed[row + i] = -1;
+    }
+    if (tid == 0) {
+        p.seq_lens_out[n] = len - E * kPage;
+        p.freed_count[n] = E;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const CacheAppendParams &p, int d, int dtype, cudaStream_t st) {
+    return dtype == KDA_DT_BF16 ? launch_append<__nv_bfloat16>(p, d, st) : launch_append<float>(p, d, st);
+}
+
+cudaError_t launch_cache_evict(const CacheEvictParams &p, cudaStream_t st) {
+    evict_kernel<<<(unsigned)p.batch, kEvictThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace kda
