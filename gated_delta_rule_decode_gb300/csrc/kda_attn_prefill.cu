@@ -244,6 +244,7 @@ cudaError_t launch_dim(const AttnPrefillParams &p, int d, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attn_prefill(const AttnPrefillParams &p, int d, int dtype, cudaStream_t st) {
+    if (attn_prefill_tc_supported(d, dtype)) return launch_attn_prefill_tc(p, d, st);
     return dtype == KDA_DT_BF16 ? launch_dim<__nv_bfloat16>(p, d, st) : launch_dim<float>(p, d, st);
 }
 

@@ -1,0 +1,502 @@
+// Causal attention over packed prompts on tcgen05 (bf16, d = 64 or 128).
+//
+//   S = Q K^T,  P = e^{scale (S - m)},  O = P V,  m and l = sum P per row
+//
+// A CTA takes two tiles of 128 query rows of one kv head and walks the
+// sequence's keys in blocks of 128.  A tile's rows are tokens x the G query
+// heads of the kv head, so a block of keys and values is loaded once for all
+// of them.  Roles:
+//
+//   warps 0-3, 4-7  softmax of tile 0 and 1: a thread owns a row, reads its
+//                   128 scores from tensor memory, and writes the weights back
+//                   over them as bf16, the operand of the second product
+//   warp 8          issues the products
+//   warp 9          TMA loads: Q once, then rings of key and value blocks
+//   warps 10, 11    look over the value blocks that some row of the tiles
+//                   must not see (below)
+//
+// While one tile's softmax runs, the tensor cores work on the other tile:
+// PV(t, j), then QK(t, j + 1), for t = 0, 1 in turn.  Tensor memory holds S
+// (P over it) and O of both tiles: 4 x 128 columns.
+//
+// The running maximum is only moved when it would grow by more than 8 (in
+// powers of two); until then weights may reach 2^8, which costs bf16 nothing,
+// and O is not rescaled.  When it moves, the row's warp waits for the last PV
+// and rescales O in tensor memory.
+//
+// P in bf16 is rounded to 8 bits, which averages out over many keys but not
+// over few.  Where a weight of the block may exceed 1/16 of its row's sum so
+// far, the tile's P takes a second bf16 term (in the other half of the score
+// columns) and a second product: rows that one or a few keys dominate keep 16
+// bits.  Sums of P are taken in fp32 before rounding.
+//
+// Masked values: a weight of zero times a NaN or an infinity would poison a
+// row that must not see it.  Scores are masked by selection, so keys need no
+// care.  In value blocks that reach past the tiles' first token, rows past the
+// sequence's end are zeroed in shared memory, and a non-finite value is zeroed
+// and remembered; if there was one, the epilogue adds those values to exactly
+// the rows that see them.
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "kda_attn_internal.h"
+#include "kda_bulk.cuh"
+#include "kda_internal.h"
+#include "kda_tc.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kRows = 128, kKeys = 128;
+constexpr int kThreads = 384;
+constexpr uint32_t kTmem = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.f;  // log2 growth of the maximum that is let stand
+constexpr float kShare = 16.f;  // weights above 1 / kShare of the row's sum take two terms
+
+template <int HD>
+struct Cfg {
+    static constexpr int kTile = 128 * HD * 2;           // bytes of a Q tile, a key block, a value block
+    static constexpr int kChunk = 128 * 128;             // 64 columns of it
+    static constexpr int NK = HD == 128 ? 2 : 4, NV = HD == 128 ? 3 : 4;
+    static constexpr int kBytes = 1024 + (2 + NK + NV) * kTile + 256;
+    static constexpr int kO = 256;                       // tensor memory column of O (tile 0); S at 0 and 128
+};
+
+struct Bars {
+    uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], k_full[4], k_empty[4], v_full[4], v_ready[4], v_empty[4], drain;
+};
+
+// Instruction descriptor of kind::f16 with bf16 operands and fp32 accumulation;
+// b_mn: B is stored with its N extent contiguous.
+constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+// Descriptor of 16 rows (keys) of a value block: N (channels) contiguous, 128-byte
+// swizzle; 64-channel chunks kChunk bytes apart, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_v(uint32_t saddr, uint32_t chunk_bytes) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(chunk_bytes >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const void *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(*reinterpret_cast<uint64_t *>(&d))
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)),
+          "l"(*reinterpret_cast<uint64_t *>(&c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<uint64_t *>(&d))
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// A bounded wait that also gives up when another role has.
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t phase, volatile int *abort_flag) {
+    for (uint32_t it = 0; it < kWaitLimit; ++it) {
+        if (mbar_try_wait(bar, phase & 1u)) return true;
+        if ((it & 255u) == 255u && *abort_flag) return false;
+    }
+    *abort_flag = 1;
+    return false;
+}
+
+// Whether `x` holds in any thread of a tile's four warps (named barrier `id`).
+__device__ __forceinline__ bool tile_any(int id, bool x) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"((int)x)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {
+    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap qmap,
+                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using C = Cfg<HD>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char *sq = smem, *sk = sq + 2 * C::kTile, *sv = sk + C::NK * C::kTile;
+    __shared__ Bars bars;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag, v_bad;
+    __shared__ volatile int two_terms[2];  // of the tile's P that is ready
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    const int kvh = (int)(blockIdx.x % (unsigned)p.Hkv);
+    const int64_t unit = (int64_t)((gridDim.x - 1 - blockIdx.x) / (unsigned)p.Hkv);
+    const int TT = kRows / p.G;  // tokens of a tile
+    int64_t pair;
+    const int s = seq_of_unit(p.cu_seqlens, p.num_seqs, 2 * TT, 1, unit, pair);
+    int t0, t1;
+    if (!seq_range(p.cu_seqlens, s, p.total_tokens, p.err_flag, t0, t1)) return;
+    const int len = t1 - t0;
+    if (pair < 0 || pair * 2 * TT >= len) return;
+    const int a0 = (int)pair * 2 * TT;  // first token of tile 0, within the sequence
+    int nblk[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int a = a0 + t * TT, b = min(a + TT, len);
+        nblk[t] = b > a ? (b + kKeys - 1) / kKeys : 0;
+    }
+    const int n = max(nblk[0], nblk[1]);
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.q_full[i], 1);
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.p_full[i], 4);
+            mbar_init(&bars.pv_done[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bars.k_full[i], 1);
+            mbar_init(&bars.k_empty[i], 1);
+            mbar_init(&bars.v_full[i], 1);
+            mbar_init(&bars.v_ready[i], 2);
+            mbar_init(&bars.v_empty[i], 1);
+        }
+        mbar_init(&bars.drain, 1);
+        fence_barrier_init();
+        abort_flag = 0;
+        v_bad = 0;
+    }
+    if (warp == 8) tc::tmem_alloc(&tmem_base, kTmem);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = tmem_base;
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 9) {
+            // ---------------- loads
+            if (lane == 0) {
+                const int box = TT * p.G * 128;  // bytes of a Q box
+                auto load_q = [&](int t) {
+                    mbar_arrive_expect_tx(&bars.q_full[t], box * (HD / 64));
+                    for (int c = 0; c < HD / 64; ++c)
+                        tma_load_3d(sq + t * C::kTile + c * C::kChunk, &qmap, 64 * c, kvh * p.G, t0 + a0 + t * TT, &bars.q_full[t]);
+                };
+                auto load_kv = [&](unsigned char *dst, const CUtensorMap *map, int j, uint64_t *bar) {
+                    mbar_arrive_expect_tx(bar, C::kTile);
+                    for (int c = 0; c < HD / 64; ++c)
+                        tma_load_3d(dst + c * C::kChunk, map, 64 * c, kvh, t0 + j * kKeys, bar);
+                };
+                int jk = 0, jv = 0;
+                load_q(0);
+                for (int j = 0; j < n; ++j) {
+                    if (j >= C::NK && !wait_or_abort(&bars.k_empty[j % C::NK], (j / C::NK - 1), &abort_flag)) break;
+                    load_kv(sk + (j % C::NK) * C::kTile, &kmap, j, &bars.k_full[j % C::NK]);
+                    jk = j + 1;
+                    if (j == 0 && nblk[1] > 0) load_q(1);
+                    if (j >= C::NV && !wait_or_abort(&bars.v_empty[j % C::NV], (j / C::NV - 1), &abort_flag)) break;
+                    load_kv(sv + (j % C::NV) * C::kTile, &vmap, j, &bars.v_full[j % C::NV]);
+                    jv = j + 1;
+                }
+                // every load lands before the CTA's memory goes
+                mbar_wait_drain(&bars.q_full[0], 0);
+                if (nblk[1] > 0) mbar_wait_drain(&bars.q_full[1], 0);
+                for (int j = max(0, jk - C::NK); j < jk; ++j) mbar_wait_drain(&bars.k_full[j % C::NK], (j / C::NK) & 1u);
+                for (int j = max(0, jv - C::NV); j < jv; ++j) mbar_wait_drain(&bars.v_full[j % C::NV], (j / C::NV) & 1u);
+            }
+        } else if (warp == 8) {
+            // ---------------- products
+            if (lane == 0) {
+                const uint32_t id_qk = idesc_bf16(128, 128, false), id_pv = idesc_bf16(128, HD, true);
+                auto qk = [&](int t, int j) {
+                    const uint32_t qa = tc::smem_u32(sq + t * C::kTile), ka = tc::smem_u32(sk + (j % C::NK) * C::kTile);
+#pragma unroll
+                    for (int ks = 0; ks < HD / 16; ++ks)
+                        tc::mma_f16_ss(tm + 128 * t, tc::desc_tf32_kstep(qa, 128, ks), tc::desc_tf32_kstep(ka, 128, ks),
+                                       id_qk, ks > 0);
+                    tc::commit(&bars.s_full[t]);
+                };
+                auto pv = [&](int t, int j) {
+                    const uint32_t va = tc::smem_u32(sv + (j % C::NV) * C::kTile);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        tc::mma_f16_ts(tm + C::kO + HD * t, tm + 128 * t + 8 * ks, desc_v(va + ks * 2048, C::kChunk), id_pv,
+                                       (j > 0 || ks > 0) ? 1u : 0u);
+                    if (two_terms[t]) {
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            tc::mma_f16_ts(tm + C::kO + HD * t, tm + 128 * t + 64 + 8 * ks, desc_v(va + ks * 2048, C::kChunk),
+                                           id_pv, 1u);
+                    }
+                    tc::commit(&bars.pv_done[t]);
+                };
+                bool ok = wait_or_abort(&bars.k_full[0], 0, &abort_flag);
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (nblk[t] == 0) continue;
+                    ok = wait_or_abort(&bars.q_full[t], 0, &abort_flag);
+                    if (ok) qk(t, 0);
+                }
+                if (ok) tc::commit(&bars.k_empty[0]);
+                for (int j = 0; j < n && ok; ++j) {
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (j < nblk[t]) {
+                            ok = wait_or_abort(&bars.p_full[t], j, &abort_flag) &&
+                                 wait_or_abort(&bars.v_ready[j % C::NV], j / C::NV, &abort_flag);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            pv(t, j);
+                        }
+                        if (j + 1 < nblk[t]) {
+                            ok = wait_or_abort(&bars.k_full[(j + 1) % C::NK], (j + 1) / C::NK, &abort_flag);
+                            if (!ok) break;
+                            qk(t, j + 1);
+                        }
+                    }
+                    if (!ok) break;
+                    tc::commit(&bars.v_empty[j % C::NV]);
+                    if (j + 1 < n) tc::commit(&bars.k_empty[(j + 1) % C::NK]);
+                }
+                tc::commit(&bars.drain);  // every product is done before the memory goes
+                mbar_wait_drain(&bars.drain, 0);
+            }
+        } else {
+            // ---------------- values that some row must not see
+            const int ft = tid - 320;  // 0..63
+            for (int j = 0; j < n; ++j) {
+                if (!__all_sync(~0u, wait_or_abort(&bars.v_full[j % C::NV], j / C::NV, &abort_flag))) break;
+                if (j * kKeys + kKeys - 1 > a0) {
+                    unsigned char *blk = sv + (j % C::NV) * C::kTile;
+                    bool bad = false;
+                    for (int i = ft; i < C::kTile / 16; i += 64) {
+                        const int key = j * kKeys + ((i >> 3) & 127);
+                        uint4 *u = reinterpret_cast<uint4 *>(blk) + i;
+                        if (key >= len) {
+                            *u = make_uint4(0, 0, 0, 0);
+                        } else if (key > a0) {
+                            uint4 x = *u;
+                            if (nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w)) {
+                                bad = true;
+                                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+                                    if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0x0000ffffu;
+                                }
+                                *u = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                    }
+                    if (bad) v_bad = 1;
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.v_ready[j % C::NV]);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // ---------------- softmax: thread = row
+        const int t = warp >> 2, row = tid & 127;
+        const int tok = a0 + t * TT + row / p.G, gi = row % p.G;  // token within the sequence
+        const bool valid = row < TT * p.G && tok < len;
+        const uint32_t s_addr = tc::lane_addr(tm, warp, 128 * t);
+        const uint32_t o_addr = tc::lane_addr(tm, warp, C::kO + HD * t);
+        const float sl2 = p.scale * kLog2e;
+        const int nb = nblk[t];
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < nb; ++j) {
+            // (after a wait gave up the loop runs on, on garbage: the tile's warps meet at a barrier below)
+            if (!__all_sync(~0u, wait_or_abort(&bars.s_full[t], j, &abort_flag))) ok = false;
+            tc::fence_after_sync();
+            float sc[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc::ld32(s_addr + 32 * i, sc[i]);
+            tc::wait_ld();
+            const int vis = tok - j * kKeys + 1;  // keys of this block that the row sees
+            if (__any_sync(~0u, vis < kKeys)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (32 * i + c >= vis) sc[i][c] = -INFINITY;
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], sc[i][c]);
+            const float mnew = fmaxf(fmaxf(m, fmaxf(mx[0], mx[1])), fmaxf(mx[2], mx[3]));
+            if (j == 0) {
+                m = mnew;
+            } else {
+                const bool grow = (mnew - m) * sl2 > kLazy;
+                if (__any_sync(~0u, grow)) {
+                    const float f = grow ? ex2((m - mnew) * sl2) : 1.f;
+                    if (grow) m = mnew;
+                    l *= f;
+                    if (!__all_sync(~0u, wait_or_abort(&bars.pv_done[t], j - 1, &abort_flag))) ok = false;
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < HD; c += 16) {
+                        float o[16];
+                        tc::ld16(o_addr + c, o);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= f;
+                        tc::st16(o_addr + c, o);
+                    }
+                    tc::wait_st();
+                }
+            }
+            const float use = m == -INFINITY ? 0.f : m;
+            // a weight above 1 / kShare of the sum (of which it is a part)?  The four
+            // warps of the tile decide together.
+            const float top = ex2((fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) - use) * sl2);
+            const bool two = tile_any(1 + t, valid && top * (kShare - 1.f) > l);
+            const float2 k2 = make_float2(sl2, sl2), b2 = make_float2(-use * sl2, -use * sl2);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    float2 x = fma2(make_float2(sc[i][2 * c], sc[i][2 * c + 1]), k2, b2);
+                    x.x = ex2(x.x);
+                    x.y = ex2(x.y);
+                    sum[c & 1] = add2(sum[c & 1], x);
+                    pk[c] = pack_bf16(x.x, x.y);
+                    sc[i][2 * c] = x.x;
+                    sc[i][2 * c + 1] = x.y;
+                }
+                tc::st16u(s_addr + 16 * i, pk);
+                if (two) {  // what the rounding left
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        pk[c] = pack_bf16(sc[i][2 * c] - __uint_as_float(pk[c] << 16),
+                                          sc[i][2 * c + 1] - __uint_as_float(pk[c] & 0xffff0000u));
+                    tc::st16u(s_addr + 64 + 16 * i, pk);
+                }
+            }
+            tc::wait_st();
+            tc::fence_before_sync();
+            if (row == 0) two_terms[t] = two;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.p_full[t]);
+            sum[0] = add2(sum[0], sum[1]);
+            l += sum[0].x + sum[0].y;
+        }
+        // ---------------- epilogue
+        if (nb > 0 && ok) ok = __all_sync(~0u, wait_or_abort(&bars.pv_done[t], nb - 1, &abort_flag));
+        if (nb > 0 && ok) {
+            tc::fence_after_sync();
+            const float inv = 1.f / l;
+            const int64_t orow = ((int64_t)(t0 + tok) * p.Hq + kvh * p.G + gi);
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + orow * HD;
+            const bool bad = *reinterpret_cast<volatile int *>(&v_bad) != 0;
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 32) {
+                float o[32];
+                tc::ld32(o_addr + c, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= inv;
+                if (!valid) continue;
+                if (bad) {  // the values that were set aside, for the rows that see them
+                    for (int key = a0 + 1; key <= tok; ++key) {
+                        const uint4 *src = reinterpret_cast<const uint4 *>(
+                            static_cast<const __nv_bfloat16 *>(p.v) + (int64_t)(t0 + key) * p.v_stride + (int64_t)kvh * HD + c);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const uint4 x = src[u];
+                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if ((w[e] & 0x7f80u) == 0x7f80u) o[8 * u + 2 * e] += __uint_as_float(w[e] << 16);
+                                if ((w[e] & 0x7f800000u) == 0x7f800000u)
+                                    o[8 * u + 2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                    *reinterpret_cast<uint4 *>(dst + c + e) =
+                        make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]), pack_bf16(o[e + 4], o[e + 5]),
+                                   pack_bf16(o[e + 6], o[e + 7]));
+            }
+            if (valid && p.lse) p.lse[orow] = (m * sl2 + log2f(l)) * kLn2;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 8) tc::tmem_dealloc(tm, kTmem);
+    if (tid == 0 && abort_flag && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_TIMEOUT);
+}
+
+bool make_map(CUtensorMap *map, const void *base, int d, int heads, int64_t tokens, int64_t stride, int box_heads,
+              int box_tokens) {
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+    const cuuint32_t elem[3] = {1, 1, 1};
+    return tensor_map_encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+                                  elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int HD>
+cudaError_t launch_tc(const AttnPrefillParams &p, cudaStream_t st) {
+    const int TT = kRows / p.G;
+    CUtensorMap qmap, kmap, vmap;
+    if (!make_map(&qmap, p.q, HD, p.Hq, p.total_tokens, p.q_stride, p.G, TT) ||
+        !make_map(&kmap, p.k, HD, p.Hkv, p.total_tokens, p.k_stride, 1, kKeys) ||
+        !make_map(&vmap, p.v, HD, p.Hkv, p.total_tokens, p.v_stride, 1, kKeys))
+        return cudaErrorInvalidValue;
+    auto kern = prefill_tc_kernel<HD>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::kBytes);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = (p.total_tokens / (2 * TT) + p.num_seqs) * p.Hkv;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    kern<<<(unsigned)blocks, kThreads, Cfg<HD>::kBytes, st>>>(p, qmap, kmap, vmap);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn_prefill_tc_supported(int d, int dtype) {
+    return dtype == KDA_DT_BF16 && (d == 64 || d == 128) && tensor_map_encode_fn() != nullptr;
+}
+
+cudaError_t launch_attn_prefill_tc(const AttnPrefillParams &p, int d, cudaStream_t st) {
+    return d == 128 ? launch_tc<128>(p, st) : launch_tc<64>(p, st);
+}
+
+}  // namespace kda
