@@ -15,8 +15,7 @@ from typing import NamedTuple
 
 import torch
 
-from .kda import (KdaError, _check, _dtype_code, _need, _ptr, _scratch, _stream_handle,  # noqa: F401
-                  lib)
+from .kda import KdaError, _check, _dtype_code, _need, lib  # noqa: F401
 
 PAGE_TOKENS = 64
 KDA_DEVERR_PAGE = 256
@@ -72,47 +71,74 @@ def _declare(lib):
 _lib = _declare(lib())
 
 
+_F32, _I32T, _F8 = torch.float32, torch.int32, torch.float8_e4m3fn
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def make_dims(q_heads: int, kv_heads: int, head_dim: int, dtype_code: int, scale: float | None = None) -> KdaAttnDims:
     return KdaAttnDims(int(q_heads), int(kv_heads), int(head_dim), int(dtype_code),
                        float(scale) if scale is not None else 0.0)
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype) -> int:
+# A small call's time is the host's, so the checks below take their quick way
+# first and look for what to say only when it fails.
+
+def _ok(t: torch.Tensor, name: str, shape: tuple, dtype):
+    """Checks a contiguous CUDA tensor."""
+    if not (t.is_cuda and t.shape == shape and t.dtype is dtype and t.is_contiguous()):
+        _need(t, name, shape, dtype)
+
+
+def _rows(t: torch.Tensor, name: str, shape: tuple, dtype) -> int:
     """Checks a tensor of token rows that may lie apart (a slice of a fused
     projection) and returns the distance between tokens in elements."""
+    H, d = shape[-2], shape[-1]
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    H, d = shape[-2], shape[-1]
-    st = t.stride()
-    apart = st[-3]
-    if shape[-3] == 1 and len(shape) == 3 or t.numel() == 0:
-        apart = max(apart, H * d)  # the distance is never used
-    ok = st[-1] == 1 and (H == 1 or st[-2] == d) and apart >= H * d
-    if len(shape) == 4 and shape[0] > 1 and t.numel():
-        if shape[1] == 1:
-            apart = st[0]
-        ok = ok and apart >= H * d and st[0] == shape[1] * apart
-    if not ok:
-        raise ValueError(f"{name} must have contiguous [heads, d] rows at one distance")
+    if t.is_contiguous():
+        apart = H * d
+    else:
+        st = t.stride()
+        apart = st[-3]
+        if shape[-3] == 1:
+            # the only token, or the only token of each sequence
+            apart = st[0] if len(shape) == 4 and shape[0] > 1 else H * d
+        ok = st[-1] == 1 and (H == 1 or st[-2] == d) and apart >= H * d
+        if len(shape) == 4 and shape[0] > 1:
+            ok = ok and st[0] == shape[1] * apart
+        if not ok:
+            raise ValueError(f"{name} must have contiguous [heads, d] rows at one distance")
     if (apart * t.element_size()) % 16 or t.data_ptr() % 16:
         raise ValueError(f"{name}'s rows must start on 16-byte boundaries")
     return apart
 
 
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_handle(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
+
+
 def _check_cache(c: KVCache):
-    N, Hkv, page, d = c.k_pages.shape
+    k, v, ks, vs = c
+    N, Hkv, page, d = k.shape
     if page != PAGE_TOKENS:
         raise ValueError(f"k_pages has {page} positions per page, expected {PAGE_TOKENS}")
-    f8 = torch.float8_e4m3fn
-    _need(c.k_pages, "k_pages", (N, Hkv, PAGE_TOKENS, d), f8)
-    _need(c.v_pages, "v_pages", (N, Hkv, d, PAGE_TOKENS), f8)
-    _need(c.k_scale, "k_scale", (N, Hkv), torch.float32)
-    _need(c.v_scale, "v_scale", (N, Hkv), torch.float32)
-    return Hkv, d, KdaKvCache(c.k_pages.data_ptr(), c.v_pages.data_ptr(), c.k_scale.data_ptr(), c.v_scale.data_ptr(), N)
+    _ok(k, "k_pages", (N, Hkv, PAGE_TOKENS, d), _F8)
+    _ok(v, "v_pages", (N, Hkv, d, PAGE_TOKENS), _F8)
+    _ok(ks, "k_scale", (N, Hkv), _F32)
+    _ok(vs, "v_scale", (N, Hkv), _F32)
+    return Hkv, d, KdaKvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), N)
 
 
 def alloc_cache(num_pages: int, kv_heads: int, head_dim: int, device="cuda") -> KVCache:
@@ -136,16 +162,16 @@ def prefill(q, k, v, cu_seqlens, out=None, *, lse=None, return_lse=False, scale=
     code = _dtype_code(q)
     qs, ks, vs = (_rows(q, "q", (T, Hq, d), dt), _rows(k, "k", (T, Hkv, d), dt), _rows(v, "v", (T, Hkv, d), dt))
     n = cu_seqlens.shape[0] - 1
-    _need(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32)
+    _ok(cu_seqlens, "cu_seqlens", (n + 1,), _I32T)
     if out is None:
         out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
     else:
-        _need(out, "out", (T, Hq, d), dt)
+        _ok(out, "out", (T, Hq, d), dt)
     if lse is None:
         if return_lse:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+            lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
     else:
-        _need(lse, "lse", (T, Hq), torch.float32)
+        _ok(lse, "lse", (T, Hq), _F32)
     dims = make_dims(Hq, Hkv, d, code, scale)
     _check(_lib.kda_attn_prefill(ctypes.byref(dims), n, _ptr(cu_seqlens), T, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
                                  _ptr(out), _ptr(lse), _ptr(err_flag), _stream_handle(stream)), "kda_attn_prefill")
@@ -164,9 +190,9 @@ def append(cache: KVCache, k, v, cu_seqlens, start_pos, block_table, *, err_flag
     code = _dtype_code(k)
     ks, vs = _rows(k, "k", (T, Hkv, d), dt), _rows(v, "v", (T, Hkv, d), dt)
     n, width = block_table.shape
-    _need(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32)
-    _need(start_pos, "start_pos", (n,), torch.int32)
-    _need(block_table, "block_table", (n, width), torch.int32)
+    _ok(cu_seqlens, "cu_seqlens", (n + 1,), _I32T)
+    _ok(start_pos, "start_pos", (n,), _I32T)
+    _ok(block_table, "block_table", (n, width), _I32T)
     dims = make_dims(Hkv, Hkv, d, code)
     _check(_lib.kda_cache_append(ctypes.byref(dims), ctypes.byref(c), n, _ptr(cu_seqlens), T, _ptr(k), ks, _ptr(v), vs,
                                  _ptr(start_pos), _ptr(block_table), width, _ptr(err_flag), _stream_handle(stream)),
@@ -196,28 +222,30 @@ def decode(q, cache: KVCache, seq_lens, block_table, out=None, *, lse=None, retu
     code = _dtype_code(q)
     qs = _rows(q, "q", (B, D, Hq, d), dt)
     width = block_table.shape[1]
-    _need(seq_lens, "seq_lens", (B,), torch.int32)
-    _need(block_table, "block_table", (B, width), torch.int32)
+    _ok(seq_lens, "seq_lens", (B,), _I32T)
+    _ok(block_table, "block_table", (B, width), _I32T)
     if out is None:
         out = torch.empty((B, D, Hq, d), dtype=dt, device=q.device)
     else:
-        _need(out, "out", (B, D, Hq, d), dt)
+        _ok(out, "out", (B, D, Hq, d), dt)
     if lse is None:
         if return_lse:
-            lse = torch.empty((B, D, Hq), dtype=torch.float32, device=q.device)
+            lse = torch.empty((B, D, Hq), dtype=_F32, device=q.device)
     else:
-        _need(lse, "lse", (B, D, Hq), torch.float32)
+        _ok(lse, "lse", (B, D, Hq), _F32)
     if weight_in is not None:
-        _need(weight_in, "weight_in", (B, width), torch.float32)
+        _ok(weight_in, "weight_in", (B, width), _F32)
     if weight_out is not None:
-        _need(weight_out, "weight_out", (B, width), torch.float32)
+        _ok(weight_out, "weight_out", (B, width), _F32)
     elif return_weight or weight_in is not None:
-        weight_out = torch.empty((B, width), dtype=torch.float32, device=q.device)
+        weight_out = torch.empty((B, width), dtype=_F32, device=q.device)
     dims = make_dims(Hq, Hkv, d, code, scale)
     pd = ctypes.byref(dims)
     if workspace is None:
         need = _lib.kda_attn_decode_workspace_bytes(pd, B, D, width, 0 if weight_out is None else 1)
-        workspace = _scratch(need, q.device, stream)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            workspace.record_stream(stream)
     else:
         need = workspace.numel() * workspace.element_size()
     _check(_lib.kda_attn_decode(pd, ctypes.byref(c), B, D, _ptr(q), qs, _ptr(seq_lens), _ptr(block_table), width,
@@ -236,9 +264,9 @@ def evict(seq_lens, block_table, weight, budget: int, sink: int = 1, recent: int
     [B, max_pages] fp32.  With ``in_place`` these three are updated.
     """
     B, width = block_table.shape
-    _need(seq_lens, "seq_lens", (B,), torch.int32)
-    _need(block_table, "block_table", (B, width), torch.int32)
-    _need(weight, "weight", (B, width), torch.float32)
+    _ok(seq_lens, "seq_lens", (B,), _I32T)
+    _ok(block_table, "block_table", (B, width), _I32T)
+    _ok(weight, "weight", (B, width), _F32)
     if in_place:
         lens, table, w = seq_lens, block_table, weight
     else:

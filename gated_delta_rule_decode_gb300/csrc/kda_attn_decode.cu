@@ -698,7 +698,8 @@ template <typename T, int HD, int MT>
 cudaError_t launch(const AttnDecodeParams &p, cudaStream_t st) {
     using S = Smem<T, HD, MT>;
     auto kern = decode_attn_kernel<T, HD, MT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), S::kBytes, done);
     if (e != cudaSuccess) return e;
     const int rows = p.D * p.G, RB = (rows + 16 * MT - 1) / (16 * MT);
     // no more workers than pages

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kda_attn.h"
 
 namespace kda {
@@ -84,6 +86,19 @@ __device__ __forceinline__ bool seq_range(const int32_t *cu, int s, int64_t tota
     if (lo >= 0 && lo <= hi && (int64_t)hi <= total) return true;
     if (err) atomicOr(err, KDA_DEVERR_SEQLENS);
     return false;
+}
+
+// Raises a kernel's dynamic shared memory limit on the current device, once per
+// device (`done`: a static of the caller, one per kernel).
+inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    const cudaError_t g = cudaGetDevice(&dev);
+    if (g != cudaSuccess) return g;
+    const uint64_t bit = (uint64_t)1 << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 cudaError_t launch_attn_prefill(const AttnPrefillParams &p, int d, int dtype, cudaStream_t s);

@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(const AttnPrefil
 template <typename T, int HD>
 cudaError_t launch_simt(const AttnPrefillParams &p, cudaStream_t st) {
     auto kern = prefill_simt_kernel<T, HD>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tiles<HD>::kBytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), Tiles<HD>::kBytes, done);
     if (e != cudaSuccess) return e;
     const int64_t blocks = (p.total_tokens / BM + p.num_seqs) * p.Hq;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;

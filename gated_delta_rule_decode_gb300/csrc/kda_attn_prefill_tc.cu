@@ -481,7 +481,8 @@ cudaError_t launch_tc(const AttnPrefillParams &p, cudaStream_t st) {
         !make_map(&vmap, p.v, HD, p.Hkv, p.total_tokens, p.v_stride, 1, kKeys))
         return cudaErrorInvalidValue;
     auto kern = prefill_tc_kernel<HD>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::kBytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), Cfg<HD>::kBytes, done);
     if (e != cudaSuccess) return e;
     const int64_t blocks = (p.total_tokens / (2 * TT) + p.num_seqs) * p.Hkv;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
