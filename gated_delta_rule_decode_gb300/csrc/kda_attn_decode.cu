@@ -5,18 +5,23 @@
 // The cache is read once, so the bound is HBM: 2 d bytes per position and kv
 // head.  Everything else is arranged around a steady stream of pages:
 //
-//  * Work is counted in pages: the items (sequence, kv head, block of 16 MT
+//  * Work is counted in pages: the items (sequence, kv head, block of 8 NB MT
 //    query rows) of the batch are laid end to end and cut into equal ranges,
 //    one per worker, so ragged batches and single long sequences balance
-//    alike.  A worker is MT warps; an item that a worker holds entirely is
-//    finished by it, one that is cut leaves partial results (o, m, l) that
-//    join_kernel adds up in worker order.
+//    alike.  A worker is a CTA of MT warps; an item that a worker holds
+//    entirely is finished by it, one that is cut leaves partial results
+//    (o, m, l) that join_kernel adds up in a fixed order.  There are a few
+//    times as many workers as fit the GPU at once: SMs do not get the same
+//    share of the memory bandwidth, and those that are served faster take
+//    more of them.
 //  * The G query heads of a kv head and the window's tokens are the rows of
 //    one tile, so a page is read once for all of them.
 //  * Each worker keeps a ring of shared-memory slots filled by bulk copies; a
 //    page's keys and values are one contiguous block each.
-//  * Products run as m16n8k16 fp16 MMAs with fp32 accumulation.  e4m3 values
-//    are exact in fp16.  A query row is scaled by a power of two into fp16's
+//  * Products run as m16n8k16 fp16 MMAs with fp32 accumulation, transposed:
+//    S^T = K Q^T and O^T = V^T P^T, so that the 16-row operand is the page and
+//    the 8-column one the query rows, of which there are few.  e4m3 values are
+//    exact in fp16.  A query row is scaled by a power of two into fp16's
 //    range, which is exact for bf16 inputs (elements below 2^-28 of the row's
 //    largest are rounded); fp32 inputs take a second fp16 term for the rest.
 //    The weights e^{s - m} are scaled by 2^15, so that fp16 holds them down
@@ -24,16 +29,18 @@
 //  * The contraction orders of both products are permuted so that a thread's
 //    operand bytes are contiguous 16-byte pieces: thread t of a quad holds
 //    channels 16 t.. of a key row and positions 16 t.. of a value channel,
-//    and the score tile j, column c stands for position 16 (c / 2) + 2 j +
-//    c % 2, which makes the score fragment the second product's operand as
-//    it is.  (The pages' value layout, a row of positions per channel, is
-//    there for this.)
+//    and row r of the score tile i stands for position 16 (r % 8 / 2) + 4 i +
+//    2 (r / 8) + r % 2; a transposed 8 x 8 move then makes score fragments the
+//    second product's operand.  (The pages' value layout, a row of positions
+//    per channel, is there for this.)
 //  * Each page's product is accumulated from zero and added to the output in
 //    fp32 round-to-nearest, because the tensor cores truncate when they add.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "kda_attn_internal.h"
 #include "kda_bulk.cuh"
@@ -42,34 +49,53 @@
 namespace kda {
 namespace {
 
-constexpr int kWarpsPerCta = 8;
-constexpr int kThreads = kWarpsPerCta * 32;
-constexpr int kMaxCtas = 152;  // one CTA per SM (the ring takes most of its shared memory)
+constexpr int kSms = 152;
+// Warps per SM, by registers and by shared memory (the rings).
+__host__ __device__ constexpr int warps_per_sm(int NB) { return NB == 1 ? 12 : 8; }
+constexpr int kRounds = 4;      // workers per place on the GPU, at most
+constexpr int kPagesPerWorker = 12;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPScale = 32768.f;  // fp16 scale of the weights
-constexpr int kRing = 3;            // page halves in flight per warp of a worker
 
-// Workspace, in floats: the cut items' partial results, two per worker (the
-// range's first item, the range's last item), then the rows' lse (base 2) and
-// page weights where weights are asked for.
+// Workspace, in floats: for each item the workers of its first and last page
+// (desc), the cut items' partial results, two per worker (the range's first
+// item, the range's last item), then the rows' lse (base 2) and page weights
+// where weights are asked for.
 struct Layout {
     int64_t desc, part_m, part_l, part_o, lse2, page_w, total;
 };
 
-__host__ __device__ inline int row_tile(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
-__host__ __device__ inline int64_t align64(int64_t x) { return (x + 63) / 64 * 64; }
+// A worker's rows: MT warps of NB tiles of 8.
+__host__ __device__ inline int tile_nb(int rows) { return rows <= 8 ? 1 : 2; }
+__host__ __device__ inline int tile_mt(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+__host__ __device__ inline int tile_rows(int rows) { return 8 * tile_nb(rows) * tile_mt(rows); }
+inline int64_t align64(int64_t x) { return (x + 63) / 64 * 64; }
 
-__host__ __device__ inline Layout make_layout(int64_t batch, int D, int Hq, int Hkv, int d, int64_t max_pages,
+// Rows of a partial result: those of an item that exist.
+__host__ __device__ inline int part_rows(int rows) { return rows < tile_rows(rows) ? rows : tile_rows(rows); }
+
+// Workers for at most `units` pages: all places on the GPU once, or as many
+// whole times as leave a worker kPagesPerWorker pages.
+inline int64_t worker_count(int64_t units, int NB, int MT) {
+    const int64_t places = (int64_t)kSms * warps_per_sm(NB) / MT;
+    int64_t rounds = units / (places * kPagesPerWorker);
+    rounds = rounds < 1 ? 1 : rounds > kRounds ? kRounds : rounds;
+    const int64_t w = places * rounds < units ? places * rounds : units;
+    return w < 1 ? 1 : w;
+}
+
+inline Layout make_layout(int64_t batch, int D, int Hq, int Hkv, int d, int64_t max_pages,
                                               bool with_weight) {
-    const int rows = D * (Hq / Hkv), MT = row_tile(rows);
-    const int64_t workers = (int64_t)kMaxCtas * kWarpsPerCta / MT;
+    const int rows = D * (Hq / Hkv), TR = tile_rows(rows), R = part_rows(rows);
+    const int64_t items = batch * Hkv * ((rows + TR - 1) / TR);
+    const int64_t workers = worker_count(items * max_pages, tile_nb(rows), tile_mt(rows));
     Layout l;
     l.desc = 0;
-    l.part_m = align64(4 * workers);
-    l.part_l = l.part_m + align64(2 * workers * 16 * MT);
-    l.part_o = l.part_l + align64(2 * workers * 16 * MT);
-    l.lse2 = l.part_o + 2 * workers * 16 * MT * d;
+    l.part_m = align64(2 * items);
+    l.part_l = l.part_m + align64(2 * workers * R);
+    l.part_o = l.part_l + align64(2 * workers * R);
+    l.lse2 = l.part_o + align64(2 * workers * R * d);
     l.page_w = l.lse2 + (with_weight ? align64(batch * D * Hq) : 0);
     l.total = l.page_w + (with_weight ? align64(batch * D * Hq * max_pages) : 0);
     return l;
@@ -83,8 +109,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -95,6 +120,13 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t
         "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(w));
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit values (two per thread).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
@@ -112,6 +144,10 @@ __device__ __forceinline__ float load1<float>(const float *p) { return *p; }
 template <>
 __device__ __forceinline__ float load1<__nv_bfloat16>(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
 __device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
 __device__ __forceinline__ void store2(__nv_bfloat16 *p, float a, float b) {
     *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(a, b);
@@ -173,56 +209,76 @@ __device__ __forceinline__ int chan(int t, int i) {
     else return (HD / 4) * t + i;
 }
 
-template <typename T, int HD, int MT>
+template <typename T, int HD>
+__device__ __forceinline__ void load_row(const T *row, int t, bool valid, float (&x)[HD / 4]) {
+#pragma unroll
+    for (int j = 0; j < HD / 4; ++j) x[j] = valid ? load1<T>(row + chan<HD>(t, j)) : 0.f;
+}
+
+// Clears the bytes of a value word (positions pos..pos + 3 of the page) from
+// `left` on, and the NaN bytes from `seen` on; the first of the latter, or kPage.
+__device__ __forceinline__ int mask_word(uint32_t &w, int pos, int left, int seen) {
+    int at = kPage;
+#pragma unroll
+    for (int b = 3; b >= 0; --b) {
+        const bool nan = ((w >> (8 * b)) & 0x7fu) == 0x7fu;
+        if (pos + b >= left) {
+            w &= ~(0xffu << (8 * b));
+        } else if (nan && pos + b >= seen) {
+            w &= ~(0xffu << (8 * b));
+            at = pos + b;
+        }
+    }
+    return at;
+}
+
+template <int HD, int NB, int MT>
 struct Smem {
+    static constexpr int kRows = 8 * NB * MT;
     static constexpr int kHalf = HD * kPage;  // bytes of a page's keys (or values)
-    static constexpr int kWorkers = kWarpsPerCta / MT;
-    static constexpr int kSlots = kRing * MT * (128 / HD);  // per worker
-    static constexpr int kRingBytes = kWorkers * kSlots * kHalf;
-    static constexpr int kBars = 2 * kWorkers * kSlots;
+    static constexpr int kSlots = (NB == 1 ? 2 : 3) * MT * (128 / HD);  // 16 or 24 KiB per warp
+    static constexpr int kRingBytes = kSlots * kHalf;
     static_assert(kSlots / 2 + 1 < kMeta / 2, "copies run at most a batch ahead of the page metadata in use");
-    static constexpr int kBytes = 128 + kRingBytes + kBars * 8 + kWorkers * (16 + kMeta * 12);
+    static constexpr int kBytes = 128 + kRingBytes + 2 * kSlots * 8 + kMeta * (int)sizeof(PageMeta);
 };
 
-template <typename T, int HD, int MT>
-__global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const AttnDecodeParams p) {
-    using S = Smem<T, HD, MT>;
+template <typename T, int HD, int NB, int MT>
+__global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_kernel(const AttnDecodeParams p, const Layout lay) {
+    using S = Smem<HD, NB, MT>;
     constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;
     constexpr int KS = HD / 16;    // contraction steps of the score product
-    constexpr int NT = HD / 8;     // column tiles of the output
-    constexpr int R = 16 * MT;     // rows of an item
+    constexpr int DT = HD / 16;    // channel tiles of the output
+    constexpr int R = 8 * NB * MT; // rows of an item
     constexpr int SL = S::kSlots;
+    constexpr int kThreads = 32 * MT;
     extern __shared__ unsigned char smem_raw[];
-    unsigned char *ring_all = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring_all + S::kRingBytes);
-    Cursor *starts = reinterpret_cast<Cursor *>(bars + S::kBars);
-    PageMeta *meta_all = reinterpret_cast<PageMeta *>(starts + S::kWorkers);
-    __shared__ int64_t warp_sum[kWarpsPerCta];
+    unsigned char *ring = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    uint64_t *full = reinterpret_cast<uint64_t *>(ring + S::kRingBytes), *empty = full + SL;
+    PageMeta *meta = reinterpret_cast<PageMeta *>(empty + SL);
+    __shared__ int64_t warp_sum[MT];
+    __shared__ Cursor start;
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, mt = tid >> 5;  // mt: row tile of the warp
     const int g = lane >> 2, t = lane & 3;
-    const int wk = warp / MT, mt = warp % MT;  // worker within the CTA, row tile of the warp
-    const int rows_all = p.D * p.G;
+    const int rows_all = p.D * p.G, PR = part_rows(rows_all);
     const int RB = (rows_all + R - 1) / R, HR = p.Hkv * RB;
-    const int64_t w = (int64_t)wk * gridDim.x + blockIdx.x;  // neighbours in work on different SMs
+    const int64_t w = blockIdx.x;
     float *ws = static_cast<float *>(p.workspace);
-    const Layout lay = make_layout(p.batch, p.D, p.Hq, p.Hkv, HD, p.max_pages, p.weight_out != nullptr);
 
-    for (int i = tid; i < S::kBars / 2; i += kThreads) {
-        mbar_init(bars + i, 1);                   // full: the copy's bytes
-        mbar_init(bars + S::kBars / 2 + i, MT);   // empty: the worker's warps
+    for (int i = tid; i < SL; i += kThreads) {
+        mbar_init(full + i, 1);    // the copy's bytes
+        mbar_init(empty + i, MT);  // the warps
     }
     fence_barrier_init();
 
-    // ---- the batch's units, and where each worker's range starts
+    // ---- the batch's units, and where this worker's range starts
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int nb = min(tid * per, p.batch), ne = min(nb + per, p.batch);
     int64_t mine = 0;
     for (int n = nb; n < ne; ++n) {
         int len;
-        const int pg = pages_of(p, n, len);
-        mine += (int64_t)pg * HR;
-        if (blockIdx.x == 0 && p.err_flag && p.seq_lens[n] > p.max_pages * kPage) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
+        mine += (int64_t)pages_of(p, n, len) * HR;
+        if (w == 0 && p.err_flag && p.seq_lens[n] > p.max_pages * kPage) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
     }
     int64_t incl = mine;
 #pragma unroll
@@ -230,23 +286,24 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const AttnDeco
         const int64_t x = __shfl_up_sync(~0u, incl, o);
         if (lane >= o) incl += x;
     }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int64_t U = 0, excl = incl - mine;
+    int64_t U = __shfl_sync(~0u, incl, 31), excl = incl - mine;
+    if constexpr (MT > 1) {
+        if (lane == 31) warp_sum[mt] = incl;
+        __syncthreads();
+        U = 0;
 #pragma unroll
-    for (int i = 0; i < kWarpsPerCta; ++i) {
-        if (i < warp) excl += warp_sum[i];
-        U += warp_sum[i];
+        for (int i = 0; i < MT; ++i) {
+            if (i < mt) excl += warp_sum[i];
+            U += warp_sum[i];
+        }
     }
     // no more workers than units, so that no range is empty
-    const int64_t W = min((int64_t)gridDim.x * S::kWorkers, max(U, (int64_t)1));
-    for (int i = 0; i < S::kWorkers; ++i) {
-        const int64_t u = U * ((int64_t)i * gridDim.x + blockIdx.x) / W;
-        if (mine > 0 && u >= excl && u < excl + mine) {
-            Cursor c{nb, excl};
-            locate(p, HR, c, u);
-            starts[i] = c;
-        }
+    const int64_t W = min((int64_t)gridDim.x, max(U, (int64_t)1));
+    const int64_t u0 = w < W ? U * w / W : 0, u1 = w < W ? U * (w + 1) / W : 0;
+    if (mine > 0 && u0 >= excl && u0 < excl + mine) {
+        Cursor c{nb, excl};
+        locate(p, HR, c, u0);
+        start = c;
     }
     // sequences without pages have no unit: their rows are written here
     for (int n = blockIdx.x; n < p.batch; n += gridDim.x) {
@@ -258,21 +315,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const AttnDeco
         }
     }
     __syncthreads();
-
-    const int64_t u0 = w < W ? U * w / W : 0, u1 = w < W ? U * (w + 1) / W : 0;
-    int *desc = reinterpret_cast<int *>(ws + lay.desc) + 4 * w;
-    if (mt == 0 && lane == 0) desc[0] = -1;
     if (u0 >= u1) return;
-
-    unsigned char *ring = ring_all + wk * SL * S::kHalf;
-    uint64_t *full = bars + wk * SL, *empty = bars + S::kBars / 2 + wk * SL;
     const int64_t count = u1 - u0;
 
     // ---- the copies: number c brings the keys (even) or values (odd) of unit
     // c / 2 into slot c % SL.  The worker's first warp looks up the pages of 32
     // units at a time, one per lane.
-    Cursor cur = starts[wk], fetch_cur = cur;
-    PageMeta *meta = meta_all + wk * kMeta;
+    Cursor cur = start, fetch_cur = cur;
     int64_t fetched = 0, issued = 0;
     auto fetch = [&]() {
         Cursor c = fetch_cur;
@@ -320,59 +369,62 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const AttnDeco
         const Unit un = locate(p, HR, cur, u0 + i);
         const int h = un.hr / RB, rb = un.hr % RB;
         const int pages_here = (int)min((int64_t)(un.pages - un.page), count - i);
-        // rows g and g + 8 of the warp's tile
-        int limit[2];
-        int64_t qrow[2], qtok[2];
-        int qhead[2];
-        bool valid[2];
+        const int row0 = rb * R + mt * 8 * NB;  // the warp's first row
+        // operand: row g of each tile; accumulators: rows 2 t and 2 t + 1
+        uint32_t qb[TERMS][NB][KS][2];
+        float qs[NB][2];
+        int limit[NB][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = rb * R + mt * 16 + g + 8 * e;
-            valid[e] = r < rows_all;
-            const int tok = valid[e] ? r / p.G : 0, gi = valid[e] ? r % p.G : 0;
-            limit[e] = valid[e] ? un.len - p.D + 1 + tok : 0;
-            qtok[e] = (int64_t)un.n * p.D + tok;
-            qhead[e] = h * p.G + gi;
-            qrow[e] = qtok[e] * p.Hq + qhead[e];
-        }
-        uint32_t qa[TERMS][KS][4];
-        float qs[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const T *src = static_cast<const T *>(p.q) + qtok[e] * p.q_stride + (int64_t)qhead[e] * HD;
+        for (int nb = 0; nb < NB; ++nb) {
+            const int r = row0 + 8 * nb + g;
+            const bool valid = r < rows_all;
+            const int tok = valid ? r / p.G : 0, gi = valid ? r - tok * p.G : 0;
+            const T *src = static_cast<const T *>(p.q) + ((int64_t)un.n * p.D + tok) * p.q_stride +
+                           (int64_t)(h * p.G + gi) * HD;
             float x[HD / 4], amax = 0.f;
+            load_row<T, HD>(src, t, valid, x);
 #pragma unroll
-            for (int j = 0; j < HD / 4; ++j) {
-                x[j] = valid[e] ? load1<T>(src + chan<HD>(t, j)) : 0.f;
-                amax = fmaxf(amax, fabsf(x[j]));
-            }
+            for (int j = 0; j < HD / 4; ++j) amax = fmaxf(amax, fabsf(x[j]));
             amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
             // the row times 2^(14 - ex): its largest element in 2^14..2^15
             int ex = (int)(__float_as_uint(amax) >> 23) - 127;
             ex = ex < -100 ? -100 : ex > 126 ? 126 : ex;
             const float mul = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-            qs[e] = __uint_as_float((uint32_t)(127 - 14 + ex) << 23) * p.scale * kLog2e;
+            const float back = __uint_as_float((uint32_t)(127 - 14 + ex) << 23) * p.scale * kLog2e;
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
+            for (int st = 0; st < KS; ++st)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const float x0 = x[4 * s + 2 * b] * mul, x1 = x[4 * s + 2 * b + 1] * mul;
-                    qa[0][s][2 * b + e] = pack_f16(x0, x1);
+                    const float x0 = x[4 * st + 2 * b] * mul, x1 = x[4 * st + 2 * b + 1] * mul;
+                    qb[0][nb][st][b] = pack_f16(x0, x1);
                     if constexpr (TERMS == 2) {
-                        const float2 hi = unpack_f16(qa[0][s][2 * b + e]);
-                        qa[1][s][2 * b + e] = pack_f16(x0 - hi.x, x1 - hi.y);
+                        const float2 hi = unpack_f16(qb[0][nb][st][b]);
+                        qb[1][nb][st][b] = pack_f16(x0 - hi.x, x1 - hi.y);
                     }
                 }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                qs[nb][e] = __shfl_sync(~0u, back, 4 * (2 * t + e));
+                const int re = row0 + 8 * nb + 2 * t + e;
+                limit[nb][e] = re < rows_all ? un.len - p.D + 1 + re / p.G : 0;
             }
         }
-        float o[NT][4];
+        float o[NB][DT][4];
+        float m[NB][2], l[NB][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[nt][c] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        float vref = 0.f;  // the scale that o is counted in
+            for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[nb][dt][c] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[nb][e] = -INFINITY;
+                l[nb][e] = 0.f;
+            }
+        }
+        float vref = 0.f;                      // the scale that o is counted in
         const int window0 = un.len - p.D + 1;  // first position that some row does not see
 
         for (int pi = 0; pi < pages_here; ++pi, ++i) {
@@ -383,234 +435,280 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const AttnDeco
             const int sk = (int)(ck % SL), sv = (int)(cv % SL);
             if (!warp_wait(full + sk, ck / SL)) { timeout = true; break; }
             const PageMeta pm = meta[i % kMeta];
-            const float ks = pm.ks, vs = pm.vs;
+            const float vs = pm.vs;
             const bool have = pm.block >= 0;
             const bool tail = pos0 + kPage > window0 || !have;
-            float s[8][4];
+            float s[NB][4][4];
             {
-                const unsigned char *kb = ring + sk * S::kHalf;
+                const unsigned char *kb = ring + sk * S::kHalf + (16 * (g >> 1) + (g & 1)) * HD;
+                // two score tiles at a time, so that several chains of products run side by side
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const unsigned char *row = kb + (16 * (g >> 1) + 2 * j + (g & 1)) * HD;
-                    uint32_t kw[HD / 16];
-                    if constexpr (HD == 128) {
-                        const uint4 a = *reinterpret_cast<const uint4 *>(row + 16 * t);
-                        const uint4 b = *reinterpret_cast<const uint4 *>(row + 64 + 16 * t);
-                        kw[0] = a.x; kw[1] = a.y; kw[2] = a.z; kw[3] = a.w;
-                        kw[4] = b.x; kw[5] = b.y; kw[6] = b.z; kw[7] = b.w;
-                    } else if constexpr (HD == 64) {
-                        const uint4 a = *reinterpret_cast<const uint4 *>(row + 16 * t);
-                        kw[0] = a.x; kw[1] = a.y; kw[2] = a.z; kw[3] = a.w;
-                    } else {
-                        const uint2 a = *reinterpret_cast<const uint2 *>(row + 8 * t);
-                        kw[0] = a.x; kw[1] = a.y;
-                    }
-                    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                for (int i2 = 0; i2 < 4; i2 += 2) {
+                    uint32_t kw[2][2][HD / 16];
 #pragma unroll
-                    for (int st = 0; st < KS; ++st) {
-                        uint32_t b0, b1;
-                        e4m3x4_to_f16(kw[st], b0, b1);
-                        float(&c)[4] = acc[st & 1];
-                        mma16816(c, qa[0][st][0], qa[0][st][1], qa[0][st][2], qa[0][st][3], b0, b1);
-                        if constexpr (TERMS == 2)
-                            mma16816(c, qa[1][st][0], qa[1][st][1], qa[1][st][2], qa[1][st][3], b0, b1);
-                    }
+                    for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[j][c] = acc[0][c] + acc[1][c];
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const unsigned char *row = kb + (4 * (i2 + ii) + 2 * hf) * HD;
+                            if constexpr (HD >= 64) {
+#pragma unroll
+                                for (int b = 0; b < HD / 64; ++b) {
+                                    const uint4 a = *reinterpret_cast<const uint4 *>(row + 64 * b + 16 * t);
+                                    kw[ii][hf][4 * b] = a.x; kw[ii][hf][4 * b + 1] = a.y;
+                                    kw[ii][hf][4 * b + 2] = a.z; kw[ii][hf][4 * b + 3] = a.w;
+                                }
+                            } else {
+                                const uint2 a = *reinterpret_cast<const uint2 *>(row + 8 * t);
+                                kw[ii][hf][0] = a.x; kw[ii][hf][1] = a.y;
+                            }
+                        }
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) s[nb][i2 + ii][c] = 0.f;
+#pragma unroll
+                    for (int st = 0; st < KS; ++st)
+#pragma unroll
+                        for (int ii = 0; ii < 2; ++ii) {
+                            uint32_t a0, a1, a2, a3;
+                            e4m3x4_to_f16(kw[ii][0][st], a0, a2);
+                            e4m3x4_to_f16(kw[ii][1][st], a1, a3);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                                for (int tm = 0; tm < TERMS; ++tm)
+                                    mma16816(s[nb][i2 + ii], a0, a1, a2, a3, qb[tm][nb][st][0], qb[tm][nb][st][1]);
+                        }
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty + sk);
+            if (MT > 1 && lane == 0) mbar_arrive(empty + sk);
             // the next copy into the slot that is free now
             if (mt == 0 && ck + SL < 2 * count) {
-                if (!warp_wait(empty + sk, ck / SL)) { timeout = true; break; }
+                if (MT > 1 && !warp_wait(empty + sk, ck / SL)) { timeout = true; break; }
                 issue(ck + SL);
             }
             // ---- softmax
-            const float f0 = qs[0] * ks, f1 = qs[1] * ks;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                s[j][0] *= f0; s[j][1] *= f0;
-                s[j][2] *= f1; s[j][3] *= f1;
-            }
             if (tail) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int pos = pos0 + 16 * t + 2 * j + (c & 1);
-                        if (!have || pos >= limit[c >> 1]) s[j][c] = -INFINITY;
-                    }
-            }
-            float mx[2] = {-INFINITY, -INFINITY};
+                    for (int ti = 0; ti < 4; ++ti)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                mx[0] = fmaxf(mx[0], fmaxf(s[j][0], s[j][1]));
-                mx[1] = fmaxf(mx[1], fmaxf(s[j][2], s[j][3]));
+                        for (int c = 0; c < 4; ++c) {
+                            const int pos = pos0 + 16 * (g >> 1) + 4 * ti + (c & 2) + (g & 1);
+                            if (!have || pos >= limit[nb][c & 1]) s[nb][ti][c] = -INFINITY;
+                        }
             }
-            float alpha[2], use[2];
+            // o is counted in the largest value scale so far, the page's weights
+            // in units of 2^-15 of it: a power of two that goes into the exponent
             const float vnew = fmaxf(vref, have ? vs : 0.f);
-            const float pmul = have ? kPScale * (vs / vnew) : 0.f;
+            const float ratio = have ? vs / vnew : 1.f;
+            const int bias = 15 + (int)(__float_as_uint(ratio) >> 23) - 127;
+            const float unbias = __uint_as_float((uint32_t)(127 - (bias < -100 ? -100 : bias)) << 23);
             const float vfix = vref > 0.f ? vref / vnew : 1.f;
             vref = vnew;
+            uint32_t pb[TERMS][NB][4][2];
+            float alpha[NB][2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 1));
-                mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 2));
-                const float mn = fmaxf(m[e], mx[e]);
-                use[e] = mn == -INFINITY ? 0.f : mn;
-                alpha[e] = ex2(m[e] - use[e]);
-                m[e] = mn;
-                l[e] *= alpha[e];
-            }
-            uint32_t pa[TERMS][4][4];
-            float rs[2] = {0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int nb = 0; nb < NB; ++nb) {
+                float f[2], use[2], rs[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float p0 = ex2(s[j][2 * e] - use[e]), p1 = ex2(s[j][2 * e + 1] - use[e]);
-                    rs[e] += p0 + p1;
-                    const float x0 = p0 * pmul, x1 = p1 * pmul;
-                    // tile 2 s: registers 0 (row g), 1 (row g + 8); tile 2 s + 1: registers 2, 3
-                    uint32_t &d = pa[0][j >> 1][2 * (j & 1) + e];
-                    d = pack_f16(x0, x1);
-                    if constexpr (TERMS == 2) {
-                        const float2 hi = unpack_f16(d);
-                        pa[1][j >> 1][2 * (j & 1) + e] = pack_f16(x0 - hi.x, x1 - hi.y);
+                    f[e] = fmaxf(qs[nb][e] * pm.ks, 1e-37f);  // positive, so that -inf stays -inf
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int ti = 0; ti < 4; ++ti) mx = fmaxf(mx, fmaxf(s[nb][ti][e], s[nb][ti][2 + e]));
+                    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+                    const float mn = fmaxf(m[nb][e], mx * f[e]);
+                    use[e] = mn == -INFINITY ? 0.f : mn;
+                    alpha[nb][e] = ex2(m[nb][e] - use[e]);
+                    m[nb][e] = mn;
+                }
+                rs[0] = rs[1] = 0.f;
+                const float b0 = (float)bias - use[0], b1 = (float)bias - use[1];
+                if (bias < -45) {  // the sum apart: these weights may vanish next to the larger scale
+#pragma unroll
+                    for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) rs[c & 1] += ex2(fmaf(s[nb][ti][c], f[c & 1], -use[c & 1]));
+                }
+#pragma unroll
+                for (int ti = 0; ti < 4; ++ti) {
+                    float w[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) w[c] = ex2(fmaf(s[nb][ti][c], f[c & 1], (c & 1) ? b1 : b0));
+                    if (bias >= -45) {
+                        rs[0] += w[0] + w[2];
+                        rs[1] += w[1] + w[3];
+                    }
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint32_t x = pack_f16(w[2 * hf], w[2 * hf + 1]);
+                        pb[0][nb][ti][hf] = transpose8x8(x);
+                        if constexpr (TERMS == 2) {
+                            const float2 hi = unpack_f16(x);
+                            pb[1][nb][ti][hf] = transpose8x8(pack_f16(w[2 * hf] - hi.x, w[2 * hf + 1] - hi.y));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (bias >= -45) rs[e] *= unbias;
+                    l[nb][e] = fmaf(l[nb][e], alpha[nb][e], rs[e]);
+                    alpha[nb][e] *= vfix;
+                }
+                if (p.weight_out != nullptr) {  // the page's share, relative to the maximum so far
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = rs[e];
+                        x += __shfl_xor_sync(~0u, x, 4);
+                        x += __shfl_xor_sync(~0u, x, 8);
+                        x += __shfl_xor_sync(~0u, x, 16);
+                        const int r = row0 + 8 * nb + 2 * t + e;
+                        if (g == 0 && r < rows_all) {
+                            const int64_t qrow = ((int64_t)un.n * p.D + r / p.G) * p.Hq + h * p.G + r % p.G;
+                            ws[lay.page_w + qrow * p.max_pages + page] = x > 0.f ? log2f(x) + use[e] : -INFINITY;
+                        }
                     }
                 }
             }
-            l[0] += rs[0];
-            l[1] += rs[1];
-            if (p.weight_out != nullptr) {  // the page's share, relative to the maximum so far
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x = rs[e];
-                    x += __shfl_xor_sync(~0u, x, 1);
-                    x += __shfl_xor_sync(~0u, x, 2);
-                    if (t == 0 && valid[e])
-                        ws[lay.page_w + qrow[e] * p.max_pages + page] = x > 0.f ? log2f(x) + use[e] : -INFINITY;
-                }
-            }
-            alpha[0] *= vfix;
-            alpha[1] *= vfix;
             // ---- output
             if (!warp_wait(full + sv, cv / SL)) { timeout = true; break; }
-            const unsigned char *vb = ring + sv * S::kHalf;
-            if (!tail) {
+            const unsigned char *vb = ring + sv * S::kHalf + g * kPage + 16 * t;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(vb + (8 * nt + g) * kPage + 16 * t);
-                    const uint32_t vw[4] = {a.x, a.y, a.z, a.w};
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int d2 = 0; d2 < DT; d2 += 2) {
+                uint32_t vw[2][2][4];
+                int nan_at[2][2] = {{kPage, kPage}, {kPage, kPage}};
 #pragma unroll
-                    for (int st = 0; st < 4; ++st) {
-                        uint32_t b0, b1;
-                        e4m3x4_to_f16(vw[st], b0, b1);
-                        mma16816(c, pa[0][st][0], pa[0][st][1], pa[0][st][2], pa[0][st][3], b0, b1);
-                        if constexpr (TERMS == 2)
-                            mma16816(c, pa[1][st][0], pa[1][st][1], pa[1][st][2], pa[1][st][3], b0, b1);
+                for (int dd = 0; dd < 2; ++dd)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint4 a = *reinterpret_cast<const uint4 *>(vb + (16 * (d2 + dd) + 8 * hf) * kPage);
+                        vw[dd][hf][0] = a.x; vw[dd][hf][1] = a.y; vw[dd][hf][2] = a.z; vw[dd][hf][3] = a.w;
                     }
+                if (tail) {
+                    // bytes past the end (whatever they hold) count as zero, and so do
+                    // the window's NaN bytes, which only the rows that see them get
+                    const int left = have ? un.len - pos0 : 0;  // positions of the page that exist
+                    const int seen = window0 - pos0;            // positions that every row sees
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) o[nt][k] = fmaf(o[nt][k], alpha[k >> 1], c[k]);
-                }
-            } else {
-                // bytes past the end (whatever they hold) count as zero, and so do
-                // the window's NaN bytes, which only the rows that see them get
-                const int left = have ? un.len - pos0 : 0;     // positions of the page that exist
-                const int seen = window0 - pos0;               // positions that every row sees
+                    for (int dd = 0; dd < 2; ++dd)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(vb + (8 * nt + g) * kPage + 16 * t);
-                    uint32_t vw[4] = {a.x, a.y, a.z, a.w};
-                    int nan_at = kPage;
+                        for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-                    for (int st = 0; st < 4; ++st)
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const int pos = 16 * t + 4 * st + b;
-                            const bool nan = ((vw[st] >> (8 * b)) & 0x7fu) == 0x7fu;
-                            if (pos >= left) {
-                                vw[st] &= ~(0xffu << (8 * b));
-                            } else if (nan && pos >= seen) {
-                                vw[st] &= ~(0xffu << (8 * b));
-                                nan_at = min(nan_at, pos);
-                            }
+                            for (int st = 0; st < 4; ++st)
+                                nan_at[dd][hf] = min(nan_at[dd][hf], mask_word(vw[dd][hf][st], 16 * t + 4 * st, left, seen));
+                            nan_at[dd][hf] = min(nan_at[dd][hf], __shfl_xor_sync(~0u, nan_at[dd][hf], 1));
+                            nan_at[dd][hf] = min(nan_at[dd][hf], __shfl_xor_sync(~0u, nan_at[dd][hf], 2));
                         }
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int st = 0; st < 4; ++st) {
-                        uint32_t b0, b1;
-                        e4m3x4_to_f16(vw[st], b0, b1);
-                        mma16816(c, pa[0][st][0], pa[0][st][1], pa[0][st][2], pa[0][st][3], b0, b1);
-                        if constexpr (TERMS == 2)
-                            mma16816(c, pa[1][st][0], pa[1][st][1], pa[1][st][2], pa[1][st][3], b0, b1);
-                    }
-                    nan_at = min(nan_at, __shfl_xor_sync(~0u, nan_at, 1));
-                    nan_at = min(nan_at, __shfl_xor_sync(~0u, nan_at, 2));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        // accumulator column 8 nt + 2 t + k % 2 is the channel of quad 2 t + k % 2
-                        const int at = __shfl_sync(~0u, nan_at, 4 * (2 * t + (k & 1)));
-                        o[nt][k] = fmaf(o[nt][k], alpha[k >> 1], c[k]);
-                        if (at < kPage && pos0 + at < limit[k >> 1]) o[nt][k] = NAN;
-                    }
                 }
+                float c[NB][2][4];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int dd = 0; dd < 2; ++dd)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) c[nb][dd][k] = 0.f;
+#pragma unroll
+                for (int st = 0; st < 4; ++st)
+#pragma unroll
+                    for (int dd = 0; dd < 2; ++dd) {
+                        uint32_t a0, a1, a2, a3;
+                        e4m3x4_to_f16(vw[dd][0][st], a0, a2);
+                        e4m3x4_to_f16(vw[dd][1][st], a1, a3);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int tm = 0; tm < TERMS; ++tm)
+                                mma16816(c[nb][dd], a0, a1, a2, a3, pb[tm][nb][st][0], pb[tm][nb][st][1]);
+                    }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int dd = 0; dd < 2; ++dd)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float &x = o[nb][d2 + dd][k];
+                            x = fmaf(x, alpha[nb][k & 1], c[nb][dd][k]);
+                            const int at = nan_at[dd][k >> 1];
+                            if (tail && at < kPage && pos0 + at < limit[nb][k & 1]) x = NAN;
+                        }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty + sv);
+            if (MT > 1 && lane == 0) mbar_arrive(empty + sv);
             if (mt == 0 && cv + SL < 2 * count) {
-                if (!warp_wait(empty + sv, cv / SL)) { timeout = true; break; }
+                if (MT > 1 && !warp_wait(empty + sv, cv / SL)) { timeout = true; break; }
                 issue(cv + SL);
             }
         }
         if (timeout) break;
+        if (i >= count) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
         // ---- the item's end
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            l[e] += __shfl_xor_sync(~0u, l[e], 1);
-            l[e] += __shfl_xor_sync(~0u, l[e], 2);
-        }
         const float unit = vref * (1.f / kPScale);
         const bool whole = un.page == 0 && pages_here == un.pages;
-        if (whole) {
+        const int64_t slot = 2 * w + (un.page == 0 ? 1 : 0);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            float f[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                if (!valid[e]) continue;
-                const float f = l[e] == 0.f ? 0.f : unit / l[e];
-                T *dst = static_cast<T *>(p.out) + qrow[e] * HD;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    store2(dst + 8 * nt + 2 * t, l[e] == 0.f ? 0.f : o[nt][2 * e] * f,
-                           l[e] == 0.f ? 0.f : o[nt][2 * e + 1] * f);
-                if (t == 0) {
-                    const float lse2 = l[e] == 0.f ? -INFINITY : m[e] + log2f(l[e]);
-                    if (p.lse) p.lse[qrow[e]] = lse2 * kLn2;
-                    if (p.weight_out) ws[lay.lse2 + qrow[e]] = lse2;
+                float x = l[nb][e];
+                x += __shfl_xor_sync(~0u, x, 4);
+                x += __shfl_xor_sync(~0u, x, 8);
+                x += __shfl_xor_sync(~0u, x, 16);
+                const int r = row0 + 8 * nb + 2 * t + e;
+                f[e] = whole ? (x == 0.f ? 0.f : unit / x) : unit;
+                if (r >= rows_all || g != 0) continue;
+                if (whole) {
+                    const int64_t qrow = ((int64_t)un.n * p.D + r / p.G) * p.Hq + h * p.G + r % p.G;
+                    const float lse2 = x == 0.f ? -INFINITY : m[nb][e] + log2f(x);
+                    if (p.lse) p.lse[qrow] = lse2 * kLn2;
+                    if (p.weight_out) ws[lay.lse2 + qrow] = lse2;
+                } else {
+                    ws[lay.part_m + slot * PR + r - rb * R] = m[nb][e];
+                    ws[lay.part_l + slot * PR + r - rb * R] = x;
                 }
             }
-        } else {
-            const int64_t slot = 2 * w + (un.page == 0 ? 1 : 0);
+            if (whole && sizeof(T) == 2) {
+                // rows g, channel pairs 2 t: four lanes write 16 bytes of a row
+                const int r = row0 + 8 * nb + g;
+                T *dst = static_cast<T *>(p.out) +
+                         (((int64_t)un.n * p.D + r / p.G) * p.Hq + h * p.G + r % p.G) * HD + 2 * t;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = mt * 16 + g + 8 * e;
-                float *dst = ws + lay.part_o + (slot * R + r) * HD;
+                for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) store2(dst + 8 * nt + 2 * t, o[nt][2 * e] * unit, o[nt][2 * e + 1] * unit);
-                if (t == 0) {
-                    ws[lay.part_m + slot * R + r] = m[e];
-                    ws[lay.part_l + slot * R + r] = l[e];
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const float x0 = f[0] == 0.f ? 0.f : o[nb][dt][2 * hf] * f[0];
+                        const float x1 = f[1] == 0.f ? 0.f : o[nb][dt][2 * hf + 1] * f[1];
+                        const uint32_t y = transpose8x8(pack_bf16(x0, x1));
+                        if (r < rows_all) *reinterpret_cast<uint32_t *>(dst + 16 * dt + 8 * hf) = y;
+                    }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = row0 + 8 * nb + 2 * t + e;
+                    if (r >= rows_all) continue;
+                    float *dst = whole ? static_cast<float *>(p.out) +
+                                             (((int64_t)un.n * p.D + r / p.G) * p.Hq + h * p.G + r % p.G) * HD
+                                       : ws + lay.part_o + (slot * PR + r - rb * R) * HD;
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf)
+                            dst[16 * dt + 8 * hf + g] = f[e] == 0.f ? 0.f : o[nb][dt][2 * hf + e] * f[e];
                 }
             }
-            if (un.page == 0 && mt == 0 && lane == 0) {
-                // this worker holds the item's first part: the join starts here
-                const int64_t end = cur.base + (int64_t)(un.hr + 1) * un.pages;  // one past the item's last unit
-                desc[1] = un.hr;
-                desc[2] = (int)((end * W + U - 1) / U - 1);                      // the worker of that last unit
-                desc[0] = un.n;
-            }
+        }
+        if (un.page == 0 && tid == 0) {  // this worker holds the item's first page
+            const int64_t end = cur.base + (int64_t)(un.hr + 1) * un.pages;  // one past the item's last unit
+            *reinterpret_cast<int2 *>(ws + lay.desc + 2 * ((int64_t)un.n * HR + un.hr)) =
+                make_int2((int)w, whole ? (int)w : (int)((end * W + U - 1) / U - 1));  // the worker of its last unit
         }
     }
     if (timeout && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_TIMEOUT);
@@ -619,48 +717,87 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const AttnDeco
             mbar_wait_drain(full + c % SL, (uint32_t)(c / SL) & 1u);
 }
 
-// Adds up the parts of one cut item: block (w, y) takes the item that starts
-// in worker w and is continued, rows 8 y..8 y + 7 of it.
-template <typename T, int HD, int MT>
-__global__ void __launch_bounds__(128) join_kernel(const AttnDecodeParams p) {
-    constexpr int R = 16 * MT;
-    const float *ws = static_cast<const float *>(p.workspace);
-    const Layout lay = make_layout(p.batch, p.D, p.Hq, p.Hkv, HD, p.max_pages, p.weight_out != nullptr);
-    const int64_t w = blockIdx.x;
-    const int *desc = reinterpret_cast<const int *>(ws + lay.desc) + 4 * w;
-    const int n = desc[0];
-    if (n < 0) return;
-    const int hr = desc[1], last = desc[2];
-    const int rows_all = p.D * p.G, RB = (rows_all + R - 1) / R;
+// Adds up the parts of the cut items: a block takes an item and a row (or,
+// where there are many items, its rows in turn).  Groups of HD / 4 threads take
+// every kJoinThreads / (HD / 4)-th part; their sums are added in order.
+constexpr int kJoinThreads = 512;
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDecodeParams p, const Layout lay, int RB, int R, int PR,
+                                                         int workers) {
+    constexpr int TPR = HD / 4, GR = kJoinThreads / TPR;
+    __shared__ float wmax[kJoinThreads / 32];
+    __shared__ float4 so[GR][TPR];
+    __shared__ float sl[GR];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float *ws = static_cast<float *>(p.workspace);
+    const int HR = p.Hkv * RB, n = blockIdx.x / HR, hr = blockIdx.x % HR;
+    if (p.seq_lens[n] <= 0) return;
+    const int2 desc = *reinterpret_cast<const int2 *>(ws + lay.desc + 2 * (int64_t)blockIdx.x);
+    // (a worker that gave up waiting leaves no or stale entries)
+    if (desc.x < 0 || desc.x >= desc.y || desc.y >= workers) return;
+    const int64_t w = desc.x;
+    const int parts = desc.y - desc.x + 1;
+    const int rows_all = p.D * p.G;
     const int h = hr / RB, rb = hr % RB;
-    // HD / 4 threads per row
-    constexpr int TPR = HD / 4, RPB = 128 / TPR;
-    const int c4 = threadIdx.x % TPR;
-    const int r = blockIdx.y * RPB + threadIdx.x / TPR;
-    const int row = rb * R + r;
-    if (r >= R || row >= rows_all) return;
-    auto slot_of = [&](int64_t x) { return 2 * x + (x == w ? 1 : 0); };
-    float m = -INFINITY;
-    for (int64_t x = w; x <= last; ++x) m = fmaxf(m, ws[lay.part_m + slot_of(x) * R + r]);
-    const float use = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t x = w; x <= last; ++x) {
-        const int64_t sl = slot_of(x) * R + r;
-        const float f = ex2(ws[lay.part_m + sl] - use);
-        const float4 v = *reinterpret_cast<const float4 *>(ws + lay.part_o + sl * HD + 4 * c4);
-        l = fmaf(f, ws[lay.part_l + sl], l);
-        o[0] = fmaf(f, v.x, o[0]); o[1] = fmaf(f, v.y, o[1]);
-        o[2] = fmaf(f, v.z, o[2]); o[3] = fmaf(f, v.w, o[3]);
-    }
-    const int64_t qrow = ((int64_t)n * p.D + row / p.G) * p.Hq + h * p.G + row % p.G;
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    T *dst = static_cast<T *>(p.out) + qrow * HD + 4 * c4;
-    store2(dst, l == 0.f ? 0.f : o[0] * f, l == 0.f ? 0.f : o[1] * f);
-    store2(dst + 2, l == 0.f ? 0.f : o[2] * f, l == 0.f ? 0.f : o[3] * f);
-    if (c4 == 0) {
-        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
-        if (p.lse) p.lse[qrow] = lse2 * kLn2;
-        if (p.weight_out) static_cast<float *>(p.workspace)[lay.lse2 + qrow] = lse2;
+    const int tid = threadIdx.x;
+    for (int r = blockIdx.y; r < PR && rb * R + r < rows_all; r += gridDim.y) {
+        const int row = rb * R + r;
+        __syncthreads();
+        // part x lies in slot 2 (w + x), the first in slot 2 w + 1
+        auto at = [&](int x) { return (2 * (w + x) + (x == 0 ? 1 : 0)) * PR + r; };
+        float m = -INFINITY;
+        for (int x = tid; x < parts; x += kJoinThreads) m = fmaxf(m, ws[lay.part_m + at(x)]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        if ((tid & 31) == 0) wmax[tid >> 5] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, wmax[i]);
+        const float use = m == -INFINITY ? 0.f : m;
+        const int c4 = tid % TPR, gr = tid / TPR;
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int BATCH = 8;  // parts whose loads are in flight together
+        for (int x0 = gr; x0 < parts; x0 += GR * BATCH) {
+            float pm[BATCH], pl[BATCH];
+            float4 v[BATCH];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int64_t k = at(min(x0 + b * GR, parts - 1));  // past the end: the last part, with weight 0
+                pm[b] = ws[lay.part_m + k];
+                pl[b] = ws[lay.part_l + k];
+                v[b] = *reinterpret_cast<const float4 *>(ws + lay.part_o + k * HD + 4 * c4);
+            }
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                if (x0 + b * GR >= parts) break;
+                const float f = ex2(pm[b] - use);
+                l = fmaf(f, pl[b], l);
+                o.x = fmaf(f, v[b].x, o.x); o.y = fmaf(f, v[b].y, o.y);
+                o.z = fmaf(f, v[b].z, o.z); o.w = fmaf(f, v[b].w, o.w);
+            }
+        }
+        so[gr][c4] = o;
+        if (c4 == 0) sl[gr] = l;
+        __syncthreads();
+        if (gr != 0) continue;
+#pragma unroll 4
+        for (int i = 1; i < GR; ++i) {
+            const float4 v = so[i][c4];
+            o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+            l += sl[i];
+        }
+        const int64_t qrow = ((int64_t)n * p.D + row / p.G) * p.Hq + h * p.G + row % p.G;
+        const float f = l == 0.f ? 0.f : 1.f / l;
+        T *dst = static_cast<T *>(p.out) + qrow * HD + 4 * c4;
+        store2(dst, l == 0.f ? 0.f : o.x * f, l == 0.f ? 0.f : o.y * f);
+        store2(dst + 2, l == 0.f ? 0.f : o.z * f, l == 0.f ? 0.f : o.w * f);
+        if (c4 == 0) {
+            const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+            if (p.lse) p.lse[qrow] = lse2 * kLn2;
+            if (p.weight_out) ws[lay.lse2 + qrow] = lse2;
+        }
     }
 }
 
@@ -669,6 +806,7 @@ __global__ void __launch_bounds__(128) join_kernel(const AttnDecodeParams p) {
 // eighth row and are added up in order.
 __global__ void __launch_bounds__(256) page_weight_kernel(const AttnDecodeParams p, Layout lay) {
     __shared__ float part[8][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const float *ws = static_cast<const float *>(p.workspace);
     const int64_t chunks = (p.max_pages + 31) / 32;
     const int n = (int)(blockIdx.x / chunks);
@@ -694,39 +832,56 @@ __global__ void __launch_bounds__(256) page_weight_kernel(const AttnDecodeParams
     }
 }
 
-template <typename T, int HD, int MT>
+// A launch that may begin while the kernel before it on the stream ends (the
+// kernel waits for that one's results by itself).
+template <typename... Args>
+cudaError_t launch_after(void (*kern)(Args...), dim3 grid, int threads, cudaStream_t st,
+                         std::common_type_t<Args>... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename T, int HD, int NB, int MT>
 cudaError_t launch(const AttnDecodeParams &p, cudaStream_t st) {
-    using S = Smem<T, HD, MT>;
-    auto kern = decode_attn_kernel<T, HD, MT>;
+    using S = Smem<HD, NB, MT>;
+    auto kern = decode_attn_kernel<T, HD, NB, MT>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), S::kBytes, done);
     if (e != cudaSuccess) return e;
-    const int rows = p.D * p.G, RB = (rows + 16 * MT - 1) / (16 * MT);
-    // no more workers than pages
-    const int64_t units = (int64_t)p.batch * p.Hkv * RB * p.max_pages;
-    int64_t ctas = (units + S::kWorkers - 1) / S::kWorkers;
-    ctas = ctas < 1 ? 1 : ctas > kMaxCtas ? kMaxCtas : ctas;
-    kern<<<(unsigned)ctas, kThreads, S::kBytes, st>>>(p);
+    const int rows = p.D * p.G, RB = (rows + S::kRows - 1) / S::kRows, PR = part_rows(rows);
+    const int64_t items = (int64_t)p.batch * p.Hkv * RB;
+    if (items > 0x7fffffff) return cudaErrorInvalidValue;
+    const Layout lay = make_layout(p.batch, p.D, p.Hq, p.Hkv, HD, p.max_pages, p.weight_out != nullptr);
+    const int64_t workers = worker_count(items * p.max_pages, NB, MT);
+    kern<<<(unsigned)workers, 32 * MT, S::kBytes, st>>>(p, lay);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int rpb = 128 / (HD / 4);
-    const dim3 grid((unsigned)(ctas * S::kWorkers), (unsigned)((16 * MT + rpb - 1) / rpb));
-    join_kernel<T, HD, MT><<<grid, 128, 0, st>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || p.weight_out == nullptr || p.max_pages == 0) return e;
-    const Layout lay = make_layout(p.batch, p.D, p.Hq, p.Hkv, HD, p.max_pages, true);
+    if (p.max_pages == 0) return cudaSuccess;
+    const int R = S::kRows;
+    e = launch_after(join_kernel<T, HD>, dim3((unsigned)items, (unsigned)(items * PR <= 4096 ? PR : 1)), kJoinThreads, st,
+                     p, lay, RB, R, PR, (int)workers);
+    if (e != cudaSuccess || p.weight_out == nullptr) return e;
     const int64_t blocks = (int64_t)p.batch * ((p.max_pages + 31) / 32);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    page_weight_kernel<<<(unsigned)blocks, 256, 0, st>>>(p, lay);
-    return cudaGetLastError();
+    return launch_after(page_weight_kernel, dim3((unsigned)blocks), 256, st, p, lay);
 }
 
 template <typename T, int HD>
 cudaError_t launch_rows(const AttnDecodeParams &p, cudaStream_t st) {
-    switch (row_tile(p.D * p.G)) {
-        case 1: return launch<T, HD, 1>(p, st);
-        case 2: return launch<T, HD, 2>(p, st);
-        default: return launch<T, HD, 4>(p, st);
+    const int rows = p.D * p.G;
+    if (rows <= 8) return launch<T, HD, 1, 1>(p, st);
+    switch (tile_mt(rows)) {
+        case 1: return launch<T, HD, 2, 1>(p, st);
+        case 2: return launch<T, HD, 2, 2>(p, st);
+        default: return launch<T, HD, 2, 4>(p, st);
     }
 }
 
