@@ -37,89 +37,30 @@
 //    fp32 round-to-nearest, because the tensor cores truncate when they add.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <stdint.h>
 
 #include <type_traits>
 
+#include "kda_attn_decode.cuh"
 #include "kda_attn_internal.h"
 #include "kda_bulk.cuh"
-#include "kda_check.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kSms = 152;
+using namespace dec;
+
 // Warps per SM, by registers and by shared memory (the rings).
 __host__ __device__ constexpr int warps_per_sm(int NB) { return NB == 1 ? 12 : 8; }
-constexpr int kRounds = 4;      // workers per place on the GPU, at most
+constexpr int kRounds = 4;  // workers per place on the GPU, at most
 constexpr int kPagesPerWorker = 12;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPScale = 32768.f;  // fp16 scale of the weights
-
-// Workspace, in floats: for each item the workers of its first and last page
-// (desc), the cut items' partial results, two per worker (the range's first
-// item, the range's last item), then the rows' lse (base 2) and page weights
-// where weights are asked for.
-struct Layout {
-    int64_t desc, part_m, part_l, part_o, lse2, page_w, total;
-};
-
-// A worker's rows: MT warps of NB tiles of 8.
-__host__ __device__ inline int tile_nb(int rows) { return rows <= 8 ? 1 : 2; }
-__host__ __device__ inline int tile_mt(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
-__host__ __device__ inline int tile_rows(int rows) { return 8 * tile_nb(rows) * tile_mt(rows); }
-inline int64_t align64(int64_t x) { return (x + 63) / 64 * 64; }
-
-// Rows of a partial result: those of an item that exist.
-__host__ __device__ inline int part_rows(int rows) { return rows < tile_rows(rows) ? rows : tile_rows(rows); }
-
-// Workers for at most `units` pages: all places on the GPU once, or as many
-// whole times as leave a worker kPagesPerWorker pages.
-inline int64_t worker_count(int64_t units, int NB, int MT) {
-    const int64_t places = (int64_t)kSms * warps_per_sm(NB) / MT;
-    int64_t rounds = units / (places * kPagesPerWorker);
-    rounds = rounds < 1 ? 1 : rounds > kRounds ? kRounds : rounds;
-    const int64_t w = places * rounds < units ? places * rounds : units;
-    return w < 1 ? 1 : w;
-}
-
-inline Layout make_layout(int64_t batch, int D, int Hq, int Hkv, int d, int64_t max_pages,
-                                              bool with_weight) {
-    const int rows = D * (Hq / Hkv), TR = tile_rows(rows), R = part_rows(rows);
-    const int64_t items = batch * Hkv * ((rows + TR - 1) / TR);
-    const int64_t workers = worker_count(items * max_pages, tile_nb(rows), tile_mt(rows));
-    Layout l;
-    l.desc = 0;
-    l.part_m = align64(2 * items);
-    l.part_l = l.part_m + align64(2 * workers * R);
-    l.part_o = l.part_l + align64(2 * workers * R);
-    l.lse2 = l.part_o + align64(2 * workers * R * d);
-    l.page_w = l.lse2 + (with_weight ? align64(batch * D * Hq) : 0);
-    l.total = l.page_w + (with_weight ? align64(batch * D * Hq * max_pages) : 0);
-    return l;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Four e4m3 bytes as two pairs of fp16 (exact).
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
 }
 
 // The transpose of an 8 x 8 matrix of 16-bit values (two per thread).
@@ -129,72 +70,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float2 unpack_f16(uint32_t u) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
-}
-
 template <typename T>
 __device__ __forceinline__ float load1(const T *p);
 template <>
 __device__ __forceinline__ float load1<float>(const float *p) { return *p; }
 template <>
 __device__ __forceinline__ float load1<__nv_bfloat16>(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
-__device__ __forceinline__ void store2(__nv_bfloat16 *p, float a, float b) {
-    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(a, b);
-}
-
-__device__ __forceinline__ int pages_of(const AttnDecodeParams &p, int n, int &len) {
-    const int cap = p.max_pages * kPage;
-    len = p.seq_lens[n];
-    len = len < 0 ? 0 : len > cap ? cap : len;
-    return (len + kPage - 1) / kPage;
-}
-
-// Where a unit (one page of one item) lies: sequence n with its first unit at
-// `base`, item hr = kv head * row blocks + row block, page index.
-struct Cursor {
-    int n;
-    int64_t base;
-};
-
-// What a worker needs to know of a page: its block in the cache (page * Hkv +
-// kv head; -1: none) and the scales.
-struct PageMeta {
-    int block;
-    float ks, vs;
-};
-constexpr int kMeta = 64;  // entries per worker: two batches of 32 units
-
-struct Unit {
-    int n, hr, page, pages, len;
-};
-
-// Moves the cursor to the sequence that holds unit u >= cursor.base.
-__device__ __forceinline__ Unit locate(const AttnDecodeParams &p, int HR, Cursor &c, int64_t u) {
-    Unit r;
-    while (true) {
-        r.pages = pages_of(p, c.n, r.len);
-        const int64_t end = c.base + (int64_t)r.pages * HR;
-        if (u < end || c.n + 1 >= p.batch) break;
-        c.base = end;
-        ++c.n;
-    }
-    const int64_t rem = u - c.base;
-    r.n = c.n;
-    r.hr = r.pages > 0 ? (int)(rem / r.pages) : 0;
-    r.page = r.pages > 0 ? (int)(rem - (int64_t)r.hr * r.pages) : 0;
-    return r;
-}
 
 // A bounded wait by all lanes of a warp with one answer.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, int64_t phase) {
@@ -215,26 +96,8 @@ __device__ __forceinline__ void load_row(const T *row, int t, bool valid, float 
     for (int j = 0; j < HD / 4; ++j) x[j] = valid ? load1<T>(row + chan<HD>(t, j)) : 0.f;
 }
 
-// Clears the bytes of a value word (positions pos..pos + 3 of the page) from
-// `left` on, and the NaN bytes from `seen` on; the first of the latter, or kPage.
-__device__ __forceinline__ int mask_word(uint32_t &w, int pos, int left, int seen) {
-    int at = kPage;
-#pragma unroll
-    for (int b = 3; b >= 0; --b) {
-        const bool nan = ((w >> (8 * b)) & 0x7fu) == 0x7fu;
-        if (pos + b >= left) {
-            w &= ~(0xffu << (8 * b));
-        } else if (nan && pos + b >= seen) {
-            w &= ~(0xffu << (8 * b));
-            at = pos + b;
-        }
-    }
-    return at;
-}
-
 template <int HD, int NB, int MT>
 struct Smem {
-    static constexpr int kRows = 8 * NB * MT;
     static constexpr int kHalf = HD * kPage;  // bytes of a page's keys (or values)
     static constexpr int kSlots = (NB == 1 ? 2 : 3) * MT * (128 / HD);  // 16 or 24 KiB per warp
     static constexpr int kRingBytes = kSlots * kHalf;
@@ -260,8 +123,7 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
 
     const int tid = threadIdx.x, lane = tid & 31, mt = tid >> 5;  // mt: row tile of the warp
     const int g = lane >> 2, t = lane & 3;
-    const int rows_all = p.D * p.G, PR = part_rows(rows_all);
-    const int RB = (rows_all + R - 1) / R, HR = p.Hkv * RB;
+    const int rows_all = p.D * p.G, PR = lay.PR, RB = lay.RB, HR = p.Hkv * RB;
     const int64_t w = blockIdx.x;
     float *ws = static_cast<float *>(p.workspace);
 
@@ -271,50 +133,8 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
     }
     fence_barrier_init();
 
-    // ---- the batch's units, and where this worker's range starts
-    const int per = (p.batch + kThreads - 1) / kThreads;
-    const int nb = min(tid * per, p.batch), ne = min(nb + per, p.batch);
-    int64_t mine = 0;
-    for (int n = nb; n < ne; ++n) {
-        int len;
-        mine += (int64_t)pages_of(p, n, len) * HR;
-        if (w == 0 && p.err_flag && p.seq_lens[n] > p.max_pages * kPage) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
-    }
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(~0u, incl, o);
-        if (lane >= o) incl += x;
-    }
-    int64_t U = __shfl_sync(~0u, incl, 31), excl = incl - mine;
-    if constexpr (MT > 1) {
-        if (lane == 31) warp_sum[mt] = incl;
-        __syncthreads();
-        U = 0;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            if (i < mt) excl += warp_sum[i];
-            U += warp_sum[i];
-        }
-    }
-    // no more workers than units, so that no range is empty
-    const int64_t W = min((int64_t)gridDim.x, max(U, (int64_t)1));
-    const int64_t u0 = w < W ? U * w / W : 0, u1 = w < W ? U * (w + 1) / W : 0;
-    if (mine > 0 && u0 >= excl && u0 < excl + mine) {
-        Cursor c{nb, excl};
-        locate(p, HR, c, u0);
-        start = c;
-    }
-    // sequences without pages have no unit: their rows are written here
-    for (int n = blockIdx.x; n < p.batch; n += gridDim.x) {
-        if (p.seq_lens[n] > 0 && p.max_pages > 0) continue;
-        T *o = static_cast<T *>(p.out) + (int64_t)n * p.D * p.Hq * HD;
-        for (int64_t i = tid; i < (int64_t)p.D * p.Hq * HD / 2; i += kThreads) store2(o + 2 * i, 0.f, 0.f);
-        for (int i = tid; i < p.D * p.Hq; i += kThreads) {
-            if (p.lse) p.lse[(int64_t)n * p.D * p.Hq + i] = -INFINITY;
-        }
-    }
-    __syncthreads();
+    int64_t U, W, u0, u1;
+    find_range<T, HD, MT>(p, HR, warp_sum, &start, U, W, u0, u1);
     if (u0 >= u1) return;
     const int64_t count = u1 - u0;
 
@@ -705,11 +525,7 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
                 }
             }
         }
-        if (un.page == 0 && tid == 0) {  // this worker holds the item's first page
-            const int64_t end = cur.base + (int64_t)(un.hr + 1) * un.pages;  // one past the item's last unit
-            *reinterpret_cast<int2 *>(ws + lay.desc + 2 * ((int64_t)un.n * HR + un.hr)) =
-                make_int2((int)w, whole ? (int)w : (int)((end * W + U - 1) / U - 1));  // the worker of its last unit
-        }
+        if (un.page == 0 && tid == 0) write_desc(ws, lay, un, cur, HR, whole, W, U);
     }
     if (timeout && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_TIMEOUT);
     if (timeout && mt == 0)  // the copies in flight land before the CTA's memory goes
@@ -720,22 +536,23 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
 // Adds up the parts of the cut items: a block takes an item and a row (or,
 // where there are many items, its rows in turn).  Groups of HD / 4 threads take
 // every kJoinThreads / (HD / 4)-th part; their sums are added in order.
-constexpr int kJoinThreads = 512;
+// Blocks of 512 threads where items have many parts, of 128 where they have few.
+constexpr int64_t kJoinBlocks = 16384;
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDecodeParams p, const Layout lay, int RB, int R, int PR,
-                                                         int workers) {
+template <typename T, int HD, int kJoinThreads>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDecodeParams p, const Layout lay) {
     constexpr int TPR = HD / 4, GR = kJoinThreads / TPR;
     __shared__ float wmax[kJoinThreads / 32];
     __shared__ float4 so[GR][TPR];
     __shared__ float sl[GR];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float *ws = static_cast<float *>(p.workspace);
+    const int RB = lay.RB, R = lay.R, PR = lay.PR;
     const int HR = p.Hkv * RB, n = blockIdx.x / HR, hr = blockIdx.x % HR;
     if (p.seq_lens[n] <= 0) return;
     const int2 desc = *reinterpret_cast<const int2 *>(ws + lay.desc + 2 * (int64_t)blockIdx.x);
     // (a worker that gave up waiting leaves no or stale entries)
-    if (desc.x < 0 || desc.x >= desc.y || desc.y >= workers) return;
+    if (desc.x < 0 || desc.x >= desc.y || desc.y >= lay.workers) return;
     const int64_t w = desc.x;
     const int parts = desc.y - desc.x + 1;
     const int rows_all = p.D * p.G;
@@ -801,6 +618,23 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDecodePara
     }
 }
 
+// A launch that may begin while the kernel before it on the stream ends (the
+// kernel waits for that one's results by itself).
+template <typename... Args>
+cudaError_t launch_after(void (*kern)(Args...), dim3 grid, int threads, cudaStream_t st,
+                         std::common_type_t<Args>... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // weight_out[n][page] = weight_in + sum over the rows of 2^(page share - lse).
 // A block takes 32 pages of a sequence; its 8 groups of threads take every
 // eighth row and are added up in order.
@@ -832,73 +666,87 @@ __global__ void __launch_bounds__(256) page_weight_kernel(const AttnDecodeParams
     }
 }
 
-// A launch that may begin while the kernel before it on the stream ends (the
-// kernel waits for that one's results by itself).
-template <typename... Args>
-cudaError_t launch_after(void (*kern)(Args...), dim3 grid, int threads, cudaStream_t st,
-                         std::common_type_t<Args>... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <typename T, int HD, int NB, int MT>
-cudaError_t launch(const AttnDecodeParams &p, cudaStream_t st) {
+cudaError_t launch_main(const AttnDecodeParams &p, const Layout &lay, cudaStream_t st) {
     using S = Smem<HD, NB, MT>;
     auto kern = decode_attn_kernel<T, HD, NB, MT>;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), S::kBytes, done);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), S::kBytes, done);
     if (e != cudaSuccess) return e;
-    const int rows = p.D * p.G, RB = (rows + S::kRows - 1) / S::kRows, PR = part_rows(rows);
-    const int64_t items = (int64_t)p.batch * p.Hkv * RB;
-    if (items > 0x7fffffff) return cudaErrorInvalidValue;
-    const Layout lay = make_layout(p.batch, p.D, p.Hq, p.Hkv, HD, p.max_pages, p.weight_out != nullptr);
-    const int64_t workers = worker_count(items * p.max_pages, NB, MT);
-    kern<<<(unsigned)workers, 32 * MT, S::kBytes, st>>>(p, lay);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    if (p.max_pages == 0) return cudaSuccess;
-    const int R = S::kRows;
-    e = launch_after(join_kernel<T, HD>, dim3((unsigned)items, (unsigned)(items * PR <= 4096 ? PR : 1)), kJoinThreads, st,
-                     p, lay, RB, R, PR, (int)workers);
+    kern<<<(unsigned)lay.workers, 32 * MT, S::kBytes, st>>>(p, lay);
+    return cudaGetLastError();
+}
+
+template <typename T, int HD>
+cudaError_t launch(const AttnDecodeParams &p, cudaStream_t st) {
+    const Layout lay = make_layout(p.batch, p.D, p.Hq, p.Hkv, HD, sizeof(T) == 2 ? KDA_DT_BF16 : KDA_DT_F32, p.max_pages,
+                                   p.weight_out != nullptr);
+    if (lay.items > 0x7fffffff) return cudaErrorInvalidValue;
+    cudaError_t e;
+    if (lay.MT == 0) e = launch_tc(p, lay, HD, st);
+    else if (lay.NB == 1) e = launch_main<T, HD, 1, 1>(p, lay, st);
+    else if (lay.MT == 1) e = launch_main<T, HD, 2, 1>(p, lay, st);
+    else if (lay.MT == 2) e = launch_main<T, HD, 2, 2>(p, lay, st);
+    else e = launch_main<T, HD, 2, 4>(p, lay, st);
+    if (e != cudaSuccess || p.max_pages == 0) return e;
+    int64_t rows = kJoinBlocks / lay.items;
+    rows = rows < 1 ? 1 : rows > lay.PR ? lay.PR : rows;
+    const dim3 grid((unsigned)lay.items, (unsigned)rows);
+    if (lay.workers > 8 * lay.items) e = launch_after(join_kernel<T, HD, 512>, grid, 512, st, p, lay);
+    else e = launch_after(join_kernel<T, HD, 128>, grid, 128, st, p, lay);
     if (e != cudaSuccess || p.weight_out == nullptr) return e;
     const int64_t blocks = (int64_t)p.batch * ((p.max_pages + 31) / 32);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     return launch_after(page_weight_kernel, dim3((unsigned)blocks), 256, st, p, lay);
 }
 
-template <typename T, int HD>
-cudaError_t launch_rows(const AttnDecodeParams &p, cudaStream_t st) {
-    const int rows = p.D * p.G;
-    if (rows <= 8) return launch<T, HD, 1, 1>(p, st);
-    switch (tile_mt(rows)) {
-        case 1: return launch<T, HD, 2, 1>(p, st);
-        case 2: return launch<T, HD, 2, 2>(p, st);
-        default: return launch<T, HD, 2, 4>(p, st);
-    }
-}
-
 template <typename T>
 cudaError_t launch_dim(const AttnDecodeParams &p, int d, cudaStream_t st) {
-    if (d == 128) return launch_rows<T, 128>(p, st);
-    if (d == 64) return launch_rows<T, 64>(p, st);
-    return launch_rows<T, 32>(p, st);
+    if (d == 128) return launch<T, 128>(p, st);
+    if (d == 64) return launch<T, 64>(p, st);
+    return launch<T, 32>(p, st);
 }
 
 }  // namespace
 
+namespace dec {
+
+Layout make_layout(int64_t batch, int D, int Hq, int Hkv, int d, int dtype, int64_t max_pages, bool with_weight) {
+    auto align64 = [](int64_t x) { return (x + 63) / 64 * 64; };
+    const int rows = D * (Hq / Hkv);
+    Layout l{};
+    if (dtype == KDA_DT_BF16 && d >= 64 && rows > 16) {
+        l.R = 128;
+    } else {
+        l.NB = rows <= 8 ? 1 : 2;
+        l.MT = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+        l.R = 8 * l.NB * l.MT;
+    }
+    l.RB = (rows + l.R - 1) / l.R;
+    l.PR = rows < l.R ? rows : l.R;
+    l.items = batch * Hkv * l.RB;
+    // all places on the GPU once, or as many whole times as leave a worker kPagesPerWorker pages
+    const int64_t units = l.items * max_pages, places = l.MT == 0 ? kSms : (int64_t)kSms * warps_per_sm(l.NB) / l.MT;
+    int64_t rounds = l.MT == 0 ? 1 : units / (places * kPagesPerWorker);
+    rounds = rounds < 1 ? 1 : rounds > kRounds ? kRounds : rounds;
+    l.workers = places * rounds < units ? places * rounds : units;
+    if (l.workers < 1) l.workers = 1;
+    l.desc = 0;
+    l.part_m = align64(2 * l.items);
+    l.part_l = l.part_m + align64(2 * l.workers * l.PR);
+    l.part_o = l.part_l + align64(2 * l.workers * l.PR);
+    l.lse2 = l.part_o + align64(2 * l.workers * l.PR * d);
+    l.page_w = l.lse2 + (with_weight ? align64(batch * D * Hq) : 0);
+    l.total = l.page_w + (with_weight ? align64(batch * D * Hq * max_pages) : 0);
+    return l;
+}
+
+}  // namespace dec
+
 size_t attn_decode_workspace_bytes(int Hq, int Hkv, int d, int dtype, int64_t batch, int D, int64_t max_pages,
                                    bool with_weight) {
-    (void)dtype;
     if (batch <= 0) return 0;
-    return (size_t)make_layout(batch, D, Hq, Hkv, d, max_pages, with_weight).total * 4;
+    return (size_t)make_layout(batch, D, Hq, Hkv, d, dtype, max_pages, with_weight).total * 4;
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeParams &p, int d, int dtype, cudaStream_t st) {

@@ -1,0 +1,193 @@
+// What the two cache attention kernels (kda_attn_decode.cu, kda_attn_decode_tc.cu)
+// share: how the batch's pages are cut into workers' ranges, the workspace, and
+// small conversions.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "kda_attn_internal.h"
+#include "kda_bulk.cuh"
+
+namespace kda {
+namespace dec {
+
+constexpr int kSms = 152;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// How a call is run, and its workspace, in floats: for each item (sequence, kv
+// head, block of R rows) the workers of its first and last page (desc), the cut
+// items' partial results, two per worker (the range's first item, the range's
+// last item), then the rows' lse (base 2) and page weights where weights are
+// asked for.
+struct Layout {
+    int64_t desc, part_m, part_l, part_o, lse2, page_w, total;
+    int64_t items, workers;
+    int32_t R, RB, PR;  // rows of an item, row blocks, rows of a partial result
+    int32_t NB, MT;     // tiles of a worker of kda_attn_decode.cu; MT = 0: kda_attn_decode_tc.cu
+};
+
+Layout make_layout(int64_t batch, int D, int Hq, int Hkv, int d, int dtype, int64_t max_pages, bool with_weight);
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four e4m3 bytes as two pairs of fp16 (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t u) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, float a, float b) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(a, b);
+}
+
+__device__ __forceinline__ int pages_of(const AttnDecodeParams &p, int n, int &len) {
+    const int cap = p.max_pages * kPage;
+    len = p.seq_lens[n];
+    len = len < 0 ? 0 : len > cap ? cap : len;
+    return (len + kPage - 1) / kPage;
+}
+
+// Where a unit (one page of one item) lies: sequence n with its first unit at
+// `base`, item hr = kv head * row blocks + row block, page index.
+struct Cursor {
+    int n;
+    int64_t base;
+};
+
+// What a worker needs to know of a page: its block in the cache (page * Hkv +
+// kv head; -1: none) and the scales.
+struct PageMeta {
+    int block;
+    float ks, vs;
+};
+constexpr int kMeta = 64;  // entries per worker: two batches of 32 units
+
+struct Unit {
+    int n, hr, page, pages, len;
+};
+
+// Moves the cursor to the sequence that holds unit u >= cursor.base.
+__device__ __forceinline__ Unit locate(const AttnDecodeParams &p, int HR, Cursor &c, int64_t u) {
+    Unit r;
+    while (true) {
+        r.pages = pages_of(p, c.n, r.len);
+        const int64_t end = c.base + (int64_t)r.pages * HR;
+        if (u < end || c.n + 1 >= p.batch) break;
+        c.base = end;
+        ++c.n;
+    }
+    const int64_t rem = u - c.base;
+    r.n = c.n;
+    r.hr = r.pages > 0 ? (int)(rem / r.pages) : 0;
+    r.page = r.pages > 0 ? (int)(rem - (int64_t)r.hr * r.pages) : 0;
+    return r;
+}
+
+// Clears the bytes of a value word (positions pos..pos + 3 of the page) from
+// `left` on, and the NaN bytes from `seen` on; the first of the latter, or kPage.
+__device__ __forceinline__ int mask_word(uint32_t &w, int pos, int left, int seen) {
+    int at = kPage;
+#pragma unroll
+    for (int b = 3; b >= 0; --b) {
+        const bool nan = ((w >> (8 * b)) & 0x7fu) == 0x7fu;
+        if (pos + b >= left) {
+            w &= ~(0xffu << (8 * b));
+        } else if (nan && pos + b >= seen) {
+            w &= ~(0xffu << (8 * b));
+            at = pos + b;
+        }
+    }
+    return at;
+}
+
+// Finds the range [u0, u1) of worker blockIdx.x among the batch's U units and
+// the cursor of its start (in shared memory, after the call's barrier; unset
+// for an empty range).  W: the workers with a range, no more than units.  Also
+// writes the rows of sequences without pages, which have no unit.
+template <typename T, int HD, int WARPS>
+__device__ __forceinline__ void find_range(const AttnDecodeParams &p, int HR, int64_t *warp_sum, Cursor *start, int64_t &U,
+                                           int64_t &W, int64_t &u0, int64_t &u1) {
+    constexpr int kThreads = 32 * WARPS;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t w = blockIdx.x;
+    const int per = (p.batch + kThreads - 1) / kThreads;
+    const int nb = min(tid * per, p.batch), ne = min(nb + per, p.batch);
+    int64_t mine = 0;
+    for (int n = nb; n < ne; ++n) {
+        int len;
+        mine += (int64_t)pages_of(p, n, len) * HR;
+        if (w == 0 && p.err_flag && p.seq_lens[n] > p.max_pages * kPage) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += x;
+    }
+    U = __shfl_sync(~0u, incl, 31);
+    int64_t excl = incl - mine;
+    if constexpr (WARPS > 1) {
+        if (lane == 31) warp_sum[warp] = incl;
+        __syncthreads();
+        U = 0;
+        for (int i = 0; i < WARPS; ++i) {
+            if (i < warp) excl += warp_sum[i];
+            U += warp_sum[i];
+        }
+    }
+    W = min((int64_t)gridDim.x, max(U, (int64_t)1));
+    u0 = w < W ? U * w / W : 0;
+    u1 = w < W ? U * (w + 1) / W : 0;
+    if (mine > 0 && u0 >= excl && u0 < excl + mine) {
+        Cursor c{nb, excl};
+        locate(p, HR, c, u0);
+        *start = c;
+    }
+    for (int n = blockIdx.x; n < p.batch; n += gridDim.x) {
+        if (p.seq_lens[n] > 0 && p.max_pages > 0) continue;
+        T *o = static_cast<T *>(p.out) + (int64_t)n * p.D * p.Hq * HD;
+        for (int64_t i = tid; i < (int64_t)p.D * p.Hq * HD / 2; i += kThreads) store2(o + 2 * i, 0.f, 0.f);
+        for (int i = tid; i < p.D * p.Hq; i += kThreads) {
+            if (p.lse) p.lse[(int64_t)n * p.D * p.Hq + i] = -INFINITY;
+        }
+    }
+    __syncthreads();
+}
+
+// The worker's entry for an item whose first page it holds: the join adds up
+// the parts of workers w..last.
+__device__ __forceinline__ void write_desc(float *ws, const Layout &lay, const Unit &un, const Cursor &c, int HR, bool whole,
+                                           int64_t W, int64_t U) {
+    const int64_t end = c.base + (int64_t)(un.hr + 1) * un.pages;  // one past the item's last unit
+    const int w = (int)blockIdx.x;
+    *reinterpret_cast<int2 *>(ws + lay.desc + 2 * ((int64_t)un.n * HR + un.hr)) =
+        make_int2(w, whole ? w : (int)((end * W + U - 1) / U - 1));  // the worker of its last unit
+}
+
+// Many rows on tcgen05 (bf16, d = 64 or 128).
+cudaError_t launch_tc(const AttnDecodeParams &p, const Layout &lay, int d, cudaStream_t st);
+
+}  // namespace dec
+}  // namespace kda

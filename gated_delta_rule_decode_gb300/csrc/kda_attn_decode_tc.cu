@@ -1,0 +1,618 @@
+// Attention of many query rows per sequence over the 8-bit paged cache, on
+// tcgen05: draft windows of grouped heads (more than 16 rows of a kv head).
+//
+// Up to 128 rows (window tokens x grouped heads) are the 128 lanes of one
+// product, so a page is read once for all of them; the work is cut into
+// workers' ranges as in kda_attn_decode.cu, one worker per SM.  Tiles are two
+// pages (128 positions) of one item:
+//
+//   S = Q K^T (128 x 128),  P = e^{S - m},  O += P V
+//
+// A page comes as bytes by bulk copies and is turned into fp16 operands (exact)
+// by six warps: both pages' rows lie as the K-major 128-byte-swizzled operand
+// wants them (keys by channel, the value layout by position).  Roles:
+//
+//   warps 0-3   softmax: thread = row; scores read from tensor memory, weights
+//               written back as fp16, O rescaled when the maximum moves
+//   warp 4      issues QK(j + 1), then PV(j)
+//   warp 5      looks up pages, issues the copies (a ring of page slots)
+//   warps 6-11  conversion; the query rows at an item's start
+//
+// The query rows are scaled by powers of two into fp16's range (exact for
+// bf16), the weights by 2^7 (the maximum is only moved when it grows by more
+// than 2^8, so they reach 2^15).  Value scales are powers of two and go into
+// the exponent of the weights, relative to the largest so far.
+//
+// Bound by HBM for long contexts; per tile the products take 1024 cycles of an
+// SM, the bytes 1400.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "kda_attn_decode.cuh"
+#include "kda_attn_internal.h"
+#include "kda_bulk.cuh"
+#include "kda_tc.cuh"
+
+namespace kda {
+namespace {
+
+using namespace dec;
+
+constexpr int kWarps = 12, kThreads = kWarps * 32;
+constexpr int kConvWarps = 6, kConv = kConvWarps * 32;
+constexpr int kMeta = 64;
+constexpr uint32_t kTmem = 512;
+constexpr float kLazy = 8.f;
+constexpr int kBias = 7;  // log2 of the weights' fp16 scale
+
+template <int HD>
+struct Cfg {
+    static constexpr int kHalf = HD * kPage;          // bytes of a page's keys (or values)
+    static constexpr int kSlots = HD == 128 ? 4 : 8;  // pages in the ring
+    static constexpr int kOp = 128 * HD * 2;          // an fp16 operand of 128 rows of HD, or HD rows of 128
+    static constexpr int kRing = kSlots * 2 * kHalf;
+    static constexpr int kBytes = 1024 + kRing + 5 * kOp;  // Q, K and V twice
+    static constexpr int kO = 256;                     // tensor memory column of O; S at 0 and 128
+};
+
+struct Bars {
+    uint64_t full[8], empty[8];                        // ring
+    uint64_t k_ready[2], k_free[2], v_ready[2], v_free[2];
+    uint64_t s_full[2], p_full[2], pv_done, o_free, drain;
+};
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, int phase, volatile int *abort_flag) {
+    for (uint32_t it = 0; it < kWaitLimit; ++it) {
+        if (mbar_try_wait(bar, (uint32_t)phase & 1u)) return true;
+        if ((it & 255u) == 255u && *abort_flag) return false;
+    }
+    *abort_flag = 1;
+    return false;
+}
+
+// The worker's range as tiles: each role walks them by itself, in the same order.
+struct Walk {
+    Cursor cur;
+    int64_t u0;            // first unit
+    int i, count;          // units done, units
+    Unit un;               // of the item at hand
+    int left;              // its pages that are left in the range
+    bool first, last;      // of the item (within the range), for the tile at hand
+    int pages;             // of the tile: 1 or 2
+    int page0;             // the item's first page in the range
+    int item, tile;        // counted from 0 within the range
+
+    __device__ __forceinline__ void begin(const Cursor &c, int64_t u, int n) {
+        cur = c; u0 = u; count = n; i = 0; left = 0; item = -1; tile = -1; pages = 0;
+    }
+    // Moves to the next tile; un.page is its first page.
+    __device__ __forceinline__ bool next(const AttnDecodeParams &p, int HR) {
+        i += pages;
+        if (i >= count) return false;
+        if (left == 0) {
+            un = locate(p, HR, cur, u0 + i);
+            left = min(un.pages - un.page, count - i);
+            first = true;
+            page0 = un.page;
+            ++item;
+        } else {
+            un.page += pages;
+            first = false;
+        }
+        pages = left >= 2 ? 2 : 1;
+        left -= pages;
+        last = left == 0;
+        ++tile;
+        return true;
+    }
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnDecodeParams p, const Layout lay) {
+    using C = Cfg<HD>;
+    using T = __nv_bfloat16;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sq = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char *sk = sq + C::kOp, *sv = sk + 2 * C::kOp, *ring = sv + 2 * C::kOp;
+    __shared__ Bars bars;
+    __shared__ PageMeta meta[kMeta];
+    __shared__ int8_t q_exp[2][128];  // exponents of the rows' scales, by item
+    __shared__ int64_t warp_sum[kWarps];
+    __shared__ Cursor start;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    __shared__ volatile int v_nan;  // a NaN was set aside in some item's window
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rows_all = p.D * p.G, RB = lay.RB, HR = p.Hkv * RB;
+    float *ws = static_cast<float *>(p.workspace);
+
+    if (tid == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.empty[i], kConvWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.k_ready[i], kConvWarps);
+            mbar_init(&bars.v_ready[i], kConvWarps);
+            mbar_init(&bars.k_free[i], 1);
+            mbar_init(&bars.v_free[i], 1);
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.p_full[i], 4);
+        }
+        mbar_init(&bars.pv_done, 1);
+        mbar_init(&bars.o_free, 4);
+        mbar_init(&bars.drain, 1);
+        fence_barrier_init();
+        abort_flag = 0;
+        v_nan = 0;
+    }
+    int64_t U, W, u0, u1;
+    find_range<T, HD, kWarps>(p, HR, warp_sum, &start, U, W, u0, u1);
+    if (u0 >= u1) return;
+    if (warp == 4) tc::tmem_alloc(&tmem_base, kTmem);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = tmem_base;
+    const int count = (int)(u1 - u0);
+    Walk wk;
+    wk.begin(start, u0, count);
+
+    if (warp == 5) {
+        // ---------------- page look-up (32 units at a time, one per lane) and copies
+        Cursor fetch_cur = start;
+        int fetched = 0, issued = 0;
+        for (int i = 0; i < count; ++i) {
+            const int slot = i % C::kSlots;
+            if (i >= C::kSlots && !__all_sync(~0u, wait_or_abort(&bars.empty[slot], i / C::kSlots - 1, &abort_flag))) break;
+            if (i >= fetched) {
+                Cursor c = fetch_cur;
+                if (fetched + lane < count) {
+                    const Unit un = locate(p, HR, c, u0 + fetched + lane);
+                    const int h = un.hr / RB;
+                    const int id = p.block_table[(int64_t)un.n * p.max_pages + un.page];
+                    PageMeta e{-1, 0.f, 0.f};
+                    if (id >= 0 && id < p.num_pages) {
+                        e.block = id * p.Hkv + h;
+                        e.ks = p.k_scale[e.block];
+                        e.vs = p.v_scale[e.block];
+                    } else if (p.err_flag) {
+                        atomicOr(p.err_flag, KDA_DEVERR_PAGE);
+                    }
+                    meta[(fetched + lane) % kMeta] = e;
+                }
+                const int from = min(31, count - 1 - fetched);
+                fetch_cur.n = __shfl_sync(~0u, c.n, from);
+                fetch_cur.base = __shfl_sync(~0u, c.base, from);
+                fetched += 32;
+                __syncwarp();
+            }
+            issued = i + 1;
+            if (lane == 0) {
+                const int block = meta[i % kMeta].block;
+                if (block < 0) {
+                    mbar_arrive(&bars.full[slot]);
+                } else {
+                    unsigned char *dst = ring + slot * 2 * C::kHalf;
+                    mbar_arrive_expect_tx(&bars.full[slot], 2 * C::kHalf);
+                    bulk_g2s(dst, p.k_pages + (int64_t)block * C::kHalf, C::kHalf, &bars.full[slot]);
+                    bulk_g2s(dst + C::kHalf, p.v_pages + (int64_t)block * C::kHalf, C::kHalf, &bars.full[slot]);
+                }
+            }
+        }
+        // every copy lands before the CTA's memory goes
+        for (int i = max(0, issued - C::kSlots); i < issued; ++i)
+            mbar_wait_drain(&bars.full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1u);
+    } else if (warp == 4) {
+        // ---------------- products
+        if (lane == 0) {
+            const uint32_t id_qk = tc::idesc_f16(128, 128), id_pv = tc::idesc_f16(128, HD);
+            const uint32_t qa = tc::smem_u32(sq);
+            auto pv = [&](int j, bool first, int item) {
+                const int b = j & 1;
+                if (!wait_or_abort(&bars.p_full[b], j >> 1, &abort_flag) ||
+                    !wait_or_abort(&bars.v_ready[b], j >> 1, &abort_flag))
+                    return false;
+                if (first && item > 0 && !wait_or_abort(&bars.o_free, item - 1, &abort_flag)) return false;
+                tc::fence_after_sync();
+                const uint32_t va = tc::smem_u32(sv + b * C::kOp);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)  // 16 positions each; a page is one 128-byte-wide chunk of HD rows
+                    tc::mma_f16_ts(tm + C::kO, tm + 128 * b + 8 * ks,
+                                   tc::desc_sw128(va + (uint32_t)((ks >> 2) * HD * 128 + (ks & 3) * 32)), id_pv,
+                                   (first && ks == 0) ? 0u : 1u);
+                tc::commit(&bars.v_free[b]);
+                tc::commit(&bars.pv_done);
+                return true;
+            };
+            bool ok = true, pfirst = false;
+            int pitem = 0;
+            while (ok && wk.next(p, HR)) {
+                const int j = wk.tile;
+                const int b = j & 1;
+                ok = wait_or_abort(&bars.k_ready[b], j >> 1, &abort_flag);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint32_t ka = tc::smem_u32(sk + b * C::kOp);
+#pragma unroll
+                for (int ks = 0; ks < HD / 16; ++ks)
+                    tc::mma_f16_ss(tm + 128 * b, tc::desc_tf32_kstep(qa, 128, ks), tc::desc_tf32_kstep(ka, 128, ks), id_qk,
+                                   ks > 0);
+                tc::commit(&bars.k_free[b]);
+                tc::commit(&bars.s_full[b]);
+                if (j > 0) ok = pv(j - 1, pfirst, pitem);
+                pfirst = wk.first;
+                pitem = wk.item;
+            }
+            if (ok) pv(wk.tile, pfirst, pitem);
+            tc::commit(&bars.drain);  // every product is done before the memory goes
+            mbar_wait_drain(&bars.drain, 0);
+        }
+    } else if (warp >= 6) {
+        // ---------------- conversion
+        const int ct = tid - 6 * 32;  // 0..kConv - 1
+        bool ok = true;
+        while (ok && wk.next(p, HR)) {
+            const int j = wk.tile;
+            const int b = j & 1;
+            // the buffers' last readers: QK(j - 2) and PV(j - 2)
+            if (j >= 2) {
+                ok = __all_sync(~0u, wait_or_abort(&bars.k_free[b], (j >> 1) - 1, &abort_flag) &&
+                                         wait_or_abort(&bars.v_free[b], (j >> 1) - 1, &abort_flag));
+                if (!ok) break;
+            }
+            if (wk.first) {
+                // the query rows: the last product of the item before has read its own
+                if (j >= 1) {
+                    ok = __all_sync(~0u, wait_or_abort(&bars.k_free[b ^ 1], (j - 1) >> 1, &abort_flag));
+                    if (!ok) break;
+                }
+                const int h = wk.un.hr / RB;
+#pragma unroll 1
+                for (int x = ct; x < 256; x += kConv) {
+                    const int r = x >> 1, half = x & 1;  // two threads per row
+                    const int row = (wk.un.hr % RB) * 128 + r;
+                    const bool valid = row < rows_all;
+                    const int tok = valid ? row / p.G : 0, gi = valid ? row - tok * p.G : 0;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        static_cast<const T *>(p.q) + ((int64_t)wk.un.n * p.D + tok) * p.q_stride + (int64_t)(h * p.G + gi) * HD +
+                        half * (HD / 2));
+                    uint4 raw[HD / 16];
+                    float amax = 0.f;
+#pragma unroll
+                    for (int u = 0; u < HD / 16; ++u) {
+                        raw[u] = valid ? src[u] : make_uint4(0, 0, 0, 0);
+                        const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+                    }
+                    amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));  // (256 is whole warps of x)
+                    int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+                    ex = ex < -100 ? -100 : ex > 126 ? 126 : ex;
+                    const float mul = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+                    if (half == 0) q_exp[wk.item & 1][r] = (int8_t)ex;
+#pragma unroll
+                    for (int u = 0; u < HD / 16; ++u) {
+                        const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            y[e] = pack_f16(__uint_as_float(w[e] << 16) * mul, __uint_as_float(w[e] & 0xffff0000u) * mul);
+                        *reinterpret_cast<uint4 *>(sq + tc::sw128_off16(r, half * (HD / 2) + 8 * u, 128)) =
+                            make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+            }
+            // keys: 16 channels of a position at a time
+#pragma unroll 1
+            for (int pg = 0; pg < wk.pages; ++pg) {
+                const int i = wk.i + pg;
+                const int slot = i % C::kSlots;
+                ok = __all_sync(~0u, wait_or_abort(&bars.full[slot], i / C::kSlots, &abort_flag));
+                if (!ok) break;
+                const unsigned char *kb = ring + slot * 2 * C::kHalf;
+                constexpr int PR = HD / 16;  // pieces per position
+#pragma unroll
+                for (int x = ct; x < kPage * PR; x += kConv) {
+                    const int r = x / PR, u = x % PR;
+                    const uint4 a = *reinterpret_cast<const uint4 *>(kb + 16 * x);
+                    uint4 y0, y1;
+                    e4m3x4_to_f16(a.x, y0.x, y0.y);
+                    e4m3x4_to_f16(a.y, y0.z, y0.w);
+                    e4m3x4_to_f16(a.z, y1.x, y1.y);
+                    e4m3x4_to_f16(a.w, y1.z, y1.w);
+                    unsigned char *dst = sk + b * C::kOp;
+                    const uint32_t o0 = tc::sw128_off16(64 * pg + r, 16 * u, 128), o1 = tc::sw128_off16(64 * pg + r, 16 * u + 8, 128);
+                    // the two halves of a row in either order, so that eight lanes write eight 16-byte banks
+                    const bool sw = (u & 4) != 0;
+                    *reinterpret_cast<uint4 *>(dst + (sw ? o1 : o0)) = sw ? y1 : y0;
+                    *reinterpret_cast<uint4 *>(dst + (sw ? o0 : o1)) = sw ? y0 : y1;
+                }
+            }
+            if (!ok) break;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.k_ready[b]);
+            // values: 16 positions of a channel at a time
+            const int window0 = wk.un.len - p.D + 1;
+#pragma unroll 1
+            for (int pg = 0; pg < 2; ++pg) {
+                unsigned char *dst = sv + b * C::kOp + pg * HD * 128;
+                const int i = wk.i + pg;
+                const int slot = i % C::kSlots;
+                const bool have = pg < wk.pages && meta[i % kMeta].block >= 0;
+                const unsigned char *vb = ring + slot * 2 * C::kHalf + C::kHalf;
+                const int pos0 = (wk.un.page + pg) * kPage;
+                const bool tail = pos0 + kPage > window0;
+#pragma unroll
+                for (int x = ct; x < HD * 4; x += kConv) {
+                    const int r = x >> 2, u = x & 3;
+                    uint4 a = make_uint4(0, 0, 0, 0);
+                    if (have) {
+                        a = *reinterpret_cast<const uint4 *>(vb + 16 * x);
+                        if (tail) {  // bytes past the end, and the window's NaN bytes, count as zero
+                            const int left = wk.un.len - pos0, seen = window0 - pos0;
+                            int at = min(min(mask_word(a.x, 16 * u, left, seen), mask_word(a.y, 16 * u + 4, left, seen)),
+                                         min(mask_word(a.z, 16 * u + 8, left, seen), mask_word(a.w, 16 * u + 12, left, seen)));
+                            if (at < kPage) v_nan = 1;
+                        }
+                    }
+                    uint4 y0, y1;
+                    e4m3x4_to_f16(a.x, y0.x, y0.y);
+                    e4m3x4_to_f16(a.y, y0.z, y0.w);
+                    e4m3x4_to_f16(a.z, y1.x, y1.y);
+                    e4m3x4_to_f16(a.w, y1.z, y1.w);
+                    *reinterpret_cast<uint4 *>(dst + tc::sw128_off16(r, 16 * u, HD)) = y0;
+                    *reinterpret_cast<uint4 *>(dst + tc::sw128_off16(r, 16 * u + 8, HD)) = y1;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars.v_ready[b]);
+                for (int pg = 0; pg < wk.pages; ++pg) mbar_arrive(&bars.empty[(wk.i + pg) % C::kSlots]);
+            }
+        }
+    } else {
+        // ---------------- softmax: thread = row
+        // Every warp waits for every PV (of the tile before, before it gives the
+        // tile's weights): QK(j) is issued before PV(j - 1), so that a wait by parity
+        // for a later one alone could take an older for it.
+        const uint32_t o_addr = tc::lane_addr(tm, warp, C::kO);
+        float m = -INFINITY, l = 0.f, qs = 0.f, vref = 0.f;
+        int limit = 0;
+        bool valid = false, ok = true;
+        int64_t qrow = 0;
+        while (ok && wk.next(p, HR)) {
+            const int j = wk.tile;
+            const int b = j & 1;
+            const uint32_t s_addr = tc::lane_addr(tm, warp, 128 * b);
+            const Unit &un = wk.un;
+            const int rb = un.hr % RB, h = un.hr / RB, row = rb * 128 + tid;
+            const bool active = rb * 128 + warp * 32 < rows_all;  // some row of this warp exists
+            ok = __all_sync(~0u, wait_or_abort(&bars.s_full[b], j >> 1, &abort_flag));
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (wk.first) {
+                valid = row < rows_all;
+                limit = valid ? un.len - p.D + 1 + row / p.G : 0;
+                qrow = valid ? ((int64_t)un.n * p.D + row / p.G) * p.Hq + h * p.G + row % p.G : 0;
+                qs = __uint_as_float((uint32_t)(127 - 14 + q_exp[wk.item & 1][tid]) << 23) * p.scale * kLog2e;
+                m = -INFINITY;
+                l = 0.f;
+                vref = 0.f;
+            }
+            if (active) {
+                // per page: factor of the raw scores, exponent bias of the weights
+                float f[2], bias[2], unbias[2];
+                bool have[2];
+                float vnew = vref;
+#pragma unroll
+                for (int pg = 0; pg < 2; ++pg) {
+                    const PageMeta e = meta[(wk.i + pg) % kMeta];
+                    have[pg] = pg < wk.pages && e.block >= 0;
+                    f[pg] = have[pg] ? fmaxf(qs * e.ks, 1e-37f) : 1.f;
+                    bias[pg] = have[pg] ? e.vs : 0.f;
+                    vnew = fmaxf(vnew, bias[pg]);
+                }
+                bool apart = false;
+#pragma unroll
+                for (int pg = 0; pg < 2; ++pg) {
+                    const float ratio = have[pg] ? bias[pg] / vnew : 1.f;
+                    const int e = kBias + (int)(__float_as_uint(ratio) >> 23) - 127;
+                    apart |= e < -45;
+                    bias[pg] = (float)e;
+                    unbias[pg] = __uint_as_float((uint32_t)(127 - (e < -100 ? -100 : e)) << 23);
+                }
+                const float vfix = vref > 0.f ? vref / vnew : 1.f;
+                vref = vnew;
+                const int pos0 = un.page * kPage;
+                const bool masked = pos0 + 2 * kPage > un.len - p.D + 1 || !have[0] || !have[1];
+                const int end = limit - pos0;  // columns that the row sees, of pages that exist
+                auto scores = [&](int pg, float(&x)[2][32]) {
+                    tc::ld32(s_addr + 64 * pg, x[0]);
+                    tc::ld32(s_addr + 64 * pg + 32, x[1]);
+                    tc::wait_ld();
+                    if (masked) {
+                        const int e = have[pg] ? end - 64 * pg : 0;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (32 * i + c >= e) x[i][c] = -INFINITY;
+                    }
+                };
+                // (read twice: the maximum first, then the weights)
+                float mx = -INFINITY;
+#pragma unroll
+                for (int pg = 0; pg < 2; ++pg) {
+                    float x[2][32], part[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    scores(pg, x);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        part[0] = fmaxf(part[0], x[0][c]);
+                        part[1] = fmaxf(part[1], x[0][c + 1]);
+                        part[2] = fmaxf(part[2], x[1][c]);
+                        part[3] = fmaxf(part[3], x[1][c + 1]);
+                    }
+                    mx = fmaxf(mx, fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])) * f[pg]);
+                }
+                const float mnew = fmaxf(m, mx);
+                float fix = vfix;
+                if (wk.first) {
+                    m = mnew;
+                } else if (mnew - m > kLazy || (m == -INFINITY && mnew > m)) {
+                    const float al = ex2(m - mnew);
+                    fix *= al;
+                    l *= al;
+                    m = mnew;
+                }
+                if (j > 0) ok = __all_sync(~0u, wait_or_abort(&bars.pv_done, j - 1, &abort_flag));
+                if (!ok) break;
+                if (__any_sync(~0u, !wk.first && fix != 1.f)) {
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < HD; c += 16) {
+                        float o[16];
+                        tc::ld16(o_addr + c, o);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= fix;
+                        tc::st16(o_addr + c, o);
+                    }
+                    tc::wait_st();
+                }
+                const float use = m == -INFINITY ? 0.f : m;
+                float rs[2] = {0.f, 0.f};
+#pragma unroll
+                for (int pg = 0; pg < 2; ++pg) {
+                    const float k = f[pg], z = bias[pg] - use;
+                    float x[2][32];
+                    scores(pg, x);
+                    if (apart) {  // these weights may vanish next to a larger value scale: their sum apart
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) rs[pg] += ex2(fmaf(x[i][c], k, -use));
+                    }
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const float x0 = ex2(fmaf(x[i][2 * c], k, z)), x1 = ex2(fmaf(x[i][2 * c + 1], k, z));
+                            sum[2 * (c & 1)] += x0;
+                            sum[2 * (c & 1) + 1] += x1;
+                            pk[c] = pack_f16(x0, x1);
+                        }
+                        tc::st16u(s_addr + 32 * pg + 16 * i, pk);
+                    }
+                    if (!apart) rs[pg] = ((sum[0] + sum[2]) + (sum[1] + sum[3])) * unbias[pg];
+                }
+                tc::wait_st();
+                l += rs[0] + rs[1];
+                if (p.weight_out != nullptr && valid) {
+#pragma unroll
+                    for (int pg = 0; pg < 2; ++pg)
+                        if (pg < wk.pages)
+                            ws[lay.page_w + qrow * p.max_pages + un.page + pg] = rs[pg] > 0.f ? log2f(rs[pg]) + use : -INFINITY;
+                }
+            } else {
+                if (j > 0) ok = __all_sync(~0u, wait_or_abort(&bars.pv_done, j - 1, &abort_flag));
+                if (!ok) break;
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.p_full[b]);
+            if (!wk.last) continue;
+
+            // ---- the item's end
+            ok = __all_sync(~0u, wait_or_abort(&bars.pv_done, j, &abort_flag));
+            if (!ok) break;
+            tc::fence_after_sync();
+            const bool from_start = wk.page0 == 0;
+            const bool whole = from_start && un.page + wk.pages == un.pages;
+            const float unit = vref * (1.f / (float)(1 << kBias));
+            if (active) {
+                const float fo = whole ? (l == 0.f ? 0.f : unit / l) : unit;
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (from_start ? 1 : 0);
+                T *dst = static_cast<T *>(p.out) + qrow * HD;
+                float *part = ws + lay.part_o + (slot * lay.PR + tid) * HD;
+                const bool nan = v_nan != 0;
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 16) {
+                    float o[16];
+                    tc::ld16(o_addr + c, o);
+                    tc::wait_ld();
+                    if (!valid) continue;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = fo == 0.f ? 0.f : o[e] * fo;
+                    if (nan) {  // the NaN values that this row sees
+                        for (int pos = max(un.len - p.D + 1, 0); pos < limit; ++pos) {
+                            const int id = p.block_table[(int64_t)un.n * p.max_pages + pos / kPage];
+                            if (id < 0 || id >= p.num_pages) continue;
+                            const unsigned char *vb = p.v_pages + ((int64_t)id * p.Hkv + h) * C::kHalf + pos % kPage;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if ((vb[(c + e) * kPage] & 0x7f) == 0x7f) o[e] = NAN;
+                        }
+                    }
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 8)
+                            *reinterpret_cast<uint4 *>(dst + c + e) =
+                                make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]),
+                                           pack_bf16(o[e + 4], o[e + 5]), pack_bf16(o[e + 6], o[e + 7]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<float4 *>(part + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+                if (valid) {
+                    if (whole) {
+                        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+                        if (p.lse) p.lse[qrow] = lse2 * kLn2;
+                        if (p.weight_out) ws[lay.lse2 + qrow] = lse2;
+                    } else {
+                        ws[lay.part_m + slot * lay.PR + tid] = m;
+                        ws[lay.part_l + slot * lay.PR + tid] = l;
+                    }
+                }
+            }
+            if (from_start && tid == 0) write_desc(ws, lay, un, wk.cur, HR, whole, W, U);
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.o_free);
+        }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 4) tc::tmem_dealloc(tm, kTmem);
+    if (tid == 0 && abort_flag && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_TIMEOUT);
+}
+
+template <int HD>
+cudaError_t launch_dim(const AttnDecodeParams &p, const Layout &lay, cudaStream_t st) {
+    auto kern = decode_attn_tc_kernel<HD>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), Cfg<HD>::kBytes, done);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)lay.workers, kThreads, Cfg<HD>::kBytes, st>>>(p, lay);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+namespace dec {
+
+cudaError_t launch_tc(const AttnDecodeParams &p, const Layout &lay, int d, cudaStream_t st) {
+    return d == 128 ? launch_dim<128>(p, lay, st) : launch_dim<64>(p, lay, st);
+}
+
+}  // namespace dec
+}  // namespace kda
