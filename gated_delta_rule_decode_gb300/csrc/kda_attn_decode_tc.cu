@@ -9,14 +9,15 @@
 //   S = Q K^T (128 x 128),  P = e^{S - m},  O += P V
 //
 // A page comes as bytes by bulk copies and is turned into fp16 operands (exact)
-// by six warps: both pages' rows lie as the K-major 128-byte-swizzled operand
+// by eight warps: both pages' rows lie as the K-major 128-byte-swizzled operand
 // wants them (keys by channel, the value layout by position).  Roles:
 //
-//   warps 0-3   softmax: thread = row; scores read from tensor memory, weights
-//               written back as fp16, O rescaled when the maximum moves
-//   warp 4      issues QK(j + 1), then PV(j)
-//   warp 5      looks up pages, issues the copies (a ring of page slots)
-//   warps 6-11  conversion; the query rows at an item's start
+//   warps 0-7    softmax: thread = row, warps 0-3 the tile's first page, 4-7 the
+//                second; scores read from tensor memory, weights written back as
+//                fp16, O rescaled when the maximum moves
+//   warp 8       issues QK(j + 1), then PV(j)
+//   warp 9       looks up pages, issues the copies (a ring of page slots)
+//   warps 10-17  conversion; the query rows at an item's start
 //
 // The query rows are scaled by powers of two into fp16's range (exact for
 // bf16), the weights by 2^7 (the maximum is only moved when it grows by more
@@ -39,9 +40,9 @@ namespace {
 
 using namespace dec;
 
-constexpr int kWarps = 12, kThreads = kWarps * 32;
-constexpr int kConvWarps = 6, kConv = kConvWarps * 32;
-constexpr int kMeta = 64;
+constexpr int kWarps = 18, kThreads = kWarps * 32;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvWarp = 10, kConvWarps = 8, kConv = kConvWarps * 32;
+constexpr int kBatch = 16, kMeta = 2 * kBatch;  // page look-ups at a time, and kept
 constexpr uint32_t kTmem = 512;
 constexpr float kLazy = 8.f;
 constexpr int kBias = 7;  // log2 of the weights' fp16 scale
@@ -53,7 +54,8 @@ struct Cfg {
     static constexpr int kOp = 128 * HD * 2;          // an fp16 operand of 128 rows of HD, or HD rows of 128
     static constexpr int kRing = kSlots * 2 * kHalf;
     static constexpr int kBytes = 1024 + kRing + 5 * kOp;  // Q, K and V twice
-    static constexpr int kO = 256;                     // tensor memory column of O; S at 0 and 128
+    static constexpr int kO = 256, kP = 384;           // tensor memory columns of O and of P; S at 0 and 128
+    static_assert(kSlots + 4 < kBatch, "copies run less than a batch ahead of the page data in use");
 };
 
 struct Bars {
@@ -69,6 +71,11 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, int phase, volatile
     }
     *abort_flag = 1;
     return false;
+}
+
+// All lanes of a warp, with one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, int phase, volatile int *abort_flag) {
+    return __all_sync(~0u, wait_or_abort(bar, phase, abort_flag));
 }
 
 // The worker's range as tiles: each role walks them by itself, in the same order.
@@ -118,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
     __shared__ Bars bars;
     __shared__ PageMeta meta[kMeta];
     __shared__ int8_t q_exp[2][128];  // exponents of the rows' scales, by item
-    __shared__ int64_t warp_sum[kWarps];
+    __shared__ int64_t exchange[128];  // the prologue's sums, then a float per (page, row)
     __shared__ Cursor start;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -138,19 +145,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
             mbar_init(&bars.k_free[i], 1);
             mbar_init(&bars.v_free[i], 1);
             mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], 4);
+            mbar_init(&bars.p_full[i], 8);
         }
         mbar_init(&bars.pv_done, 1);
-        mbar_init(&bars.o_free, 4);
+        mbar_init(&bars.o_free, 8);
         mbar_init(&bars.drain, 1);
         fence_barrier_init();
         abort_flag = 0;
         v_nan = 0;
     }
     int64_t U, W, u0, u1;
-    find_range<T, HD, kWarps>(p, HR, warp_sum, &start, U, W, u0, u1);
+    find_range<T, HD, kWarps>(p, HR, exchange, &start, U, W, u0, u1);
     if (u0 >= u1) return;
-    if (warp == 4) tc::tmem_alloc(&tmem_base, kTmem);
+    if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, kTmem);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -159,16 +166,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
     Walk wk;
     wk.begin(start, u0, count);
 
-    if (warp == 5) {
-        // ---------------- page look-up (32 units at a time, one per lane) and copies
+    if (warp == kLoadWarp) {
+        // ---------------- page look-up (kBatch units at a time, one per lane) and copies
         Cursor fetch_cur = start;
         int fetched = 0, issued = 0;
         for (int i = 0; i < count; ++i) {
             const int slot = i % C::kSlots;
-            if (i >= C::kSlots && !__all_sync(~0u, wait_or_abort(&bars.empty[slot], i / C::kSlots - 1, &abort_flag))) break;
+            if (i >= C::kSlots && !warp_wait(&bars.empty[slot], i / C::kSlots - 1, &abort_flag)) break;
             if (i >= fetched) {
                 Cursor c = fetch_cur;
-                if (fetched + lane < count) {
+                if (lane < kBatch && fetched + lane < count) {
                     const Unit un = locate(p, HR, c, u0 + fetched + lane);
                     const int h = un.hr / RB;
                     const int id = p.block_table[(int64_t)un.n * p.max_pages + un.page];
@@ -182,10 +189,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                     }
                     meta[(fetched + lane) % kMeta] = e;
                 }
-                const int from = min(31, count - 1 - fetched);
+                const int from = min(kBatch - 1, count - 1 - fetched);
                 fetch_cur.n = __shfl_sync(~0u, c.n, from);
                 fetch_cur.base = __shfl_sync(~0u, c.base, from);
-                fetched += 32;
+                fetched += kBatch;
                 __syncwarp();
             }
             issued = i + 1;
@@ -204,68 +211,65 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
         // every copy lands before the CTA's memory goes
         for (int i = max(0, issued - C::kSlots); i < issued; ++i)
             mbar_wait_drain(&bars.full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1u);
-    } else if (warp == 4) {
-        // ---------------- products
-        if (lane == 0) {
-            const uint32_t id_qk = tc::idesc_f16(128, 128), id_pv = tc::idesc_f16(128, HD);
-            const uint32_t qa = tc::smem_u32(sq);
-            auto pv = [&](int j, bool first, int item) {
-                const int b = j & 1;
-                if (!wait_or_abort(&bars.p_full[b], j >> 1, &abort_flag) ||
-                    !wait_or_abort(&bars.v_ready[b], j >> 1, &abort_flag))
-                    return false;
-                if (first && item > 0 && !wait_or_abort(&bars.o_free, item - 1, &abort_flag)) return false;
-                tc::fence_after_sync();
-                const uint32_t va = tc::smem_u32(sv + b * C::kOp);
+    } else if (warp == kMmaWarp) {
+        // ---------------- products (the whole warp in step: see mma_f16_ss_warp)
+        const uint32_t id_qk = tc::idesc_f16(128, 128), id_pv = tc::idesc_f16(128, HD);
+        const uint32_t qa = tc::smem_u32(sq);
+        auto pv = [&](int j, bool first, int item) {
+            const int b = j & 1;
+            if (!warp_wait(&bars.p_full[b], j >> 1, &abort_flag) ||
+                !warp_wait(&bars.v_ready[b], j >> 1, &abort_flag))
+                return false;
+            if (first && item > 0 && !warp_wait(&bars.o_free, item - 1, &abort_flag)) return false;
+            tc::fence_after_sync();
+            const uint32_t va = tc::smem_u32(sv + b * C::kOp);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)  // 16 positions each; a page is one 128-byte-wide chunk of HD rows
-                    tc::mma_f16_ts(tm + C::kO, tm + 128 * b + 8 * ks,
-                                   tc::desc_sw128(va + (uint32_t)((ks >> 2) * HD * 128 + (ks & 3) * 32)), id_pv,
-                                   (first && ks == 0) ? 0u : 1u);
-                tc::commit(&bars.v_free[b]);
-                tc::commit(&bars.pv_done);
-                return true;
-            };
-            bool ok = true, pfirst = false;
-            int pitem = 0;
-            while (ok && wk.next(p, HR)) {
-                const int j = wk.tile;
-                const int b = j & 1;
-                ok = wait_or_abort(&bars.k_ready[b], j >> 1, &abort_flag);
-                if (!ok) break;
-                tc::fence_after_sync();
-                const uint32_t ka = tc::smem_u32(sk + b * C::kOp);
+            for (int ks = 0; ks < 8; ++ks)  // 16 positions each; a page is one 128-byte-wide chunk of HD rows
+                tc::mma_f16_ts_warp(tm + C::kO, tm + C::kP + 64 * b + 8 * ks,
+                               tc::desc_sw128(va + (uint32_t)((ks >> 2) * HD * 128 + (ks & 3) * 32)), id_pv,
+                               (first && ks == 0) ? 0u : 1u);
+            tc::commit_warp(&bars.v_free[b]);
+            tc::commit_warp(&bars.pv_done);
+            return true;
+        };
+        bool ok = true, pfirst = false;
+        int pitem = 0;
+        while (ok && wk.next(p, HR)) {
+            const int j = wk.tile;
+            const int b = j & 1;
+            ok = warp_wait(&bars.k_ready[b], j >> 1, &abort_flag);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint32_t ka = tc::smem_u32(sk + b * C::kOp);
 #pragma unroll
-                for (int ks = 0; ks < HD / 16; ++ks)
-                    tc::mma_f16_ss(tm + 128 * b, tc::desc_tf32_kstep(qa, 128, ks), tc::desc_tf32_kstep(ka, 128, ks), id_qk,
-                                   ks > 0);
-                tc::commit(&bars.k_free[b]);
-                tc::commit(&bars.s_full[b]);
-                if (j > 0) ok = pv(j - 1, pfirst, pitem);
-                pfirst = wk.first;
-                pitem = wk.item;
-            }
-            if (ok) pv(wk.tile, pfirst, pitem);
-            tc::commit(&bars.drain);  // every product is done before the memory goes
-            mbar_wait_drain(&bars.drain, 0);
+            for (int ks = 0; ks < HD / 16; ++ks)
+                tc::mma_f16_ss_warp(tm + 128 * b, tc::desc_tf32_kstep(qa, 128, ks), tc::desc_tf32_kstep(ka, 128, ks), id_qk,
+                               ks > 0);
+            tc::commit_warp(&bars.k_free[b]);
+            tc::commit_warp(&bars.s_full[b]);
+            if (j > 0) ok = pv(j - 1, pfirst, pitem);
+            pfirst = wk.first;
+            pitem = wk.item;
         }
-    } else if (warp >= 6) {
+        if (ok) pv(wk.tile, pfirst, pitem);
+        tc::commit_warp(&bars.drain);  // every product is done before the memory goes
+        __all_sync(~0u, mbar_wait_drain(&bars.drain, 0));
+    } else if (warp >= kConvWarp) {
         // ---------------- conversion
-        const int ct = tid - 6 * 32;  // 0..kConv - 1
+        const int ct = tid - kConvWarp * 32;  // 0..kConv - 1
         bool ok = true;
         while (ok && wk.next(p, HR)) {
             const int j = wk.tile;
             const int b = j & 1;
             // the buffers' last readers: QK(j - 2) and PV(j - 2)
             if (j >= 2) {
-                ok = __all_sync(~0u, wait_or_abort(&bars.k_free[b], (j >> 1) - 1, &abort_flag) &&
-                                         wait_or_abort(&bars.v_free[b], (j >> 1) - 1, &abort_flag));
+                ok = warp_wait(&bars.k_free[b], (j >> 1) - 1, &abort_flag) && warp_wait(&bars.v_free[b], (j >> 1) - 1, &abort_flag);
                 if (!ok) break;
             }
             if (wk.first) {
                 // the query rows: the last product of the item before has read its own
                 if (j >= 1) {
-                    ok = __all_sync(~0u, wait_or_abort(&bars.k_free[b ^ 1], (j - 1) >> 1, &abort_flag));
+                    ok = warp_wait(&bars.k_free[b ^ 1], (j - 1) >> 1, &abort_flag);
                     if (!ok) break;
                 }
                 const int h = wk.un.hr / RB;
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
             for (int pg = 0; pg < wk.pages; ++pg) {
                 const int i = wk.i + pg;
                 const int slot = i % C::kSlots;
-                ok = __all_sync(~0u, wait_or_abort(&bars.full[slot], i / C::kSlots, &abort_flag));
+                ok = warp_wait(&bars.full[slot], i / C::kSlots, &abort_flag);
                 if (!ok) break;
                 const unsigned char *kb = ring + slot * 2 * C::kHalf;
                 constexpr int PR = HD / 16;  // pieces per position
@@ -353,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                     if (have) {
                         a = *reinterpret_cast<const uint4 *>(vb + 16 * x);
                         if (tail) {  // bytes past the end, and the window's NaN bytes, count as zero
+                            asm volatile("" ::: "memory");  // (a branch, not predicates)
                             const int left = wk.un.len - pos0, seen = window0 - pos0;
                             int at = min(min(mask_word(a.x, 16 * u, left, seen), mask_word(a.y, 16 * u + 4, left, seen)),
                                          min(mask_word(a.z, 16 * u + 8, left, seen), mask_word(a.w, 16 * u + 12, left, seen)));
@@ -376,91 +381,93 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
             }
         }
     } else {
-        // ---------------- softmax: thread = row
+        // ---------------- softmax: thread = (row, page of the tile)
         // Every warp waits for every PV (of the tile before, before it gives the
         // tile's weights): QK(j) is issued before PV(j - 1), so that a wait by parity
-        // for a later one alone could take an older for it.
-        const uint32_t o_addr = tc::lane_addr(tm, warp, C::kO);
+        // for a later one alone could take an older for it.  After a wait gave up the
+        // loop runs on, on garbage: the two warps of a row meet at barriers.
+        const int pg = warp >> 2, quad = warp & 3, r = tid & 127;
+        const uint32_t o_addr = tc::lane_addr(tm, quad, C::kO + pg * (HD / 2));  // its half of the channels
+        float *mine = reinterpret_cast<float *>(exchange) + pg * 128 + r;
+        const float *other = reinterpret_cast<float *>(exchange) + (pg ^ 1) * 128 + r;
+        auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); };
         float m = -INFINITY, l = 0.f, qs = 0.f, vref = 0.f;
         int limit = 0;
         bool valid = false, ok = true;
         int64_t qrow = 0;
-        while (ok && wk.next(p, HR)) {
+        while (wk.next(p, HR)) {
             const int j = wk.tile;
             const int b = j & 1;
-            const uint32_t s_addr = tc::lane_addr(tm, warp, 128 * b);
             const Unit &un = wk.un;
-            const int rb = un.hr % RB, h = un.hr / RB, row = rb * 128 + tid;
-            const bool active = rb * 128 + warp * 32 < rows_all;  // some row of this warp exists
-            ok = __all_sync(~0u, wait_or_abort(&bars.s_full[b], j >> 1, &abort_flag));
-            if (!ok) break;
+            const int rb = un.hr % RB, h = un.hr / RB, row = rb * 128 + r;
+            const bool active = rb * 128 + quad * 32 < rows_all;  // some row of this warp exists
+            if (!warp_wait(&bars.s_full[b], j >> 1, &abort_flag)) ok = false;
             tc::fence_after_sync();
             if (wk.first) {
                 valid = row < rows_all;
                 limit = valid ? un.len - p.D + 1 + row / p.G : 0;
                 qrow = valid ? ((int64_t)un.n * p.D + row / p.G) * p.Hq + h * p.G + row % p.G : 0;
-                qs = __uint_as_float((uint32_t)(127 - 14 + q_exp[wk.item & 1][tid]) << 23) * p.scale * kLog2e;
+                qs = __uint_as_float((uint32_t)(127 - 14 + q_exp[wk.item & 1][r]) << 23) * p.scale * kLog2e;
                 m = -INFINITY;
                 l = 0.f;
                 vref = 0.f;
             }
+            float fix = 1.f, use = 0.f, f = 1.f, z = 0.f, unbias = 1.f;
+            bool masked = false, apart = false;
+            int end = 0;  // columns of its page that the row sees
+            const uint32_t s_addr = tc::lane_addr(tm, quad, 128 * b + 64 * pg);
+            // (the column loops are rolled: their bodies then stay in the instruction caches)
+            auto scores = [&](int i, float(&x)[32]) {
+                tc::ld32(s_addr + 32 * i, x);
+                tc::wait_ld();
+                if (masked) {
+                    asm volatile("" ::: "memory");  // (a branch, not predicates)
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (32 * i + c >= end) x[c] = -INFINITY;
+                }
+            };
             if (active) {
-                // per page: factor of the raw scores, exponent bias of the weights
-                float f[2], bias[2], unbias[2];
-                bool have[2];
-                float vnew = vref;
+                // factor of the raw scores, and the exponent bias of the weights: O is
+                // counted in the largest value scale so far
+                float vs = 0.f, vnew = vref;
+                bool have = false;
 #pragma unroll
-                for (int pg = 0; pg < 2; ++pg) {
-                    const PageMeta e = meta[(wk.i + pg) % kMeta];
-                    have[pg] = pg < wk.pages && e.block >= 0;
-                    f[pg] = have[pg] ? fmaxf(qs * e.ks, 1e-37f) : 1.f;
-                    bias[pg] = have[pg] ? e.vs : 0.f;
-                    vnew = fmaxf(vnew, bias[pg]);
-                }
-                bool apart = false;
-#pragma unroll
-                for (int pg = 0; pg < 2; ++pg) {
-                    const float ratio = have[pg] ? bias[pg] / vnew : 1.f;
-                    const int e = kBias + (int)(__float_as_uint(ratio) >> 23) - 127;
-                    apart |= e < -45;
-                    bias[pg] = (float)e;
-                    unbias[pg] = __uint_as_float((uint32_t)(127 - (e < -100 ? -100 : e)) << 23);
-                }
-                const float vfix = vref > 0.f ? vref / vnew : 1.f;
-                vref = vnew;
-                const int pos0 = un.page * kPage;
-                const bool masked = pos0 + 2 * kPage > un.len - p.D + 1 || !have[0] || !have[1];
-                const int end = limit - pos0;  // columns that the row sees, of pages that exist
-                auto scores = [&](int pg, float(&x)[2][32]) {
-                    tc::ld32(s_addr + 64 * pg, x[0]);
-                    tc::ld32(s_addr + 64 * pg + 32, x[1]);
-                    tc::wait_ld();
-                    if (masked) {
-                        const int e = have[pg] ? end - 64 * pg : 0;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (32 * i + c >= e) x[i][c] = -INFINITY;
+                for (int x = 0; x < 2; ++x) {
+                    const PageMeta e = meta[(wk.i + x) % kMeta];
+                    const bool hx = x < wk.pages && e.block >= 0;
+                    if (hx) vnew = fmaxf(vnew, e.vs);
+                    if (x == pg) {
+                        have = hx;
+                        f = hx ? fmaxf(qs * e.ks, 1e-37f) : 1.f;
+                        vs = e.vs;
                     }
-                };
+                }
+                const float ratio = have ? vs / vnew : 1.f;
+                const int e = kBias + (int)(__float_as_uint(ratio) >> 23) - 127;
+                apart = e < -45;
+                z = (float)e;
+                unbias = __uint_as_float((uint32_t)(127 - (e < -100 ? -100 : e)) << 23);
+                fix = vref > 0.f ? vref / vnew : 1.f;
+                vref = vnew;
+                end = have ? limit - (un.page + pg) * kPage : 0;
+                masked = !have || (un.page + pg + 1) * kPage > un.len - p.D + 1;
                 // (read twice: the maximum first, then the weights)
                 float mx = -INFINITY;
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    float x[32], part[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    scores(i, x);
 #pragma unroll
-                for (int pg = 0; pg < 2; ++pg) {
-                    float x[2][32], part[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    scores(pg, x);
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        part[0] = fmaxf(part[0], x[0][c]);
-                        part[1] = fmaxf(part[1], x[0][c + 1]);
-                        part[2] = fmaxf(part[2], x[1][c]);
-                        part[3] = fmaxf(part[3], x[1][c + 1]);
-                    }
-                    mx = fmaxf(mx, fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])) * f[pg]);
+                    for (int c = 0; c < 32; ++c) part[c & 3] = fmaxf(part[c & 3], x[c]);
+                    mx = fmaxf(mx, fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])));
                 }
+                mx *= f;
+                *mine = mx;
+                pair_sync();
+                mx = fmaxf(mx, *other);
+                pair_sync();
                 const float mnew = fmaxf(m, mx);
-                float fix = vfix;
                 if (wk.first) {
                     m = mnew;
                 } else if (mnew - m > kLazy || (m == -INFINITY && mnew > m)) {
@@ -469,12 +476,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                     l *= al;
                     m = mnew;
                 }
-                if (j > 0) ok = __all_sync(~0u, wait_or_abort(&bars.pv_done, j - 1, &abort_flag));
-                if (!ok) break;
+                use = m == -INFINITY ? 0.f : m;
+                z -= use;
+            }
+            if (j > 0 && !warp_wait(&bars.pv_done, j - 1, &abort_flag)) ok = false;
+            if (active) {
                 if (__any_sync(~0u, !wk.first && fix != 1.f)) {
                     tc::fence_after_sync();
 #pragma unroll 1
-                    for (int c = 0; c < HD; c += 16) {
+                    for (int c = 0; c < HD / 2; c += 16) {
                         float o[16];
                         tc::ld16(o_addr + c, o);
                         tc::wait_ld();
@@ -484,45 +494,33 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                     }
                     tc::wait_st();
                 }
-                const float use = m == -INFINITY ? 0.f : m;
-                float rs[2] = {0.f, 0.f};
-#pragma unroll
-                for (int pg = 0; pg < 2; ++pg) {
-                    const float k = f[pg], z = bias[pg] - use;
-                    float x[2][32];
-                    scores(pg, x);
+                float rs = 0.f;
+                const uint32_t p_addr = tc::lane_addr(tm, quad, C::kP + 64 * b + 32 * pg);
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    float x[32];
+                    scores(i, x);
                     if (apart) {  // these weights may vanish next to a larger value scale: their sum apart
+                        asm volatile("" ::: "memory");
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) rs[pg] += ex2(fmaf(x[i][c], k, -use));
+                        for (int c = 0; c < 32; ++c) rs += ex2(fmaf(x[c], f, -use));
                     }
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            const float x0 = ex2(fmaf(x[i][2 * c], k, z)), x1 = ex2(fmaf(x[i][2 * c + 1], k, z));
-                            sum[2 * (c & 1)] += x0;
-                            sum[2 * (c & 1) + 1] += x1;
-                            pk[c] = pack_f16(x0, x1);
-                        }
-                        tc::st16u(s_addr + 32 * pg + 16 * i, pk);
+                    for (int c = 0; c < 16; ++c) {
+                        const float x0 = ex2(fmaf(x[2 * c], f, z)), x1 = ex2(fmaf(x[2 * c + 1], f, z));
+                        sum[2 * (c & 1)] += x0;
+                        sum[2 * (c & 1) + 1] += x1;
+                        pk[c] = pack_f16(x0, x1);
                     }
-                    if (!apart) rs[pg] = ((sum[0] + sum[2]) + (sum[1] + sum[3])) * unbias[pg];
+                    tc::st16u(p_addr + 16 * i, pk);
+                    if (!apart) rs = fmaf((sum[0] + sum[2]) + (sum[1] + sum[3]), unbias, rs);
                 }
                 tc::wait_st();
-                l += rs[0] + rs[1];
-                if (p.weight_out != nullptr && valid) {
-#pragma unroll
-                    for (int pg = 0; pg < 2; ++pg)
-                        if (pg < wk.pages)
-                            ws[lay.page_w + qrow * p.max_pages + un.page + pg] = rs[pg] > 0.f ? log2f(rs[pg]) + use : -INFINITY;
-                }
-            } else {
-                if (j > 0) ok = __all_sync(~0u, wait_or_abort(&bars.pv_done, j - 1, &abort_flag));
-                if (!ok) break;
+                l += rs;
+                if (p.weight_out != nullptr && valid && pg < wk.pages)
+                    ws[lay.page_w + qrow * p.max_pages + un.page + pg] = rs > 0.f ? log2f(rs) + use : -INFINITY;
             }
             tc::fence_before_sync();
             __syncwarp();
@@ -530,34 +528,40 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
             if (!wk.last) continue;
 
             // ---- the item's end
-            ok = __all_sync(~0u, wait_or_abort(&bars.pv_done, j, &abort_flag));
-            if (!ok) break;
+            if (!warp_wait(&bars.pv_done, j, &abort_flag)) ok = false;
             tc::fence_after_sync();
             const bool from_start = wk.page0 == 0;
             const bool whole = from_start && un.page + wk.pages == un.pages;
-            const float unit = vref * (1.f / (float)(1 << kBias));
             if (active) {
-                const float fo = whole ? (l == 0.f ? 0.f : unit / l) : unit;
+                *mine = l;
+                pair_sync();
+                const float l0 = pg == 0 ? l : *other, l1 = pg == 0 ? *other : l;
+                pair_sync();
+                const float total = l0 + l1;
+                const float unit = vref * (1.f / (float)(1 << kBias));
+                const float fo = whole ? (total == 0.f ? 0.f : unit / total) : unit;
                 const int64_t slot = 2 * (int64_t)blockIdx.x + (from_start ? 1 : 0);
-                T *dst = static_cast<T *>(p.out) + qrow * HD;
-                float *part = ws + lay.part_o + (slot * lay.PR + tid) * HD;
+                T *dst = static_cast<T *>(p.out) + qrow * HD + pg * (HD / 2);
+                float *part = ws + lay.part_o + (slot * lay.PR + r) * HD + pg * (HD / 2);
                 const bool nan = v_nan != 0;
 #pragma unroll 1
-                for (int c = 0; c < HD; c += 16) {
+                for (int c = 0; c < HD / 2; c += 16) {
                     float o[16];
                     tc::ld16(o_addr + c, o);
                     tc::wait_ld();
-                    if (!valid) continue;
+                    if (!valid || !ok) continue;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) o[e] = fo == 0.f ? 0.f : o[e] * fo;
                     if (nan) {  // the NaN values that this row sees
+                        asm volatile("" ::: "memory");
                         for (int pos = max(un.len - p.D + 1, 0); pos < limit; ++pos) {
                             const int id = p.block_table[(int64_t)un.n * p.max_pages + pos / kPage];
                             if (id < 0 || id >= p.num_pages) continue;
-                            const unsigned char *vb = p.v_pages + ((int64_t)id * p.Hkv + h) * C::kHalf + pos % kPage;
+                            const unsigned char *vb = p.v_pages + ((int64_t)id * p.Hkv + h) * C::kHalf +
+                                                      (pg * (HD / 2) + c) * kPage + pos % kPage;
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                if ((vb[(c + e) * kPage] & 0x7f) == 0x7f) o[e] = NAN;
+                                if ((vb[e * kPage] & 0x7f) == 0x7f) o[e] = NAN;
                         }
                     }
                     if (whole) {
@@ -572,18 +576,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                             *reinterpret_cast<float4 *>(part + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                 }
-                if (valid) {
+                if (valid && ok && pg == 0) {
                     if (whole) {
-                        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+                        const float lse2 = total == 0.f ? -INFINITY : m + log2f(total);
                         if (p.lse) p.lse[qrow] = lse2 * kLn2;
                         if (p.weight_out) ws[lay.lse2 + qrow] = lse2;
                     } else {
-                        ws[lay.part_m + slot * lay.PR + tid] = m;
-                        ws[lay.part_l + slot * lay.PR + tid] = l;
+                        ws[lay.part_m + slot * lay.PR + r] = m;
+                        ws[lay.part_l + slot * lay.PR + r] = total;
                     }
                 }
             }
-            if (from_start && tid == 0) write_desc(ws, lay, un, wk.cur, HR, whole, W, U);
+            if (from_start && tid == 0 && ok) write_desc(ws, lay, un, wk.cur, HR, whole, W, U);
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.o_free);
@@ -592,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 4) tc::tmem_dealloc(tm, kTmem);
+    if (warp == kMmaWarp) tc::tmem_dealloc(tm, kTmem);
     if (tid == 0 && abort_flag && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_TIMEOUT);
 }
 

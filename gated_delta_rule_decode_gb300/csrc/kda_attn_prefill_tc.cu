@@ -137,6 +137,11 @@ __device__ __forceinline__ bool tile_any(int id, bool x) {
     return r != 0;
 }
 
+// All lanes of a warp, with one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, volatile int *abort_flag) {
+    return __all_sync(~0u, wait_or_abort(bar, phase, abort_flag));
+}
+
 __device__ __forceinline__ bool nonfinite2(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
@@ -232,65 +237,63 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
                 for (int j = max(0, jv - C::NV); j < jv; ++j) mbar_wait_drain(&bars.v_full[j % C::NV], (j / C::NV) & 1u);
             }
         } else if (warp == 8) {
-            // ---------------- products
-            if (lane == 0) {
-                const uint32_t id_qk = idesc_bf16(128, 128, false), id_pv = idesc_bf16(128, HD, true);
-                auto qk = [&](int t, int j) {
-                    const uint32_t qa = tc::smem_u32(sq + t * C::kTile), ka = tc::smem_u32(sk + (j % C::NK) * C::kTile);
+            // ---------------- products (the whole warp in step: see mma_f16_ss_warp)
+            const uint32_t id_qk = idesc_bf16(128, 128, false), id_pv = idesc_bf16(128, HD, true);
+            auto qk = [&](int t, int j) {
+                const uint32_t qa = tc::smem_u32(sq + t * C::kTile), ka = tc::smem_u32(sk + (j % C::NK) * C::kTile);
 #pragma unroll
-                    for (int ks = 0; ks < HD / 16; ++ks)
-                        tc::mma_f16_ss(tm + 128 * t, tc::desc_tf32_kstep(qa, 128, ks), tc::desc_tf32_kstep(ka, 128, ks),
-                                       id_qk, ks > 0);
-                    tc::commit(&bars.s_full[t]);
-                };
-                auto pv = [&](int t, int j) {
-                    const uint32_t va = tc::smem_u32(sv + (j % C::NV) * C::kTile);
+                for (int ks = 0; ks < HD / 16; ++ks)
+                    tc::mma_f16_ss_warp(tm + 128 * t, tc::desc_tf32_kstep(qa, 128, ks), tc::desc_tf32_kstep(ka, 128, ks),
+                                   id_qk, ks > 0);
+                tc::commit_warp(&bars.s_full[t]);
+            };
+            auto pv = [&](int t, int j) {
+                const uint32_t va = tc::smem_u32(sv + (j % C::NV) * C::kTile);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    tc::mma_f16_ts_warp(tm + C::kO + HD * t, tm + 128 * t + 8 * ks, desc_v(va + ks * 2048, C::kChunk), id_pv,
+                                   (j > 0 || ks > 0) ? 1u : 0u);
+                if (__any_sync(~0u, two_terms[t])) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        tc::mma_f16_ts(tm + C::kO + HD * t, tm + 128 * t + 8 * ks, desc_v(va + ks * 2048, C::kChunk), id_pv,
-                                       (j > 0 || ks > 0) ? 1u : 0u);
-                    if (two_terms[t]) {
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            tc::mma_f16_ts(tm + C::kO + HD * t, tm + 128 * t + 64 + 8 * ks, desc_v(va + ks * 2048, C::kChunk),
-                                           id_pv, 1u);
-                    }
-                    tc::commit(&bars.pv_done[t]);
-                };
-                bool ok = wait_or_abort(&bars.k_full[0], 0, &abort_flag);
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (nblk[t] == 0) continue;
-                    ok = wait_or_abort(&bars.q_full[t], 0, &abort_flag);
-                    if (ok) qk(t, 0);
+                        tc::mma_f16_ts_warp(tm + C::kO + HD * t, tm + 128 * t + 64 + 8 * ks, desc_v(va + ks * 2048, C::kChunk),
+                                       id_pv, 1u);
                 }
-                if (ok) tc::commit(&bars.k_empty[0]);
-                for (int j = 0; j < n && ok; ++j) {
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        if (j < nblk[t]) {
-                            ok = wait_or_abort(&bars.p_full[t], j, &abort_flag) &&
-                                 wait_or_abort(&bars.v_ready[j % C::NV], j / C::NV, &abort_flag);
-                            if (!ok) break;
-                            tc::fence_after_sync();
-                            pv(t, j);
-                        }
-                        if (j + 1 < nblk[t]) {
-                            ok = wait_or_abort(&bars.k_full[(j + 1) % C::NK], (j + 1) / C::NK, &abort_flag);
-                            if (!ok) break;
-                            qk(t, j + 1);
-                        }
-                    }
-                    if (!ok) break;
-                    tc::commit(&bars.v_empty[j % C::NV]);
-                    if (j + 1 < n) tc::commit(&bars.k_empty[(j + 1) % C::NK]);
-                }
-                tc::commit(&bars.drain);  // every product is done before the memory goes
-                mbar_wait_drain(&bars.drain, 0);
+                tc::commit_warp(&bars.pv_done[t]);
+            };
+            bool ok = warp_wait(&bars.k_full[0], 0, &abort_flag);
+            for (int t = 0; t < 2 && ok; ++t) {
+                if (nblk[t] == 0) continue;
+                ok = warp_wait(&bars.q_full[t], 0, &abort_flag);
+                if (ok) qk(t, 0);
             }
+            if (ok) tc::commit_warp(&bars.k_empty[0]);
+            for (int j = 0; j < n && ok; ++j) {
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (j < nblk[t]) {
+                        ok = warp_wait(&bars.p_full[t], j, &abort_flag) &&
+                             warp_wait(&bars.v_ready[j % C::NV], j / C::NV, &abort_flag);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        pv(t, j);
+                    }
+                    if (j + 1 < nblk[t]) {
+                        ok = warp_wait(&bars.k_full[(j + 1) % C::NK], (j + 1) / C::NK, &abort_flag);
+                        if (!ok) break;
+                        qk(t, j + 1);
+                    }
+                }
+                if (!ok) break;
+                tc::commit_warp(&bars.v_empty[j % C::NV]);
+                if (j + 1 < n) tc::commit_warp(&bars.k_empty[(j + 1) % C::NK]);
+            }
+            tc::commit_warp(&bars.drain);  // every product is done before the memory goes
+            __all_sync(~0u, mbar_wait_drain(&bars.drain, 0));
         } else {
             // ---------------- values that some row must not see
             const int ft = tid - 320;  // 0..63
             for (int j = 0; j < n; ++j) {
-                if (!__all_sync(~0u, wait_or_abort(&bars.v_full[j % C::NV], j / C::NV, &abort_flag))) break;
+                if (!warp_wait(&bars.v_full[j % C::NV], j / C::NV, &abort_flag)) break;
                 if (j * kKeys + kKeys - 1 > a0) {
                     unsigned char *blk = sv + (j % C::NV) * C::kTile;
                     bool bad = false;
@@ -334,7 +337,7 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
         bool ok = true;
         for (int j = 0; j < nb; ++j) {
             // (after a wait gave up the loop runs on, on garbage: the tile's warps meet at a barrier below)
-            if (!__all_sync(~0u, wait_or_abort(&bars.s_full[t], j, &abort_flag))) ok = false;
+            if (!warp_wait(&bars.s_full[t], j, &abort_flag)) ok = false;
             tc::fence_after_sync();
             float sc[4][32];
 #pragma unroll
@@ -362,7 +365,7 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
                     const float f = grow ? ex2((m - mnew) * sl2) : 1.f;
                     if (grow) m = mnew;
                     l *= f;
-                    if (!__all_sync(~0u, wait_or_abort(&bars.pv_done[t], j - 1, &abort_flag))) ok = false;
+                    if (!warp_wait(&bars.pv_done[t], j - 1, &abort_flag)) ok = false;
                     tc::fence_after_sync();
 #pragma unroll 1
                     for (int c = 0; c < HD; c += 16) {
@@ -414,7 +417,7 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
             l += sum[0].x + sum[0].y;
         }
         // ---------------- epilogue
-        if (nb > 0 && ok) ok = __all_sync(~0u, wait_or_abort(&bars.pv_done[t], nb - 1, &abort_flag));
+        if (nb > 0 && ok) ok = warp_wait(&bars.pv_done[t], nb - 1, &abort_flag);
         if (nb > 0 && ok) {
             tc::fence_after_sync();
             const float inv = 1.f / l;
