@@ -65,17 +65,26 @@ struct CacheEvictParams {
 };
 
 // The packed sequence that owns unit u when sequence s gets the units
-// [cu[s] / per + s, cu[s+1] / per + s + 1): at least ceil(len / per) of them,
-// found by bisection on cu_seqlens alone.  Also gives the unit's index within
-// the sequence.  Reads cu[0..num_seqs] only, whatever the offsets hold.
+// [cu[s] / per + s extra, cu[s+1] / per + (s + 1) extra), at least
+// ceil(len / per) (extra >= 1) of them: the last s whose first unit is <= u, by
+// a 32-way search of a converged warp on cu_seqlens alone (two dependent reads
+// for 1024 sequences).  Also gives the unit's index within the sequence.
+// Reads cu[0..num_seqs - 1] only, whatever the offsets hold.
 __device__ __forceinline__ int seq_of_unit(const int32_t *cu, int num_seqs, int per, int extra, int64_t u,
                                            int64_t &local) {
-    int a = 0, b = num_seqs - 1;  // last s with its first unit <= u
-    while (a < b) {
-        const int m = (a + b + 1) >> 1;
-        if ((int64_t)(cu[m] / per) + (int64_t)m * extra <= u) a = m; else b = m - 1;
-    }
-    local = u - ((int64_t)(cu[a] / per) + (int64_t)a * extra);
+    const int lane = threadIdx.x & 31;
+    int a = 0, n = num_seqs, first = 0;  // candidates a..a + n - 1, and the first unit of a
+    do {
+        const int step = (n + 31) / 32, m = a + lane * step;
+        int64_t at = 0;
+        if (lane * step < n) at = (int64_t)(cu[m] / per) + (int64_t)m * extra;
+        const unsigned in = __ballot_sync(~0u, lane * step < n && (lane == 0 || at <= u));
+        const int k = 31 - __clz(in);
+        first = __shfl_sync(~0u, (int)(u - at), k);
+        a += k * step;
+        n = min(step, n - k * step);
+    } while (n > 1);
+    local = first;
     return a;
 }
 

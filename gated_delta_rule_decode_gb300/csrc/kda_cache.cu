@@ -11,15 +11,19 @@ namespace {
 
 // ---------------------------------------------------------------- append
 //
-// One CTA per (page that gets new rows, head, keys or values).  The page's
-// new rows (up to 64) are loaded once into registers as 16-byte pieces, a
-// block reduction gives their largest finite magnitude and so the scale, and
-// the rows leave as bytes: keys as they lie, values through a shared tile
-// that turns them into one row of positions per channel.
+// A page that gets new rows, a head, and keys or values make one task.  The new
+// rows' largest finite magnitude gives the scale; a page whose scale grows first
+// has its earlier rows rescaled.  The scale is a power of two, so x / s' is
+// exact and rescaling re-rounds only what becomes subnormal in e4m3.
 //
-// The scale is a power of two, so x / s' is exact and a page whose scale
-// grows re-rounds only what becomes subnormal in e4m3.
+// Two kernels, by the tokens per sequence of the call (kFewTokens): prompts take
+// a CTA per task, which holds the page's rows in registers and turns values into
+// rows of positions through shared memory; decode steps take a CTA per page and
+// a warp per task, which goes over the one or few rows twice.  Bound by HBM
+// (prompts) and by the chain of dependent reads (steps).
 constexpr int kAppendThreads = 128;
+constexpr int kStepWarps = 8;
+constexpr int64_t kFewTokens = 8;
 
 __device__ __forceinline__ float pow2_need(float amax) {
     // smallest e >= -126 with amax <= 1.75 * 2^8 * 2^e
@@ -74,119 +78,211 @@ struct Piece<__nv_bfloat16> {
     }
 };
 
+template <typename T>
+__device__ __forceinline__ float piece_max(const uint4 &u) {
+    float x[Piece<T>::N], m = 0.f;
+    Piece<T>::get(u, x);
+#pragma unroll
+    for (int j = 0; j < Piece<T>::N; ++j) m = fmaxf(m, finite_abs(x[j]));
+    return m;
+}
+
+// The page of a unit: its sequence's rows lo..hi - 1 (positions), the first of
+// them token `tok`.  False where the unit has no page, or (flagged) a bad one.
+struct PageRows {
+    int64_t page, tok;
+    int rows, off;  // new rows, and the place of the first in the page
+};
+
+__device__ __forceinline__ bool page_of_unit(const CacheAppendParams &p, int64_t unit, PageRows &r) {
+    int64_t c = 0;
+    const int s = seq_of_unit(p.cu_seqlens, p.num_seqs, kPage, 2, unit, c);
+    int t0, t1;
+    if (!seq_range(p.cu_seqlens, s, p.total_tokens, p.err_flag, t0, t1)) return false;
+    const int64_t start = p.start_pos[s];
+    if (c < 0 || t1 == t0 || start < 0) return false;
+    const int64_t end = start + (t1 - t0), idx = start / kPage + c;
+    if (idx * kPage >= end) return false;
+    const int64_t lo = idx * kPage > start ? idx * kPage : start;
+    const int64_t hi = (idx + 1) * kPage < end ? (idx + 1) * kPage : end;
+    r.rows = (int)(hi - lo);
+    r.off = (int)(lo - idx * kPage);
+    r.tok = (int64_t)t0 + (lo - start);
+    r.page = idx < p.max_pages ? p.block_table[(int64_t)s * p.max_pages + idx] : -1;
+    if (r.page < 0 || r.page >= p.num_pages) {
+        if (p.err_flag && (threadIdx.x & 31) == 0) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
+        return false;
+    }
+    return true;
+}
+
+// Rescales the page's first `off` positions; threads tid of n.
+template <int HD>
+__device__ __forceinline__ void rescale_rows(unsigned char *dst, bool is_v, int off, float ratio, int tid, int n) {
+    for (int i = tid; i < off * HD; i += n) {
+        unsigned char *b = is_v ? dst + (i / off) * kPage + i % off : dst + i;
+        *b = requant1(*b, ratio);
+    }
+}
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const CacheAppendParams p) {
-    constexpr int N = Piece<T>::N;                  // elements per 16-byte piece
-    constexpr int PR = HD / N;                      // pieces per row
-    constexpr int RS = kAppendThreads / PR;         // rows per step of the block
-    constexpr int STEPS = (kPage + RS - 1) / RS;
-    __shared__ __align__(16) unsigned char tile[HD][kPage + 4];
+    constexpr int N = Piece<T>::N;                 // elements per 16-byte piece
+    constexpr int PR = HD / N;                     // pieces per row
+    constexpr int GROUPS = kPage / 4;              // groups of four positions
+    constexpr int STEPS = (PR * GROUPS + kAppendThreads - 1) / kAppendThreads;
+    __shared__ __align__(16) uint32_t tile[HD][GROUPS + 1];  // values: four positions of a channel
     __shared__ float warp_max[kAppendThreads / 32];
     const int tid = threadIdx.x, h = blockIdx.y;
     const bool is_v = blockIdx.z != 0;
+    PageRows pr;
+    if (!page_of_unit(p, blockIdx.x, pr)) return;
+    const int off = pr.off, last = pr.off + pr.rows;
 
-    int64_t c = 0;
-    const int s = seq_of_unit(p.cu_seqlens, p.num_seqs, kPage, 2, blockIdx.x, c);
-    int t0, t1;
-    if (!seq_range(p.cu_seqlens, s, p.total_tokens, p.err_flag, t0, t1)) return;
-    const int64_t start = p.start_pos[s];
-    if (t1 == t0 || start < 0) return;
-    const int64_t end = start + (t1 - t0);
-    const int64_t page_idx = start / kPage + c;
-    if (page_idx * kPage >= end) return;
-    const int64_t lo = page_idx * kPage > start ? page_idx * kPage : start;
-    const int64_t hi = (page_idx + 1) * kPage < end ? (page_idx + 1) * kPage : end;
-    const int rows = (int)(hi - lo), off = (int)(lo - page_idx * kPage);
-    const int page = page_idx < p.max_pages ? p.block_table[(int64_t)s * p.max_pages + page_idx] : -1;
-    if (page < 0 || page >= p.num_pages) {
-        if (tid == 0 && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
-        return;
-    }
-
+    // a thread holds one piece of the rows at four neighbouring places of the page
     const int64_t stride = is_v ? p.v_stride : p.k_stride;
-    const T *src = static_cast<const T *>(is_v ? p.v : p.k) + ((int64_t)t0 + (lo - start)) * stride + (int64_t)h * HD;
-    const int r0 = tid / PR, piece = tid % PR;
-    uint4 raw[STEPS];
+    const T *src = static_cast<const T *>(is_v ? p.v : p.k) + (pr.tok - off) * stride + (int64_t)h * HD;
+    uint4 raw[STEPS][4];
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-        const int r = r0 + i * RS;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (r < rows) raw[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)r * stride + piece * N);
-    }
+        const int x = tid + i * kAppendThreads, grp = x / PR, piece = x % PR;
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        float x[N];
-        Piece<T>::get(raw[i], x);
-#pragma unroll
-        for (int j = 0; j < N; ++j) amax = fmaxf(amax, finite_abs(x[j]));
+        for (int e = 0; e < 4; ++e) {
+            const int at = 4 * grp + e;
+            raw[i][e] = make_uint4(0, 0, 0, 0);
+            if (at >= off && at < last) raw[i][e] = __ldcs(reinterpret_cast<const uint4 *>(src + (int64_t)at * stride + piece * N));
+        }
     }
+    float *scale = (is_v ? p.v_scale : p.k_scale) + pr.page * p.Hkv + h;
+    const float old = off > 0 ? *scale : 0.f;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, piece_max<T>(raw[i][e]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
     if ((tid & 31) == 0) warp_max[tid >> 5] = amax;
-    float *scale = (is_v ? p.v_scale : p.k_scale) + (int64_t)page * p.Hkv + h;
-    const float old = off > 0 ? *scale : 0.f;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, warp_max[w]);
     const float now = fmaxf(old, pow2_need(amax));
     const float inv = pow2_inverse(now);
-    const int64_t base = ((int64_t)page * p.Hkv + h) * (int64_t)(HD * kPage);
-    unsigned char *dst = (is_v ? p.v_pages : p.k_pages) + base;
+    unsigned char *dst = (is_v ? p.v_pages : p.k_pages) + (pr.page * p.Hkv + h) * (int64_t)(HD * kPage);
+    if (off > 0 && now > old) rescale_rows<HD>(dst, is_v, off, old * inv, tid, kAppendThreads);
 
-    if (off > 0 && now > old) {  // the page's earlier rows take the new scale
-        const float ratio = old * inv;
-        for (int i = tid; i < off * HD; i += kAppendThreads) {
-            unsigned char *b = is_v ? dst + (i / off) * kPage + i % off : dst + i;
-            *b = requant1(*b, ratio);
-        }
-    }
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-        const int r = r0 + i * RS;
-        if (r >= rows) continue;
-        float x[N];
-        Piece<T>::get(raw[i], x);
-        uint32_t w[N / 4];
+        const int x = tid + i * kAppendThreads, grp = x / PR, piece = x % PR;
+        if (STEPS * kAppendThreads > PR * GROUPS && grp >= GROUPS) continue;
+        uint32_t w[4][N / 4];  // row e, four channels a word
 #pragma unroll
-        for (int j = 0; j < N / 4; ++j)
-            w[j] = quant2(x[4 * j] * inv, x[4 * j + 1] * inv) | (quant2(x[4 * j + 2] * inv, x[4 * j + 3] * inv) << 16);
+        for (int e = 0; e < 4; ++e) {
+            float y[N];
+            Piece<T>::get(raw[i][e], y);
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j)
+                w[e][j] = quant2(y[4 * j] * inv, y[4 * j + 1] * inv) | (quant2(y[4 * j + 2] * inv, y[4 * j + 3] * inv) << 16);
+        }
         if (!is_v) {
-            uint32_t *o = reinterpret_cast<uint32_t *>(dst + (off + r) * HD + piece * N);
-            if constexpr (N == 8) *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
-            else *o = w[0];
-        } else {
 #pragma unroll
-            for (int j = 0; j < N; ++j) tile[piece * N + j][off + r] = (unsigned char)(w[j / 4] >> (8 * (j % 4)));
+            for (int e = 0; e < 4; ++e) {
+                const int at = 4 * grp + e;
+                if (at < off || at >= last) continue;
+                uint32_t *o = reinterpret_cast<uint32_t *>(dst + at * HD + piece * N);
+                if constexpr (N == 8) *reinterpret_cast<uint2 *>(o) = make_uint2(w[e][0], w[e][1]);
+                else *o = w[e][0];
+            }
+        } else {
+            // 4 x 4 bytes turned: four positions of a channel a word
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j) {
+                const uint32_t a = __byte_perm(w[0][j], w[1][j], 0x5140), b = __byte_perm(w[2][j], w[3][j], 0x5140);
+                const uint32_t c = __byte_perm(w[0][j], w[1][j], 0x7362), d = __byte_perm(w[2][j], w[3][j], 0x7362);
+                tile[piece * N + 4 * j][grp] = __byte_perm(a, b, 0x5410);
+                tile[piece * N + 4 * j + 1][grp] = __byte_perm(a, b, 0x7632);
+                tile[piece * N + 4 * j + 2][grp] = __byte_perm(c, d, 0x5410);
+                tile[piece * N + 4 * j + 3][grp] = __byte_perm(c, d, 0x7632);
+            }
         }
     }
     if (tid == 0) *scale = now;
     if (!is_v) return;
     __syncthreads();
-    // words of four positions that are all new, single bytes at the two ends
-    const int last = off + rows;
+    // words of four new positions, single bytes at the two ends
     const int w0 = off / 4, nw = (last + 3) / 4 - w0;
     for (int i = tid; i < HD * nw; i += kAppendThreads) {
-        const int ch = i / nw, pos = 4 * (w0 + i % nw);
+        const int ch = i / nw, g = w0 + i % nw, pos = 4 * g;
+        const uint32_t x = tile[ch][g];
         if (pos >= off && pos + 4 <= last) {
-            *reinterpret_cast<uint32_t *>(dst + ch * kPage + pos) = *reinterpret_cast<const uint32_t *>(&tile[ch][pos]);
+            *reinterpret_cast<uint32_t *>(dst + ch * kPage + pos) = x;
         } else {
-            for (int j = pos; j < pos + 4; ++j)
-                if (j >= off && j < last) dst[ch * kPage + j] = tile[ch][j];
+            for (int j = 0; j < 4; ++j)
+                if (pos + j >= off && pos + j < last) dst[ch * kPage + pos + j] = (unsigned char)(x >> (8 * j));
         }
     }
 }
 
-template <typename T>
-cudaError_t launch_append(const CacheAppendParams &p, int d, cudaStream_t st) {
+template <typename T, int HD>
+__global__ void __launch_bounds__(32 * kStepWarps) append_step_kernel(const CacheAppendParams p) {
+    constexpr int N = Piece<T>::N, PR = HD / N;  // pieces per row: 4..32
+    constexpr int RW = 32 / PR;                  // rows at a time
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    PageRows pr;
+    if (!page_of_unit(p, blockIdx.x, pr)) return;
+    const int off = pr.off, piece = lane % PR, r0 = lane / PR;
+    for (int task = warp; task < 2 * p.Hkv; task += kStepWarps) {
+        const int h = task >> 1;
+        const bool is_v = task & 1;
+        const int64_t stride = is_v ? p.v_stride : p.k_stride;
+        const T *src = static_cast<const T *>(is_v ? p.v : p.k) + pr.tok * stride + (int64_t)h * HD + piece * N;
+        float *scale = (is_v ? p.v_scale : p.k_scale) + pr.page * p.Hkv + h;
+        const float old = off > 0 ? *scale : 0.f;
+        float amax = 0.f;
+        for (int r = r0; r < pr.rows; r += RW) amax = fmaxf(amax, piece_max<T>(*reinterpret_cast<const uint4 *>(src + r * stride)));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+        const float now = fmaxf(old, pow2_need(amax));
+        const float inv = pow2_inverse(now);
+        unsigned char *dst = (is_v ? p.v_pages : p.k_pages) + (pr.page * p.Hkv + h) * (int64_t)(HD * kPage);
+        if (off > 0 && now > old) rescale_rows<HD>(dst, is_v, off, old * inv, lane, 32);
+        for (int r = r0; r < pr.rows; r += RW) {
+            float y[N];
+            Piece<T>::get(*reinterpret_cast<const uint4 *>(src + r * stride), y);
+            uint32_t w[N / 4];
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j)
+                w[j] = quant2(y[4 * j] * inv, y[4 * j + 1] * inv) | (quant2(y[4 * j + 2] * inv, y[4 * j + 3] * inv) << 16);
+            if (!is_v) {
+                uint32_t *o = reinterpret_cast<uint32_t *>(dst + (off + r) * HD + piece * N);
+                if constexpr (N == 8) *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+                else *o = w[0];
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j) dst[(piece * N + j) * kPage + off + r] = (unsigned char)(w[j / 4] >> (8 * (j % 4)));
+            }
+        }
+        if (lane == 0) *scale = now;
+    }
+}
+
+template <typename T, int HD>
+cudaError_t launch_append_dim(const CacheAppendParams &p, cudaStream_t st) {
     // units of seq_of_unit: cu / 64 + 2 s, so every sequence has its pages
     const int64_t units = p.total_tokens / kPage + 2 * (int64_t)p.num_seqs;
     if (units > 0x7fffffff) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)units, (unsigned)p.Hkv, 2);
-    if (d == 128) append_kernel<T, 128><<<grid, kAppendThreads, 0, st>>>(p);
-    else if (d == 64) append_kernel<T, 64><<<grid, kAppendThreads, 0, st>>>(p);
-    else append_kernel<T, 32><<<grid, kAppendThreads, 0, st>>>(p);
+    if (p.total_tokens <= kFewTokens * p.num_seqs)
+        append_step_kernel<T, HD><<<(unsigned)units, 32 * kStepWarps, 0, st>>>(p);
+    else
+        append_kernel<T, HD><<<dim3((unsigned)units, (unsigned)p.Hkv, 2), kAppendThreads, 0, st>>>(p);
     return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_append(const CacheAppendParams &p, int d, cudaStream_t st) {
+    if (d == 128) return launch_append_dim<T, 128>(p, st);
+    if (d == 64) return launch_append_dim<T, 64>(p, st);
+    return launch_append_dim<T, 32>(p, st);
 }
 
 // ---------------------------------------------------------------- evict
