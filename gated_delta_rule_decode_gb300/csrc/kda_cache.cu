@@ -78,6 +78,34 @@ struct Piece<__nv_bfloat16> {
     }
 };
 
+// Magnitudes are compared as integers (two bf16 values a word): one and-mask and
+// one maximum a word.  `finite` is false where a value of the maximum is an
+// infinity or NaN; the caller then takes piece_max over the finite ones.
+template <typename T>
+struct Magnitude;
+template <>
+struct Magnitude<float> {
+    static __device__ __forceinline__ uint32_t of(uint32_t m, uint32_t w) { return max(m, w & 0x7fffffffu); }
+    static __device__ __forceinline__ float value(uint32_t m, bool &finite) {
+        finite = m < 0x7f800000u;
+        return __uint_as_float(m);
+    }
+};
+template <>
+struct Magnitude<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t of(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+    static __device__ __forceinline__ float value(uint32_t m, bool &finite) {
+        const uint32_t x = max(m & 0xffffu, m >> 16);
+        finite = x < 0x7f80u;
+        return __uint_as_float(x << 16);
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t piece_bits(uint32_t m, const uint4 &u) {
+    return Magnitude<T>::of(Magnitude<T>::of(Magnitude<T>::of(Magnitude<T>::of(m, u.x), u.y), u.z), u.w);
+}
+
 template <typename T>
 __device__ __forceinline__ float piece_max(const uint4 &u) {
     float x[Piece<T>::N], m = 0.f;
@@ -88,7 +116,8 @@ __device__ __forceinline__ float piece_max(const uint4 &u) {
 }
 
 // The page of a unit: its sequence's rows lo..hi - 1 (positions), the first of
-// them token `tok`.  False where the unit has no page, or (flagged) a bad one.
+// them token `tok`.  False where the unit has no page.  The page's id is not
+// checked here, so that its read and those of the rows overlap.
 struct PageRows {
     int64_t page, tok;
     int rows, off;  // new rows, and the place of the first in the page
@@ -98,8 +127,8 @@ __device__ __forceinline__ bool page_of_unit(const CacheAppendParams &p, int64_t
     int64_t c = 0;
     const int s = seq_of_unit(p.cu_seqlens, p.num_seqs, kPage, 2, unit, c);
     int t0, t1;
-    if (!seq_range(p.cu_seqlens, s, p.total_tokens, p.err_flag, t0, t1)) return false;
     const int64_t start = p.start_pos[s];
+    if (!seq_range(p.cu_seqlens, s, p.total_tokens, p.err_flag, t0, t1)) return false;
     if (c < 0 || t1 == t0 || start < 0) return false;
     const int64_t end = start + (t1 - t0), idx = start / kPage + c;
     if (idx * kPage >= end) return false;
@@ -109,11 +138,13 @@ __device__ __forceinline__ bool page_of_unit(const CacheAppendParams &p, int64_t
     r.off = (int)(lo - idx * kPage);
     r.tok = (int64_t)t0 + (lo - start);
     r.page = idx < p.max_pages ? p.block_table[(int64_t)s * p.max_pages + idx] : -1;
-    if (r.page < 0 || r.page >= p.num_pages) {
-        if (p.err_flag && (threadIdx.x & 31) == 0) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
-        return false;
-    }
     return true;
+}
+
+__device__ __forceinline__ bool page_ok(const CacheAppendParams &p, int64_t page) {
+    if (page >= 0 && page < p.num_pages) return true;
+    if (p.err_flag && (threadIdx.x & 31) == 0) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
+    return false;
 }
 
 // Rescales the page's first `off` positions; threads tid of n.
@@ -126,24 +157,25 @@ __device__ __forceinline__ void rescale_rows(unsigned char *dst, bool is_v, int 
 }
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const CacheAppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 8 : 5) append_kernel(const CacheAppendParams p) {
     constexpr int N = Piece<T>::N;                 // elements per 16-byte piece
     constexpr int PR = HD / N;                     // pieces per row
     constexpr int GROUPS = kPage / 4;              // groups of four positions
     constexpr int STEPS = (PR * GROUPS + kAppendThreads - 1) / kAppendThreads;
     __shared__ __align__(16) uint32_t tile[HD][GROUPS + 1];  // values: four positions of a channel
     __shared__ float warp_max[kAppendThreads / 32];
-    const int tid = threadIdx.x, h = blockIdx.y;
-    const bool is_v = blockIdx.z != 0;
+    // neighbouring CTAs take the heads of the same rows, which lie side by side
+    const int tid = threadIdx.x, h = (int)(blockIdx.x % (unsigned)p.Hkv);
+    const unsigned rest = blockIdx.x / (unsigned)p.Hkv;
+    const bool is_v = rest & 1;
     PageRows pr;
-    if (!page_of_unit(p, blockIdx.x, pr)) return;
+    if (!page_of_unit(p, rest >> 1, pr)) return;
     const int off = pr.off, last = pr.off + pr.rows;
 
     // a thread holds one piece of the rows at four neighbouring places of the page
     const int64_t stride = is_v ? p.v_stride : p.k_stride;
     const T *src = static_cast<const T *>(is_v ? p.v : p.k) + (pr.tok - off) * stride + (int64_t)h * HD;
     uint4 raw[STEPS][4];
-    float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         const int x = tid + i * kAppendThreads, grp = x / PR, piece = x % PR;
@@ -154,12 +186,23 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const CacheAppen
             if (at >= off && at < last) raw[i][e] = __ldcs(reinterpret_cast<const uint4 *>(src + (int64_t)at * stride + piece * N));
         }
     }
+    if (!page_ok(p, pr.page)) return;
     float *scale = (is_v ? p.v_scale : p.k_scale) + pr.page * p.Hkv + h;
     const float old = off > 0 ? *scale : 0.f;
+    uint32_t bits = 0;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, piece_max<T>(raw[i][e]));
+        for (int e = 0; e < 4; ++e) bits = piece_bits<T>(bits, raw[i][e]);
+    bool finite;
+    float amax = Magnitude<T>::value(bits, finite);
+    if (!finite) {
+        amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) amax = fmaxf(amax, piece_max<T>(raw[i][e]));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
     if ((tid & 31) == 0) warp_max[tid >> 5] = amax;
@@ -229,7 +272,7 @@ __global__ void __launch_bounds__(32 * kStepWarps) append_step_kernel(const Cach
     constexpr int RW = 32 / PR;                  // rows at a time
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     PageRows pr;
-    if (!page_of_unit(p, blockIdx.x, pr)) return;
+    if (!page_of_unit(p, blockIdx.x, pr) || !page_ok(p, pr.page)) return;
     const int off = pr.off, piece = lane % PR, r0 = lane / PR;
     for (int task = warp; task < 2 * p.Hkv; task += kStepWarps) {
         const int h = task >> 1;
@@ -270,11 +313,11 @@ template <typename T, int HD>
 cudaError_t launch_append_dim(const CacheAppendParams &p, cudaStream_t st) {
     // units of seq_of_unit: cu / 64 + 2 s, so every sequence has its pages
     const int64_t units = p.total_tokens / kPage + 2 * (int64_t)p.num_seqs;
-    if (units > 0x7fffffff) return cudaErrorInvalidValue;
+    if (units * 2 * p.Hkv > 0x7fffffff) return cudaErrorInvalidValue;
     if (p.total_tokens <= kFewTokens * p.num_seqs)
         append_step_kernel<T, HD><<<(unsigned)units, 32 * kStepWarps, 0, st>>>(p);
     else
-        append_kernel<T, HD><<<dim3((unsigned)units, (unsigned)p.Hkv, 2), kAppendThreads, 0, st>>>(p);
+        append_kernel<T, HD><<<(unsigned)(units * 2 * p.Hkv), kAppendThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
 
