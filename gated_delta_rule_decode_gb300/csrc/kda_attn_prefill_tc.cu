@@ -25,7 +25,7 @@
 // and rescales O in tensor memory.
 //
 // P in bf16 is rounded to 8 bits, which averages out over many keys but not
-// over few.  Where a weight of the block may exceed 1/16 of its row's sum so
+// over few.  Where a weight of the block may exceed 1/4 of its row's sum so
 // far, the tile's P takes a second bf16 term (in the other half of the score
 // columns) and a second product: rows that one or a few keys dominate keep 16
 // bits.  Sums of P are taken in fp32 before rounding.
@@ -53,7 +53,7 @@ constexpr uint32_t kTmem = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;  // log2 growth of the maximum that is let stand
-constexpr float kShare = 16.f;  // weights above 1 / kShare of the row's sum take two terms
+constexpr float kShare = 4.f;  // weights above 1 / kShare of the row's sum take two terms
 
 template <int HD>
 struct Cfg {
@@ -271,16 +271,14 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
             for (int j = 0; j < n && ok; ++j) {
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (j < nblk[t]) {
-                        ok = warp_wait(&bars.p_full[t], j, &abort_flag) &&
-                             warp_wait(&bars.v_ready[j % C::NV], j / C::NV, &abort_flag);
+                        // (what the loads bring is waited for while the tile's softmax still runs)
+                        ok = warp_wait(&bars.v_ready[j % C::NV], j / C::NV, &abort_flag) &&
+                             (j + 1 >= nblk[t] || warp_wait(&bars.k_full[(j + 1) % C::NK], (j + 1) / C::NK, &abort_flag)) &&
+                             warp_wait(&bars.p_full[t], j, &abort_flag);
                         if (!ok) break;
                         tc::fence_after_sync();
                         pv(t, j);
-                    }
-                    if (j + 1 < nblk[t]) {
-                        ok = warp_wait(&bars.k_full[(j + 1) % C::NK], (j + 1) / C::NK, &abort_flag);
-                        if (!ok) break;
-                        qk(t, j + 1);
+                        if (j + 1 < nblk[t]) qk(t, j + 1);
                     }
                 }
                 if (!ok) break;
