@@ -11,9 +11,9 @@
 //                   128 scores from tensor memory, and writes the weights back
 //                   over them as bf16, the operand of the second product
 //   warp 8          issues the products
-//   warp 9          TMA loads: Q once, then rings of key and value blocks
-//   warps 10, 11    look over the value blocks that some row of the tiles
-//                   must not see (below)
+//   warp 9          TMA loads: Q once, then rings of key and value blocks; at
+//                   the end looks over the value blocks that some row of the
+//                   tiles must not see (below)
 //
 // While one tile's softmax runs, the tensor cores work on the other tile:
 // PV(t, j), then QK(t, j + 1), for t = 0, 1 in turn.  Tensor memory holds S
@@ -39,6 +39,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kda_attn_internal.h"
 #include "kda_bulk.cuh"
 #include "kda_internal.h"
@@ -48,7 +50,7 @@ namespace kda {
 namespace {
 
 constexpr int kRows = 128, kKeys = 128;
-constexpr int kThreads = 384;
+constexpr int kThreads = 384;  // warps 10, 11 only give their registers to the softmax, which holds 128 scores
 constexpr uint32_t kTmem = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -65,7 +67,7 @@ struct Cfg {
 };
 
 struct Bars {
-    uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], k_full[4], k_empty[4], v_full[4], v_ready[4], v_empty[4], drain;
+    uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], k_full[4], k_empty[4], v_full[4], v_empty[4], v_fixed[4], drain;
 };
 
 // Instruction descriptor of kind::f16 with bf16 operands and fp32 accumulation;
@@ -125,18 +127,6 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t phase, vol
     return false;
 }
 
-// Whether `x` holds in any thread of a tile's four warps (named barrier `id`).
-__device__ __forceinline__ bool tile_any(int id, bool x) {
-    int r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\t"
-        "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"((int)x)
-        : "memory");
-    return r != 0;
-}
-
 // All lanes of a warp, with one answer.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, volatile int *abort_flag) {
     return __all_sync(~0u, wait_or_abort(bar, phase, abort_flag));
@@ -157,7 +147,7 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
     __shared__ Bars bars;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag, v_bad;
-    __shared__ volatile int two_terms[2];  // of the tile's P that is ready
+    __shared__ __align__(4) volatile unsigned char two_terms[2][4];  // by tile and warp: its P has a second term
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     const int kvh = (int)(blockIdx.x % (unsigned)p.Hkv);
@@ -177,6 +167,8 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
         nblk[t] = b > a ? (b + kKeys - 1) / kKeys : 0;
     }
     const int n = max(nblk[0], nblk[1]);
+    // the first block with a key that some row must not see; at most three more follow
+    const int diag = (a0 + 1) / kKeys;
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -189,7 +181,7 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
             mbar_init(&bars.k_full[i], 1);
             mbar_init(&bars.k_empty[i], 1);
             mbar_init(&bars.v_full[i], 1);
-            mbar_init(&bars.v_ready[i], 2);
+            mbar_init(&bars.v_fixed[i], 1);
             mbar_init(&bars.v_empty[i], 1);
         }
         mbar_init(&bars.drain, 1);
@@ -203,39 +195,72 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
     tc::fence_after_sync();
     const uint32_t tm = tmem_base;
 
+    // 168 registers a thread at launch: 2 x 128 x 208 + 128 x 88 = 384 x 168
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 9) {
             // ---------------- loads
-            if (lane == 0) {
-                const int box = TT * p.G * 128;  // bytes of a Q box
-                auto load_q = [&](int t) {
-                    mbar_arrive_expect_tx(&bars.q_full[t], box * (HD / 64));
-                    for (int c = 0; c < HD / 64; ++c)
-                        tma_load_3d(sq + t * C::kTile + c * C::kChunk, &qmap, 64 * c, kvh * p.G, t0 + a0 + t * TT, &bars.q_full[t]);
-                };
-                auto load_kv = [&](unsigned char *dst, const CUtensorMap *map, int j, uint64_t *bar) {
-                    mbar_arrive_expect_tx(bar, C::kTile);
-                    for (int c = 0; c < HD / 64; ++c)
-                        tma_load_3d(dst + c * C::kChunk, map, 64 * c, kvh, t0 + j * kKeys, bar);
-                };
-                int jk = 0, jv = 0;
-                load_q(0);
-                for (int j = 0; j < n; ++j) {
-                    if (j >= C::NK && !wait_or_abort(&bars.k_empty[j % C::NK], (j / C::NK - 1), &abort_flag)) break;
-                    load_kv(sk + (j % C::NK) * C::kTile, &kmap, j, &bars.k_full[j % C::NK]);
-                    jk = j + 1;
-                    if (j == 0 && nblk[1] > 0) load_q(1);
-                    if (j >= C::NV && !wait_or_abort(&bars.v_empty[j % C::NV], (j / C::NV - 1), &abort_flag)) break;
-                    load_kv(sv + (j % C::NV) * C::kTile, &vmap, j, &bars.v_full[j % C::NV]);
-                    jv = j + 1;
-                }
-                // every load lands before the CTA's memory goes
-                mbar_wait_drain(&bars.q_full[0], 0);
-                if (nblk[1] > 0) mbar_wait_drain(&bars.q_full[1], 0);
-                for (int j = max(0, jk - C::NK); j < jk; ++j) mbar_wait_drain(&bars.k_full[j % C::NK], (j / C::NK) & 1u);
-                for (int j = max(0, jv - C::NV); j < jv; ++j) mbar_wait_drain(&bars.v_full[j % C::NV], (j / C::NV) & 1u);
+            const int box = TT * p.G * 128;  // bytes of a Q box
+            auto load_q = [&](int t) {
+                if (lane != 0) return;
+                mbar_arrive_expect_tx(&bars.q_full[t], box * (HD / 64));
+                for (int c = 0; c < HD / 64; ++c)
+                    tma_load_3d(sq + t * C::kTile + c * C::kChunk, &qmap, 64 * c, kvh * p.G, t0 + a0 + t * TT, &bars.q_full[t]);
+            };
+            auto load_kv = [&](unsigned char *dst, const CUtensorMap *map, int j, uint64_t *bar) {
+                if (lane != 0) return;
+                mbar_arrive_expect_tx(bar, C::kTile);
+                for (int c = 0; c < HD / 64; ++c) tma_load_3d(dst + c * C::kChunk, map, 64 * c, kvh, t0 + j * kKeys, bar);
+            };
+            int jk = 0, jv = 0;
+            bool ok = true;
+            load_q(0);
+            for (int j = 0; j < n && ok; ++j) {
+                ok = j < C::NK || warp_wait(&bars.k_empty[j % C::NK], j / C::NK - 1, &abort_flag);
+                if (!ok) break;
+                load_kv(sk + (j % C::NK) * C::kTile, &kmap, j, &bars.k_full[j % C::NK]);
+                jk = j + 1;
+                if (j == 0 && nblk[1] > 0) load_q(1);
+                ok = j < C::NV || warp_wait(&bars.v_empty[j % C::NV], j / C::NV - 1, &abort_flag);
+                if (!ok) break;
+                load_kv(sv + (j % C::NV) * C::kTile, &vmap, j, &bars.v_full[j % C::NV]);
+                jv = j + 1;
             }
+            // ---------------- values that some row must not see
+            for (int j = diag; j < n && ok; ++j) {
+                ok = warp_wait(&bars.v_full[j % C::NV], j / C::NV, &abort_flag);
+                if (!ok) break;
+                unsigned char *blk = sv + (j % C::NV) * C::kTile;
+                bool bad = false;
+#pragma unroll 4
+                for (int i = lane; i < C::kTile / 16; i += 32) {
+                    const int key = j * kKeys + ((i >> 3) & (kKeys - 1));
+                    uint4 *u = reinterpret_cast<uint4 *>(blk) + i;
+                    uint4 x = *u;
+                    const bool odd = nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w);
+                    if (key >= len) {
+                        *u = make_uint4(0, 0, 0, 0);
+                    } else if (key > a0 && odd) {
+                        bad = true;
+                        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+                            if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0x0000ffffu;
+                        }
+                        *u = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                if (bad) v_bad = 1;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.v_fixed[j - diag]);
+            }
+            // every load lands before the CTA's memory goes
+            mbar_wait_drain(&bars.q_full[0], 0);
+            if (nblk[1] > 0) mbar_wait_drain(&bars.q_full[1], 0);
+            for (int j = max(0, jk - C::NK); j < jk; ++j) mbar_wait_drain(&bars.k_full[j % C::NK], (j / C::NK) & 1u);
+            for (int j = max(0, jv - C::NV); j < jv; ++j) mbar_wait_drain(&bars.v_full[j % C::NV], (j / C::NV) & 1u);
         } else if (warp == 8) {
             // ---------------- products (the whole warp in step: see mma_f16_ss_warp)
             const uint32_t id_qk = idesc_bf16(128, 128, false), id_pv = idesc_bf16(128, HD, true);
@@ -253,7 +278,7 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
                 for (int ks = 0; ks < 8; ++ks)
                     tc::mma_f16_ts_warp(tm + C::kO + HD * t, tm + 128 * t + 8 * ks, desc_v(va + ks * 2048, C::kChunk), id_pv,
                                    (j > 0 || ks > 0) ? 1u : 0u);
-                if (__any_sync(~0u, two_terms[t])) {
+                if (__any_sync(~0u, *reinterpret_cast<volatile const int *>(&two_terms[t][0]) != 0)) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         tc::mma_f16_ts_warp(tm + C::kO + HD * t, tm + 128 * t + 64 + 8 * ks, desc_v(va + ks * 2048, C::kChunk),
@@ -269,17 +294,17 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
             }
             if (ok) tc::commit_warp(&bars.k_empty[0]);
             for (int j = 0; j < n && ok; ++j) {
+                // (what the loads bring is waited for while the softmax still runs)
+                ok = (j < diag ? warp_wait(&bars.v_full[j % C::NV], j / C::NV, &abort_flag)
+                               : warp_wait(&bars.v_fixed[j - diag], 0, &abort_flag)) &&
+                     (j + 1 >= n || warp_wait(&bars.k_full[(j + 1) % C::NK], (j + 1) / C::NK, &abort_flag));
                 for (int t = 0; t < 2 && ok; ++t) {
-                    if (j < nblk[t]) {
-                        // (what the loads bring is waited for while the tile's softmax still runs)
-                        ok = warp_wait(&bars.v_ready[j % C::NV], j / C::NV, &abort_flag) &&
-                             (j + 1 >= nblk[t] || warp_wait(&bars.k_full[(j + 1) % C::NK], (j + 1) / C::NK, &abort_flag)) &&
-                             warp_wait(&bars.p_full[t], j, &abort_flag);
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        pv(t, j);
-                        if (j + 1 < nblk[t]) qk(t, j + 1);
-                    }
+                    if (j >= nblk[t]) continue;
+                    ok = warp_wait(&bars.p_full[t], j, &abort_flag);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    pv(t, j);
+                    if (j + 1 < nblk[t]) qk(t, j + 1);
                 }
                 if (!ok) break;
                 tc::commit_warp(&bars.v_empty[j % C::NV]);
@@ -287,39 +312,6 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
             }
             tc::commit_warp(&bars.drain);  // every product is done before the memory goes
             __all_sync(~0u, mbar_wait_drain(&bars.drain, 0));
-        } else {
-            // ---------------- values that some row must not see
-            const int ft = tid - 320;  // 0..63
-            for (int j = 0; j < n; ++j) {
-                if (!warp_wait(&bars.v_full[j % C::NV], j / C::NV, &abort_flag)) break;
-                if (j * kKeys + kKeys - 1 > a0) {
-                    unsigned char *blk = sv + (j % C::NV) * C::kTile;
-                    bool bad = false;
-                    for (int i = ft; i < C::kTile / 16; i += 64) {
-                        const int key = j * kKeys + ((i >> 3) & 127);
-                        uint4 *u = reinterpret_cast<uint4 *>(blk) + i;
-                        if (key >= len) {
-                            *u = make_uint4(0, 0, 0, 0);
-                        } else if (key > a0) {
-                            uint4 x = *u;
-                            if (nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w)) {
-                                bad = true;
-                                uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
-                                    if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0x0000ffffu;
-                                }
-                                *u = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        }
-                    }
-                    if (bad) v_bad = 1;
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.v_ready[j % C::NV]);
-            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -334,7 +326,7 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int j = 0; j < nb; ++j) {
-            // (after a wait gave up the loop runs on, on garbage: the tile's warps meet at a barrier below)
+            // (after a wait gave up the loop runs on, on garbage, to its end)
             if (!warp_wait(&bars.s_full[t], j, &abort_flag)) ok = false;
             tc::fence_after_sync();
             float sc[4][32];
@@ -378,37 +370,37 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
                 }
             }
             const float use = m == -INFINITY ? 0.f : m;
-            // a weight above 1 / kShare of the sum (of which it is a part)?  The four
-            // warps of the tile decide together.
+            // a weight above 1 / kShare of the sum (of which it is a part)?
             const float top = ex2((fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) - use) * sl2);
-            const bool two = tile_any(1 + t, valid && top * (kShare - 1.f) > l);
+            const bool two = __any_sync(~0u, valid && top * (kShare - 1.f) > l);
             const float2 k2 = make_float2(sl2, sl2), b2 = make_float2(-use * sl2, -use * sl2);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            auto weights = [&](auto with_two) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t pk[16];
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t pk[16], rest[16];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    float2 x = fma2(make_float2(sc[i][2 * c], sc[i][2 * c + 1]), k2, b2);
-                    x.x = ex2(x.x);
-                    x.y = ex2(x.y);
-                    sum[c & 1] = add2(sum[c & 1], x);
-                    pk[c] = pack_bf16(x.x, x.y);
-                    sc[i][2 * c] = x.x;
-                    sc[i][2 * c + 1] = x.y;
+                    for (int c = 0; c < 16; ++c) {
+                        float2 x = fma2(make_float2(sc[i][2 * c], sc[i][2 * c + 1]), k2, b2);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        sum[c & 1] = add2(sum[c & 1], x);
+                        pk[c] = pack_bf16(x.x, x.y);
+                        // the second term: what the rounding left, or zero (another warp of
+                        // the tile may have one, and the product takes all rows)
+                        rest[c] = with_two ? pack_bf16(x.x - __uint_as_float(pk[c] << 16),
+                                                       x.y - __uint_as_float(pk[c] & 0xffff0000u))
+                                           : 0u;
+                    }
+                    tc::st16u(s_addr + 16 * i, pk);
+                    tc::st16u(s_addr + 64 + 16 * i, rest);
                 }
-                tc::st16u(s_addr + 16 * i, pk);
-                if (two) {  // what the rounding left
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        pk[c] = pack_bf16(sc[i][2 * c] - __uint_as_float(pk[c] << 16),
-                                          sc[i][2 * c + 1] - __uint_as_float(pk[c] & 0xffff0000u));
-                    tc::st16u(s_addr + 64 + 16 * i, pk);
-                }
-            }
+            };
+            if (two) weights(std::true_type{});
+            else weights(std::false_type{});
             tc::wait_st();
             tc::fence_before_sync();
-            if (row == 0) two_terms[t] = two;
+            if (lane == 0) two_terms[t][warp & 3] = two;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.p_full[t]);
             sum[0] = add2(sum[0], sum[1]);
