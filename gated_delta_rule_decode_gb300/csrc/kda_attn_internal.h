@@ -111,8 +111,7 @@ inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_
 }
 
 cudaError_t launch_attn_prefill(const AttnPrefillParams &p, int d, int dtype, cudaStream_t s);
-// Prompts on the tensor cores (bf16, d = 64 or 128).
-bool attn_prefill_tc_supported(int d, int dtype);
+// Prompts in bf16, on the tensor cores.
 cudaError_t launch_attn_prefill_tc(const AttnPrefillParams &p, int d, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheAppendParams &p, int d, int dtype, cudaStream_t s);
 size_t attn_decode_workspace_bytes(int Hq, int Hkv, int d, int dtype, int64_t batch, int D, int64_t max_pages,

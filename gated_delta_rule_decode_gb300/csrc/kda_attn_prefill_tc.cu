@@ -1,4 +1,4 @@
-// Causal attention over packed prompts on tcgen05 (bf16, d = 64 or 128).
+// Causal attention over packed prompts on tcgen05 (bf16).
 //
 //   S = Q K^T,  P = e^{scale (S - m)},  O = P V,  m and l = sum P per row
 //
@@ -60,7 +60,10 @@ constexpr float kShare = 4.f;  // weights above 1 / kShare of the row's sum take
 template <int HD>
 struct Cfg {
     static constexpr int kTile = 128 * HD * 2;           // bytes of a Q tile, a key block, a value block
-    static constexpr int kChunk = 128 * 128;             // 64 columns of it
+    // A tile's rows are swizzled pieces of 64 columns (32 where d is), one chunk of 128 rows after the other.
+    static constexpr int kCols = HD < 64 ? HD : 64, kRowBytes = 2 * kCols, kChunks = HD / kCols;
+    static constexpr int kChunk = 128 * kRowBytes;
+    static constexpr uint32_t kSwizzle = kRowBytes == 128 ? 2u : 4u;  // descriptor code of the 128- and 64-byte swizzle
     static constexpr int NK = HD == 128 ? 2 : 4, NV = HD == 128 ? 3 : 4;
     static constexpr int kBytes = 1024 + (2 + NK + NV) * kTile + 256;
     static constexpr int kO = 256;                       // tensor memory column of O (tile 0); S at 0 and 128
@@ -77,11 +80,26 @@ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) {
            ((uint32_t)(M >> 4) << 24);
 }
 
-// Descriptor of 16 rows (keys) of a value block: N (channels) contiguous, 128-byte
-// swizzle; 64-channel chunks kChunk bytes apart, 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_v(uint32_t saddr, uint32_t chunk_bytes) {
+// Shared-memory descriptors of one K = 16 step.  Operands with the contraction
+// contiguous (Q and K): step ks is 32 bytes of every row.  Values: 16 rows
+// (keys) with the channels contiguous; the chunks of channels lie kChunk apart.
+// 8-row groups follow one another in both.
+template <int HD>
+__device__ __forceinline__ uint64_t desc_of(uint32_t saddr, uint32_t chunk_bytes) {
+    using C = Cfg<HD>;
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(chunk_bytes >> 4) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+           ((uint64_t)(8 * C::kRowBytes >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)C::kSwizzle << 61);
+}
+template <int HD>
+__device__ __forceinline__ uint64_t desc_qk(uint32_t tile, int ks) {
+    using C = Cfg<HD>;
+    constexpr int kSteps = C::kRowBytes / 32;  // in a chunk
+    return desc_of<HD>(tile + (uint32_t)((ks / kSteps) * C::kChunk + (ks % kSteps) * 32), 16);
+}
+template <int HD>
+__device__ __forceinline__ uint64_t desc_v(uint32_t block, int ks) {
+    using C = Cfg<HD>;
+    return desc_of<HD>(block + (uint32_t)(ks * 16 * C::kRowBytes), C::kChunk);
 }
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const void *map, int x, int y, int z, uint64_t *bar) {
@@ -200,17 +218,17 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 9) {
             // ---------------- loads
-            const int box = TT * p.G * 128;  // bytes of a Q box
+            const int box = TT * p.G * C::kRowBytes;  // bytes of a Q box
             auto load_q = [&](int t) {
                 if (lane != 0) return;
-                mbar_arrive_expect_tx(&bars.q_full[t], box * (HD / 64));
-                for (int c = 0; c < HD / 64; ++c)
-                    tma_load_3d(sq + t * C::kTile + c * C::kChunk, &qmap, 64 * c, kvh * p.G, t0 + a0 + t * TT, &bars.q_full[t]);
+                mbar_arrive_expect_tx(&bars.q_full[t], box * C::kChunks);
+                for (int c = 0; c < C::kChunks; ++c)
+                    tma_load_3d(sq + t * C::kTile + c * C::kChunk, &qmap, C::kCols * c, kvh * p.G, t0 + a0 + t * TT, &bars.q_full[t]);
             };
             auto load_kv = [&](unsigned char *dst, const CUtensorMap *map, int j, uint64_t *bar) {
                 if (lane != 0) return;
                 mbar_arrive_expect_tx(bar, C::kTile);
-                for (int c = 0; c < HD / 64; ++c) tma_load_3d(dst + c * C::kChunk, map, 64 * c, kvh, t0 + j * kKeys, bar);
+                for (int c = 0; c < C::kChunks; ++c) tma_load_3d(dst + c * C::kChunk, map, C::kCols * c, kvh, t0 + j * kKeys, bar);
             };
             int jk = 0, jv = 0;
             bool ok = true;
@@ -234,7 +252,7 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
                 bool bad = false;
 #pragma unroll 4
                 for (int i = lane; i < C::kTile / 16; i += 32) {
-                    const int key = j * kKeys + ((i >> 3) & (kKeys - 1));
+                    const int key = j * kKeys + ((i / (C::kRowBytes / 16)) & (kKeys - 1));
                     uint4 *u = reinterpret_cast<uint4 *>(blk) + i;
                     uint4 x = *u;
                     const bool odd = nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w);
@@ -268,20 +286,19 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
                 const uint32_t qa = tc::smem_u32(sq + t * C::kTile), ka = tc::smem_u32(sk + (j % C::NK) * C::kTile);
 #pragma unroll
                 for (int ks = 0; ks < HD / 16; ++ks)
-                    tc::mma_f16_ss_warp(tm + 128 * t, tc::desc_tf32_kstep(qa, 128, ks), tc::desc_tf32_kstep(ka, 128, ks),
-                                   id_qk, ks > 0);
+                    tc::mma_f16_ss_warp(tm + 128 * t, desc_qk<HD>(qa, ks), desc_qk<HD>(ka, ks), id_qk, ks > 0);
                 tc::commit_warp(&bars.s_full[t]);
             };
             auto pv = [&](int t, int j) {
                 const uint32_t va = tc::smem_u32(sv + (j % C::NV) * C::kTile);
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                    tc::mma_f16_ts_warp(tm + C::kO + HD * t, tm + 128 * t + 8 * ks, desc_v(va + ks * 2048, C::kChunk), id_pv,
+                    tc::mma_f16_ts_warp(tm + C::kO + HD * t, tm + 128 * t + 8 * ks, desc_v<HD>(va, ks), id_pv,
                                    (j > 0 || ks > 0) ? 1u : 0u);
                 if (__any_sync(~0u, *reinterpret_cast<volatile const int *>(&two_terms[t][0]) != 0)) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        tc::mma_f16_ts_warp(tm + C::kO + HD * t, tm + 128 * t + 64 + 8 * ks, desc_v(va + ks * 2048, C::kChunk),
+                        tc::mma_f16_ts_warp(tm + C::kO + HD * t, tm + 128 * t + 64 + 8 * ks, desc_v<HD>(va, ks),
                                        id_pv, 1u);
                 }
                 tc::commit_warp(&bars.pv_done[t]);
@@ -458,10 +475,11 @@ bool make_map(CUtensorMap *map, const void *base, int d, int heads, int64_t toke
               int box_tokens) {
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+    const cuuint32_t box[3] = {(cuuint32_t)(d < 64 ? d : 64), (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
     const cuuint32_t elem[3] = {1, 1, 1};
     return tensor_map_encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
-                                  elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                  elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                  d < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -485,12 +503,11 @@ cudaError_t launch_tc(const AttnPrefillParams &p, cudaStream_t st) {
 
 }  // namespace
 
-bool attn_prefill_tc_supported(int d, int dtype) {
-    return dtype == KDA_DT_BF16 && (d == 64 || d == 128) && tensor_map_encode_fn() != nullptr;
-}
-
 cudaError_t launch_attn_prefill_tc(const AttnPrefillParams &p, int d, cudaStream_t st) {
-    return d == 128 ? launch_tc<128>(p, st) : launch_tc<64>(p, st);
+    if (tensor_map_encode_fn() == nullptr) return cudaErrorNotSupported;
+    if (d == 128) return launch_tc<128>(p, st);
+    if (d == 64) return launch_tc<64>(p, st);
+    return launch_tc<32>(p, st);
 }
 
 }  // namespace kda
