@@ -681,7 +681,7 @@ template <typename T, int HD>
 cudaError_t launch(const AttnDecodeParams &p, cudaStream_t st) {
     const Layout lay = make_layout(p.batch, p.D, p.Hq, p.Hkv, HD, sizeof(T) == 2 ? KDA_DT_BF16 : KDA_DT_F32, p.max_pages,
                                    p.weight_out != nullptr);
-    if (lay.items > 0x7fffffff) return cudaErrorInvalidValue;
+    if (lay.items > 0x7fffffff || (int64_t)p.max_pages * p.Hkv * lay.RB > 0x7fffffff) return cudaErrorInvalidValue;
     cudaError_t e;
     if (lay.MT == 0) e = launch_tc(p, lay, HD, st);
     else if (lay.NB == 1) e = launch_main<T, HD, 1, 1>(p, lay, st);

@@ -98,10 +98,10 @@ __device__ __forceinline__ Unit locate(const AttnDecodeParams &p, int HR, Cursor
         c.base = end;
         ++c.n;
     }
-    const int64_t rem = u - c.base;
+    const int rem = (int)(u - c.base);  // (a sequence's units fit 32 bits: checked by the launcher)
     r.n = c.n;
-    r.hr = r.pages > 0 ? (int)(rem / r.pages) : 0;
-    r.page = r.pages > 0 ? (int)(rem - (int64_t)r.hr * r.pages) : 0;
+    r.hr = r.pages > 0 ? rem / r.pages : 0;
+    r.page = r.pages > 0 ? rem - r.hr * r.pages : 0;
     return r;
 }
 

@@ -64,18 +64,9 @@ struct Bars {
     uint64_t s_full[2], p_full[2], pv_done, o_free, drain;
 };
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, int phase, volatile int *abort_flag) {
-    for (uint32_t it = 0; it < kWaitLimit; ++it) {
-        if (mbar_try_wait(bar, (uint32_t)phase & 1u)) return true;
-        if ((it & 255u) == 255u && *abort_flag) return false;
-    }
-    *abort_flag = 1;
-    return false;
-}
-
 // All lanes of a warp, with one answer.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, int phase, volatile int *abort_flag) {
-    return __all_sync(~0u, wait_or_abort(bar, phase, abort_flag));
+    return __all_sync(~0u, mbar_wait_or_abort(bar, (uint32_t)phase, abort_flag));
 }
 
 // The worker's range as tiles: each role walks them by itself, in the same order.
@@ -223,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
             if (first && item > 0 && !warp_wait(&bars.o_free, item - 1, &abort_flag)) return false;
             tc::fence_after_sync();
             const uint32_t va = tc::smem_u32(sv + b * C::kOp);
-#pragma unroll
+#pragma unroll 1
             for (int ks = 0; ks < 8; ++ks)  // 16 positions each; a page is one 128-byte-wide chunk of HD rows
                 tc::mma_f16_ts_warp(tm + C::kO, tm + C::kP + 64 * b + 8 * ks,
                                tc::desc_sw128(va + (uint32_t)((ks >> 2) * HD * 128 + (ks & 3) * 32)), id_pv,
@@ -241,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
             if (!ok) break;
             tc::fence_after_sync();
             const uint32_t ka = tc::smem_u32(sk + b * C::kOp);
-#pragma unroll
+#pragma unroll 1
             for (int ks = 0; ks < HD / 16; ++ks)
                 tc::mma_f16_ss_warp(tm + 128 * b, tc::desc_tf32_kstep(qa, 128, ks), tc::desc_tf32_kstep(ka, 128, ks), id_qk,
                                ks > 0);

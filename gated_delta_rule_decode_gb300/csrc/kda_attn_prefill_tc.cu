@@ -135,19 +135,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// A bounded wait that also gives up when another role has.
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t phase, volatile int *abort_flag) {
-    for (uint32_t it = 0; it < kWaitLimit; ++it) {
-        if (mbar_try_wait(bar, phase & 1u)) return true;
-        if ((it & 255u) == 255u && *abort_flag) return false;
-    }
-    *abort_flag = 1;
-    return false;
-}
-
 // All lanes of a warp, with one answer.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, volatile int *abort_flag) {
-    return __all_sync(~0u, wait_or_abort(bar, phase, abort_flag));
+    return __all_sync(~0u, mbar_wait_or_abort(bar, (uint32_t)phase, abort_flag));
 }
 
 __device__ __forceinline__ bool nonfinite2(uint32_t w) {

@@ -83,6 +83,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t phase) {
     return false;
 }
 
+// Bounded wait that also gives up when another role of the CTA has (and tells
+// them when it does).  Not unrolled: it is inlined at many places.
+__device__ __forceinline__ bool mbar_wait_or_abort(uint64_t *bar, uint32_t phase, volatile int *abort_flag) {
+#pragma unroll 1
+    for (uint32_t it = 0; it < kWaitLimit; ++it) {
+#ifdef KDA_WAIT_NONBLOCKING
+        if (mbar_test_wait(bar, phase & 1u)) return true;
+#else
+        if (mbar_try_wait(bar, phase & 1u)) return true;
+#endif
+        if ((it & 255u) == 255u && *abort_flag) return false;
+    }
+    *abort_flag = 1;
+    return false;
+}
+
 // Drain wait: phase `phase` must be the one of an operation that was issued
 // and not yet observed complete (a wait on a phase that nothing will complete
 // spins out the whole limit).
