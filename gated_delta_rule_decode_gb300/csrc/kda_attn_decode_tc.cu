@@ -252,9 +252,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
         while (ok && wk.next(p, HR)) {
             const int j = wk.tile;
             const int b = j & 1;
-            // the buffers' last readers: QK(j - 2) and PV(j - 2)
+            // the buffers' last readers are QK(j - 2) and PV(j - 2); the keys need not wait
+            // for the latter, so that QK(j) can be ready while softmax (j - 1) runs
             if (j >= 2) {
-                ok = warp_wait(&bars.k_free[b], (j >> 1) - 1, &abort_flag) && warp_wait(&bars.v_free[b], (j >> 1) - 1, &abort_flag);
+                ok = warp_wait(&bars.k_free[b], (j >> 1) - 1, &abort_flag) &&
+                     (!wk.first || warp_wait(&bars.v_free[b], (j >> 1) - 1, &abort_flag));
                 if (!ok) break;
             }
             if (wk.first) {
@@ -331,6 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.k_ready[b]);
             // values: 16 positions of a channel at a time
+            if (j >= 2) ok = warp_wait(&bars.v_free[b], (j >> 1) - 1, &abort_flag);
+            if (!ok) break;
             const int window0 = wk.un.len - p.D + 1;
 #pragma unroll 1
             for (int pg = 0; pg < 2; ++pg) {
