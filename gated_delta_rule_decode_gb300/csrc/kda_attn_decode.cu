@@ -35,6 +35,13 @@
 //    per channel, is there for this.)
 //  * Each page's product is accumulated from zero and added to the output in
 //    fp32 round-to-nearest, because the tensor cores truncate when they add.
+//
+// Measured (d = 128, bf16): 64 sequences of up to 32 768 positions, 32 heads
+// over 8, 369 us, 5.8 TB/s, with the rows as the 16-row operand 425; one
+// sequence of 102 400, 50 us (41 in this kernel, the rest the join), 7 pages a
+// worker.  Above 16 rows a warp's conversions are repeated by each of MT warps:
+// bf16 calls go to kda_attn_decode_tc.cu there (7 tokens x 8 heads, 32 sequences
+// of up to 8192: 207 us here, 108 there); fp32 and d = 32 stay.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -52,7 +59,10 @@ using namespace dec;
 
 // Warps per SM, by registers and by shared memory (the rings).
 __host__ __device__ constexpr int warps_per_sm(int NB) { return NB == 1 ? 12 : 8; }
-constexpr int kRounds = 4;  // workers per place on the GPU, at most
+// Workers per place on the GPU, at most, and the pages that make another round
+// worth its start-up.  1, 2, 4 and 8 rounds took 399, 397, 383 and 402 us for the
+// 64-sequence batch above.
+constexpr int kRounds = 4;
 constexpr int kPagesPerWorker = 12;
 constexpr float kPScale = 32768.f;  // fp16 scale of the weights
 

@@ -24,8 +24,12 @@
 // than 2^8, so they reach 2^15).  Value scales are powers of two and go into
 // the exponent of the weights, relative to the largest so far.
 //
-// Bound by HBM for long contexts; per tile the products take 1024 cycles of an
-// SM, the bytes 1400.
+// Per tile the products take 1040 cycles of an SM and the bytes 1400, but two
+// tiles in flight take about 2 x 5000: the chain conversion - QK - softmax - PV
+// is what bounds it, and within it instruction fetch (five roles' code), which
+// is why loops are rolled where they can be (137 us unrolled, 114 rolled).
+// Measured: 7 tokens x 8 heads, 32 sequences of up to 8192, d = 128: 108 us,
+// 1.3 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>

@@ -10,7 +10,9 @@
 // x 4 keys and 4 rows x d / 16 channels; operands come from shared memory in
 // 16-byte pieces along the contraction, and pairs of products use the packed
 // fp32 instructions.  Tiles of 32 rows rather than 64 because the longest tile
-// of a call is its tail.  Bound by the fp32 units (4 d operations a score).
+// of a call is its tail (1537 tokens in 3 prompts, 8 heads, d = 64: 68 us, 96
+// with 64 rows and no copies ahead).  Bound by the fp32 units (4 d operations a
+// score) where tiles are many, here by the longest tile's 18 blocks.
 #include <stdint.h>
 
 #include "kda_attn_internal.h"
