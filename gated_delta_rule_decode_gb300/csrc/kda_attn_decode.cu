@@ -37,7 +37,7 @@
 //    fp32 round-to-nearest, because the tensor cores truncate when they add.
 //
 // Measured (d = 128, bf16): 64 sequences of up to 32 768 positions, 32 heads
-// over 8, 369 us, 5.8 TB/s, with the rows as the 16-row operand 425; one
+// over 8, 378 us, 5.7 TB/s; one
 // sequence of 102 400, 50 us (41 in this kernel, the rest the join), 7 pages a
 // worker.  Above 16 rows a warp's conversions are repeated by each of MT warps:
 // bf16 calls go to kda_attn_decode_tc.cu there (7 tokens x 8 heads, 32 sequences
@@ -59,11 +59,16 @@ using namespace dec;
 
 // Warps per SM, by registers and by shared memory (the rings).
 __host__ __device__ constexpr int warps_per_sm(int NB) { return NB == 1 ? 12 : 8; }
-// Workers per place on the GPU, at most, and the pages that make another round
-// worth its start-up.  1, 2, 4 and 8 rounds took 399, 397, 383 and 402 us for the
-// 64-sequence batch above.
-constexpr int kRounds = 4;
-constexpr int kPagesPerWorker = 12;
+// Short rows of the block table are not cut: a worker per item, no partial
+// results and no join.  That needs enough items to fill the GPU; with fewer,
+// the cut gives each a share of the SMs.  Cut and whole took, at 8 and at 16
+// pages: with 512 items of up to 8 rows 43.6 and 31.4, 58 and 48 us; with 128 of
+// them 23.2 and 27.3, 35.5 and 39.6; 64 items of kda_attn_decode_tc.cu 33.5 and
+// 21.1, 37.5 and 29.3. At 32 pages whole
+// still gains 3 to 16 % with that many items (77 and 74 us; 103 and 87), and its
+// longest item sets the time of a ragged batch, so the rule stops before.
+constexpr int64_t kWholePages = 16;
+constexpr int64_t kWholeItems = 512, kWholeItemsTc = 64;
 constexpr float kPScale = 32768.f;  // fp16 scale of the weights
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -144,7 +149,7 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
     fence_barrier_init();
 
     int64_t U, W, u0, u1;
-    find_range<T, HD, MT>(p, HR, warp_sum, &start, U, W, u0, u1);
+    find_range<T, HD, MT>(p, HR, lay.whole, warp_sum, &start, U, W, u0, u1);
     if (u0 >= u1) return;
     const int64_t count = u1 - u0;
 
@@ -535,7 +540,7 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
                 }
             }
         }
-        if (un.page == 0 && tid == 0) write_desc(ws, lay, un, cur, HR, whole, W, U);
+        if (un.page == 0 && tid == 0 && !lay.whole) write_desc(ws, lay, un, cur, HR, whole, W, U);
     }
     if (timeout && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_TIMEOUT);
     if (timeout && mt == 0)  // the copies in flight land before the CTA's memory goes
@@ -699,11 +704,15 @@ cudaError_t launch(const AttnDecodeParams &p, cudaStream_t st) {
     else if (lay.MT == 2) e = launch_main<T, HD, 2, 2>(p, lay, st);
     else e = launch_main<T, HD, 2, 4>(p, lay, st);
     if (e != cudaSuccess || p.max_pages == 0) return e;
-    int64_t rows = kJoinBlocks / lay.items;
-    rows = rows < 1 ? 1 : rows > lay.PR ? lay.PR : rows;
-    const dim3 grid((unsigned)lay.items, (unsigned)rows);
-    if (lay.workers > 8 * lay.items) e = launch_after(join_kernel<T, HD, 512>, grid, 512, st, p, lay);
-    else e = launch_after(join_kernel<T, HD, 128>, grid, 128, st, p, lay);
+    if (lay.whole) {
+        if (p.weight_out == nullptr) return cudaSuccess;
+    } else {
+        int64_t rows = kJoinBlocks / lay.items;
+        rows = rows < 1 ? 1 : rows > lay.PR ? lay.PR : rows;
+        const dim3 grid((unsigned)lay.items, (unsigned)rows);
+        if (lay.workers > 8 * lay.items) e = launch_after(join_kernel<T, HD, 512>, grid, 512, st, p, lay);
+        else e = launch_after(join_kernel<T, HD, 128>, grid, 128, st, p, lay);
+    }
     if (e != cudaSuccess || p.weight_out == nullptr) return e;
     const int64_t blocks = (int64_t)p.batch * ((p.max_pages + 31) / 32);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
@@ -735,18 +744,21 @@ Layout make_layout(int64_t batch, int D, int Hq, int Hkv, int d, int dtype, int6
     l.RB = (rows + l.R - 1) / l.R;
     l.PR = rows < l.R ? rows : l.R;
     l.items = batch * Hkv * l.RB;
-    // all places on the GPU once, or as many whole times as leave a worker kPagesPerWorker pages
+    // A worker per place on the GPU.  2 and 4 of them per place never took less and
+    // up to 1.6 times as much (same lengths for all): the 64-sequence batch above
+    // 378, 385 and 399 us, 48 sequences with windows of 4 tokens 168, 179 and 274.
     const int64_t units = l.items * max_pages, places = l.MT == 0 ? kSms : (int64_t)kSms * warps_per_sm(l.NB) / l.MT;
-    int64_t rounds = l.MT == 0 ? 1 : units / (places * kPagesPerWorker);
-    rounds = rounds < 1 ? 1 : rounds > kRounds ? kRounds : rounds;
-    l.workers = places * rounds < units ? places * rounds : units;
+    l.workers = places < units ? places : units;
     if (l.workers < 1) l.workers = 1;
+    l.whole = max_pages > 0 && l.items <= 0x7fffffff &&
+              (max_pages == 1 || (max_pages <= kWholePages && l.items >= (l.MT == 0 ? kWholeItemsTc : kWholeItems)));
     l.desc = 0;
     l.part_m = align64(2 * l.items);
     l.part_l = l.part_m + align64(2 * l.workers * l.PR);
     l.part_o = l.part_l + align64(2 * l.workers * l.PR);
     l.lse2 = l.part_o + align64(2 * l.workers * l.PR * d);
     l.page_w = l.lse2 + (with_weight ? align64(batch * D * Hq) : 0);
+    if (l.whole) l.workers = l.items;
     l.total = l.page_w + (with_weight ? align64(batch * D * Hq * max_pages) : 0);
     return l;
 }

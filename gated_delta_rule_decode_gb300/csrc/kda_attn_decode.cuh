@@ -27,6 +27,7 @@ struct Layout {
     int64_t items, workers;
     int32_t R, RB, PR;  // rows of an item, row blocks, rows of a partial result
     int32_t NB, MT;     // tiles of a worker of kda_attn_decode.cu; MT = 0: kda_attn_decode_tc.cu
+    int32_t whole;      // a worker per item: short rows of the block table, no item is cut, no join
 };
 
 Layout make_layout(int64_t batch, int D, int Hq, int Hkv, int d, int dtype, int64_t max_pages, bool with_weight);
@@ -122,16 +123,40 @@ __device__ __forceinline__ int mask_word(uint32_t &w, int pos, int left, int see
     return at;
 }
 
+// The rows of a sequence that sees nothing.
+template <typename T, int HD>
+__device__ __forceinline__ void write_empty(const AttnDecodeParams &p, int n, int tid, int threads) {
+    T *o = static_cast<T *>(p.out) + (int64_t)n * p.D * p.Hq * HD;
+    for (int64_t i = tid; i < (int64_t)p.D * p.Hq * HD / 2; i += threads) store2(o + 2 * i, 0.f, 0.f);
+    if (p.lse)
+        for (int i = tid; i < p.D * p.Hq; i += threads) p.lse[(int64_t)n * p.D * p.Hq + i] = -INFINITY;
+}
+
 // Finds the range [u0, u1) of worker blockIdx.x among the batch's U units and
 // the cursor of its start (in shared memory, after the call's barrier; unset
 // for an empty range).  W: the workers with a range, no more than units.  Also
 // writes the rows of sequences without pages, which have no unit.
 template <typename T, int HD, int WARPS>
-__device__ __forceinline__ void find_range(const AttnDecodeParams &p, int HR, int64_t *warp_sum, Cursor *start, int64_t &U,
-                                           int64_t &W, int64_t &u0, int64_t &u1) {
+__device__ __forceinline__ void find_range(const AttnDecodeParams &p, int HR, bool whole, int64_t *warp_sum, Cursor *start,
+                                           int64_t &U, int64_t &W, int64_t &u0, int64_t &u1) {
     constexpr int kThreads = 32 * WARPS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t w = blockIdx.x;
+    if (whole) {  // units are counted within the sequence
+        const int n = (int)(w / HR), hr = (int)(w % HR);
+        int len;
+        const int pages = pages_of(p, n, len);
+        U = W = 1;
+        u0 = (int64_t)hr * pages;
+        u1 = u0 + pages;
+        if (tid == 0) {
+            *start = Cursor{n, 0};
+            if (hr == 0 && p.err_flag && p.seq_lens[n] > p.max_pages * kPage) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
+        }
+        if (pages == 0 && hr == 0) write_empty<T, HD>(p, n, tid, kThreads);
+        __syncthreads();
+        return;
+    }
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int nb = min(tid * per, p.batch), ne = min(nb + per, p.batch);
     int64_t mine = 0;
@@ -167,11 +192,7 @@ __device__ __forceinline__ void find_range(const AttnDecodeParams &p, int HR, in
     }
     for (int n = blockIdx.x; n < p.batch; n += gridDim.x) {
         if (p.seq_lens[n] > 0 && p.max_pages > 0) continue;
-        T *o = static_cast<T *>(p.out) + (int64_t)n * p.D * p.Hq * HD;
-        for (int64_t i = tid; i < (int64_t)p.D * p.Hq * HD / 2; i += kThreads) store2(o + 2 * i, 0.f, 0.f);
-        for (int i = tid; i < p.D * p.Hq; i += kThreads) {
-            if (p.lse) p.lse[(int64_t)n * p.D * p.Hq + i] = -INFINITY;
-        }
+        write_empty<T, HD>(p, n, tid, kThreads);
     }
     __syncthreads();
 }

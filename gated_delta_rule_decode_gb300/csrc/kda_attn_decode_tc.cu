@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
         v_nan = 0;
     }
     int64_t U, W, u0, u1;
-    find_range<T, HD, kWarps>(p, HR, exchange, &start, U, W, u0, u1);
+    find_range<T, HD, kWarps>(p, HR, lay.whole, exchange, &start, U, W, u0, u1);
     if (u0 >= u1) return;
     if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, kTmem);
     tc::fence_before_sync();
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                     }
                 }
             }
-            if (from_start && tid == 0 && ok) write_desc(ws, lay, un, wk.cur, HR, whole, W, U);
+            if (from_start && tid == 0 && ok && !lay.whole) write_desc(ws, lay, un, wk.cur, HR, whole, W, U);
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.o_free);

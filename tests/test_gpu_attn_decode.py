@@ -82,6 +82,27 @@ def test_many_short_sequences():
     _check(*s, _run(*s, return_weight=True))
 
 
+@pytest.mark.parametrize("dtype,d,B,D,hq,hkv,longest", [
+    ("bf16", 128, 130, 1, 8, 4, 700),   # rows of up to 12 pages, 520 items: none is cut
+    ("f32", 64, 130, 4, 8, 4, 700),
+    ("bf16", 32, 130, 8, 12, 4, 500),   # 24 rows: two row tiles
+    ("bf16", 128, 17, 7, 32, 4, 900),   # 56 rows, 68 items
+    ("bf16", 64, 9, 16, 72, 4, 600),    # 288 rows: three row blocks
+    ("bf16", 128, 3, 7, 16, 2, 63),     # tables of one page
+    ("f32", 32, 3, 1, 2, 1, 63),
+])
+def test_short_rows_of_the_table_are_not_cut(dtype, d, B, D, hq, hkv, longest):
+    lens = [0, 1, longest] + [(37 * i) % (longest + 1) for i in range(B - 3)]
+    q, cache, n, table = _setup(lens, D, hq, hkv, d, dtype, seed=B + D)
+    if longest < 64:
+        table = table[:, :1].contiguous()
+    s = q, cache, n, table
+    got = _run(*s, return_weight=True)
+    _check(*s, got)
+    plain = _run(*s)  # without weights nothing follows the kernel
+    assert torch.equal(plain[0], got[0]) and torch.equal(plain[1], got[1])
+
+
 def test_scales_far_apart_between_pages():
     """Pages whose scales differ by many powers of two, in both orders."""
     for dtype in ("bf16", "f32"):
