@@ -24,8 +24,9 @@
 //    exact in fp16.  A query row is scaled by a power of two into fp16's
 //    range, which is exact for bf16 inputs (elements below 2^-28 of the row's
 //    largest are rounded); fp32 inputs take a second fp16 term for the rest.
-//    The weights e^{s - m} are scaled by 2^15, so that fp16 holds them down
-//    to 2^-39 of the largest; fp32 takes a second term here as well.
+//    The weights go into fp16 times their page's value scale, the row's largest
+//    such product in 2^14..2^15 (see kda_attn_decode.cuh), so that fp16 holds
+//    them down to 2^-39 of it; fp32 takes a second term here as well.
 //  * The contraction orders of both products are permuted so that a thread's
 //    operand bytes are contiguous 16-byte pieces: thread t of a quad holds
 //    channels 16 t.. of a key row and positions 16 t.. of a value channel,
@@ -247,6 +248,7 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
         }
         float o[NB][DT][4];
         float m[NB][2], l[NB][2];
+        int unit[NB][2];  // the exponent that o is counted in
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -257,9 +259,9 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
             for (int e = 0; e < 2; ++e) {
                 m[nb][e] = -INFINITY;
                 l[nb][e] = 0.f;
+                unit[nb][e] = kNoUnit;
             }
         }
-        float vref = 0.f;                      // the scale that o is counted in
         const int window0 = un.len - p.D + 1;  // first position that some row does not see
 
         for (int pi = 0; pi < pages_here; ++pi, ++i) {
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
             const int sk = (int)(ck % SL), sv = (int)(cv % SL);
             if (!warp_wait(full + sk, ck / SL)) { timeout = true; break; }
             const PageMeta pm = meta[i % kMeta];
-            const float vs = pm.vs;
+            const int vexp = exponent_of(pm.vs);
             const bool have = pm.block >= 0;
             const bool tail = pos0 + kPage > window0 || !have;
             float s[NB][4][4];
@@ -337,19 +339,13 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
                             if (!have || pos >= limit[nb][c & 1]) s[nb][ti][c] = -INFINITY;
                         }
             }
-            // o is counted in the largest value scale so far, the page's weights
-            // in units of 2^-15 of it: a power of two that goes into the exponent
-            const float vnew = fmaxf(vref, have ? vs : 0.f);
-            const float ratio = have ? vs / vnew : 1.f;
-            const int bias = 15 + (int)(__float_as_uint(ratio) >> 23) - 127;
-            const float unbias = __uint_as_float((uint32_t)(127 - (bias < -100 ? -100 : bias)) << 23);
-            const float vfix = vref > 0.f ? vref / vnew : 1.f;
-            vref = vnew;
             uint32_t pb[TERMS][NB][4][2];
             float alpha[NB][2];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 float f[2], use[2], rs[2];
+                float before[2];
+                int bias[2], to[2];  // of the weights' exponents: 2^15 stands for the largest contribution
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     f[e] = fmaxf(qs[nb][e] * pm.ks, 1e-37f);  // positive, so that -inf stays -inf
@@ -358,29 +354,39 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
                     for (int ti = 0; ti < 4; ++ti) mx = fmaxf(mx, fmaxf(s[nb][ti][e], s[nb][ti][2 + e]));
                     mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-                    const float mn = fmaxf(m[nb][e], mx * f[e]);
-                    use[e] = mn == -INFINITY ? 0.f : mn;
-                    alpha[nb][e] = ex2(m[nb][e] - use[e]);
-                    m[nb][e] = mn;
+                    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16)) * f[e];
+                    before[e] = m[nb][e];
+                    m[nb][e] = fmaxf(m[nb][e], mx);
+                    use[e] = m[nb][e] == -INFINITY ? 0.f : m[nb][e];
+                    to[e] = max(unit[nb][e] + __float2int_ru(fmaxf(before[e] - use[e], kFarBelow)), contribution(vexp, mx, use[e]));
+                    bias[e] = 15 + vexp - to[e];
+                    alpha[nb][e] = 1.f;
+                }
+                if (__any_sync(~0u, before[0] != m[nb][0] || before[1] != m[nb][1] || to[0] != unit[nb][0] || to[1] != unit[nb][1])) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 by = moved(before[e], use[e], unit[nb][e], to[e]);
+                        l[nb][e] *= by.x;
+                        alpha[nb][e] = by.y;
+                        unit[nb][e] = to[e];
+                    }
                 }
                 rs[0] = rs[1] = 0.f;
-                const float b0 = (float)bias - use[0], b1 = (float)bias - use[1];
-                if (bias < -45) {  // the sum apart: these weights may vanish next to the larger scale
+                const float b0 = (float)bias[0] - use[0], b1 = (float)bias[1] - use[1];
 #pragma unroll
-                    for (int ti = 0; ti < 4; ++ti)
+                for (int e = 0; e < 2; ++e)
+                    if (bias[e] < kApart) {  // the sum apart: these weights may vanish next to a larger contribution
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) rs[c & 1] += ex2(fmaf(s[nb][ti][c], f[c & 1], -use[c & 1]));
-                }
+                        for (int ti = 0; ti < 4; ++ti)
+                            rs[e] += ex2(fmaf(s[nb][ti][e], f[e], -use[e])) + ex2(fmaf(s[nb][ti][2 + e], f[e], -use[e]));
+                    }
 #pragma unroll
                 for (int ti = 0; ti < 4; ++ti) {
                     float w[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) w[c] = ex2(fmaf(s[nb][ti][c], f[c & 1], (c & 1) ? b1 : b0));
-                    if (bias >= -45) {
-                        rs[0] += w[0] + w[2];
-                        rs[1] += w[1] + w[3];
-                    }
+                    if (bias[0] >= kApart) rs[0] += w[0] + w[2];
+                    if (bias[1] >= kApart) rs[1] += w[1] + w[3];
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         const uint32_t x = pack_f16(w[2 * hf], w[2 * hf + 1]);
@@ -393,9 +399,8 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    if (bias >= -45) rs[e] *= unbias;
-                    l[nb][e] = fmaf(l[nb][e], alpha[nb][e], rs[e]);
-                    alpha[nb][e] *= vfix;
+                    if (bias[e] >= kApart) rs[e] *= pow2(-bias[e]);
+                    l[nb][e] += rs[e];
                 }
                 if (p.weight_out != nullptr) {  // the page's share, relative to the maximum so far
 #pragma unroll
@@ -485,12 +490,11 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
         if (i >= count) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
         // ---- the item's end
-        const float unit = vref * (1.f / kPScale);
         const bool whole = un.page == 0 && pages_here == un.pages;
         const int64_t slot = 2 * w + (un.page == 0 ? 1 : 0);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            float f[2];
+            float f[2], in[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float x = l[nb][e];
@@ -498,7 +502,8 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
                 x += __shfl_xor_sync(~0u, x, 8);
                 x += __shfl_xor_sync(~0u, x, 16);
                 const int r = row0 + 8 * nb + 2 * t + e;
-                f[e] = whole ? (x == 0.f ? 0.f : unit / x) : unit;
+                f[e] = x == 0.f ? 0.f : whole ? 1.f / x : 1.f;
+                in[e] = pow2(unit[nb][e]) * (1.f / kPScale);
                 if (r >= rows_all || g != 0) continue;
                 if (whole) {
                     const int64_t qrow = ((int64_t)un.n * p.D + r / p.G) * p.Hq + h * p.G + r % p.G;
@@ -519,8 +524,8 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
                 for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
-                        const float x0 = f[0] == 0.f ? 0.f : o[nb][dt][2 * hf] * f[0];
-                        const float x1 = f[1] == 0.f ? 0.f : o[nb][dt][2 * hf + 1] * f[1];
+                        const float x0 = f[0] == 0.f ? 0.f : o[nb][dt][2 * hf] * in[0] * f[0];
+                        const float x1 = f[1] == 0.f ? 0.f : o[nb][dt][2 * hf + 1] * in[1] * f[1];
                         const uint32_t y = transpose8x8(pack_bf16(x0, x1));
                         if (r < rows_all) *reinterpret_cast<uint32_t *>(dst + 16 * dt + 8 * hf) = y;
                     }
@@ -536,7 +541,7 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
                     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf)
-                            dst[16 * dt + 8 * hf + g] = f[e] == 0.f ? 0.f : o[nb][dt][2 * hf + e] * f[e];
+                            dst[16 * dt + 8 * hf + g] = f[e] == 0.f ? 0.f : o[nb][dt][2 * hf + e] * in[e] * f[e];
                 }
             }
         }

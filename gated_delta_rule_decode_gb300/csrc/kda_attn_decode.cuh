@@ -38,6 +38,43 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// 2^e up to 2^127, through fp32's subnormal values down to 0.
+__device__ __forceinline__ float pow2(int e) {
+    const uint32_t up = (uint32_t)(min(e, 127) + 127) << 23;
+    return __uint_as_float(e < -126 ? 0x800000u >> min(-126 - e, 31) : up);
+}
+
+// The exponent of a value scale (a power of two).
+__device__ __forceinline__ int exponent_of(float s) { return (int)(__float_as_uint(s) >> 23) - 127; }
+
+// How a row's output is counted.  The sum of its weights is taken relative to
+// the largest weight, e^m.  Its output is not: what a page gives is its weights
+// times its value scale, and the pages' scales may differ by any power of two
+// (one outlier sets a page's scale), so the largest weights and the largest
+// contributions may lie on different pages.  The output is counted in units of
+// e^m 2^unit, `unit` no less than the largest (exponent of the page's value
+// scale + log2 of its largest weight) so far; a page's fp16 weights are then
+// relative to the largest contribution and what is lost of them does not count.
+// Exponents are whole numbers, so the scaling is exact.
+constexpr int kNoUnit = -8192;    // nothing seen yet
+constexpr float kFarBelow = -4096.f;  // log2 of weights that are nothing
+// Below this bias of a page's weights their sum is taken apart: with it, those
+// that are 2^-100 of the largest and more still count in full.
+constexpr int kApart = -25;
+
+// log2 of the largest contribution of a page to a row, rounded up: its largest
+// weight is 2^(top - use).
+__device__ __forceinline__ int contribution(int scale_exp, float top, float use) {
+    return scale_exp + __float2int_ru(fmaxf(top - use, kFarBelow));
+}
+
+// The factors of sum and output when the maximum goes from m to use and the
+// unit from `unit` to `to` (no less than unit + the maximum's fall, rounded up).
+__device__ __forceinline__ float2 moved(float m, float use, int unit, int to) {
+    const float by = fmaxf(m - use, kFarBelow), whole = floorf(by), rest = ex2(by - whole);
+    return make_float2(rest * pow2((int)whole), rest * pow2((int)whole + unit - to));
+}
+
 // Four e4m3 bytes as two pairs of fp16 (exact).
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"

@@ -20,9 +20,10 @@
 //   warps 10-17  conversion; the query rows at an item's start
 //
 // The query rows are scaled by powers of two into fp16's range (exact for
-// bf16), the weights by 2^7 (the maximum is only moved when it grows by more
-// than 2^8, so they reach 2^15).  Value scales are powers of two and go into
-// the exponent of the weights, relative to the largest so far.
+// bf16).  Value scales are powers of two and go into the exponent of the weights,
+// which stand at 2^7 for the row's largest contribution (see kda_attn_decode.cuh);
+// maximum and unit are only moved when they grow by more than 2^8, so the weights
+// reach 2^15.
 //
 // Per tile the products take 1040 cycles of an SM and the bytes 1400, but two
 // tiles in flight take about 2 x 5000: the chain conversion - QK - softmax - PV
@@ -390,8 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
         float *mine = reinterpret_cast<float *>(exchange) + pg * 128 + r;
         const float *other = reinterpret_cast<float *>(exchange) + (pg ^ 1) * 128 + r;
         auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); };
-        float m = -INFINITY, l = 0.f, qs = 0.f, vref = 0.f;
-        int limit = 0;
+        float m = -INFINITY, l = 0.f, qs = 0.f;
+        int limit = 0, unit = kNoUnit;  // the exponent that O is counted in
         bool valid = false, ok = true;
         int64_t qrow = 0;
         while (wk.next(p, HR)) {
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                 qs = __uint_as_float((uint32_t)(127 - 14 + q_exp[wk.item & 1][r]) << 23) * p.scale * kLog2e;
                 m = -INFINITY;
                 l = 0.f;
-                vref = 0.f;
+                unit = kNoUnit;
             }
             float fix = 1.f, use = 0.f, f = 1.f, z = 0.f, unbias = 1.f;
             bool masked = false, apart = false;
@@ -427,28 +428,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                 }
             };
             if (active) {
-                // factor of the raw scores, and the exponent bias of the weights: O is
-                // counted in the largest value scale so far
-                float vs = 0.f, vnew = vref;
-                bool have = false;
+                // factor of the raw scores, and the exponents of both pages' value scales
+                int vexp[2];
+                bool has[2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const PageMeta e = meta[(wk.i + x) % kMeta];
-                    const bool hx = x < wk.pages && e.block >= 0;
-                    if (hx) vnew = fmaxf(vnew, e.vs);
-                    if (x == pg) {
-                        have = hx;
-                        f = hx ? fmaxf(qs * e.ks, 1e-37f) : 1.f;
-                        vs = e.vs;
-                    }
+                    has[x] = x < wk.pages && e.block >= 0;
+                    vexp[x] = exponent_of(e.vs);
+                    if (x == pg) f = has[x] ? fmaxf(qs * e.ks, 1e-37f) : 1.f;
                 }
-                const float ratio = have ? vs / vnew : 1.f;
-                const int e = kBias + (int)(__float_as_uint(ratio) >> 23) - 127;
-                apart = e < -45;
-                z = (float)e;
-                unbias = __uint_as_float((uint32_t)(127 - (e < -100 ? -100 : e)) << 23);
-                fix = vref > 0.f ? vref / vnew : 1.f;
-                vref = vnew;
+                const bool have = pg == 0 ? has[0] : has[1];
                 end = have ? limit - (un.page + pg) * kPage : 0;
                 masked = !have || (un.page + pg + 1) * kPage > un.len - p.D + 1;
                 // (read twice: the maximum first, then the weights)
@@ -464,18 +454,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                 mx *= f;
                 *mine = mx;
                 pair_sync();
-                mx = fmaxf(mx, *other);
+                const float theirs = *other;
                 pair_sync();
-                const float mnew = fmaxf(m, mx);
-                if (wk.first) {
-                    m = mnew;
-                } else if (mnew - m > kLazy || (m == -INFINITY && mnew > m)) {
-                    const float al = ex2(m - mnew);
-                    fix *= al;
-                    l *= al;
-                    m = mnew;
-                }
+                const float mnew = fmaxf(m, fmaxf(mx, theirs)), before = m;
+                const bool move = wk.first || mnew - m > kLazy || (m == -INFINITY && mnew > m);
+                if (move) m = mnew;
                 use = m == -INFINITY ? 0.f : m;
+                int most = kNoUnit;  // the tile's largest contribution
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (has[x]) most = max(most, contribution(vexp[x], x == pg ? mx : theirs, use));
+                int to = unit;
+                if (move) to += __float2int_ru(fmaxf(before - use, kFarBelow));
+                if (move || most > to + (int)kLazy) to = max(to, most);
+                if (!wk.first && (move || to != unit)) {
+                    const float2 by = moved(move ? before : use, use, unit, to);
+                    l *= by.x;
+                    fix = by.y;
+                }
+                unit = to;
+                const int e = have ? kBias + (pg == 0 ? vexp[0] : vexp[1]) - unit : 0;
+                apart = e < kApart;
+                z = (float)e;
+                unbias = pow2(-e);
                 z -= use;
             }
             if (j > 0 && !warp_wait(&bars.pv_done, j - 1, &abort_flag)) ok = false;
@@ -537,8 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                 const float l0 = pg == 0 ? l : *other, l1 = pg == 0 ? *other : l;
                 pair_sync();
                 const float total = l0 + l1;
-                const float unit = vref * (1.f / (float)(1 << kBias));
-                const float fo = whole ? (total == 0.f ? 0.f : unit / total) : unit;
+                const float in = pow2(unit) * (1.f / (float)(1 << kBias));
+                const float fo = total == 0.f ? 0.f : whole ? 1.f / total : 1.f;
                 const int64_t slot = 2 * (int64_t)blockIdx.x + (from_start ? 1 : 0);
                 T *dst = static_cast<T *>(p.out) + qrow * HD + pg * (HD / 2);
                 float *part = ws + lay.part_o + (slot * lay.PR + r) * HD + pg * (HD / 2);
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                     tc::wait_ld();
                     if (!valid || !ok) continue;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = fo == 0.f ? 0.f : o[e] * fo;
+                    for (int e = 0; e < 16; ++e) o[e] = fo == 0.f ? 0.f : o[e] * in * fo;
                     if (nan) {  // the NaN values that this row sees
                         asm volatile("" ::: "memory");
                         for (int pos = max(un.len - p.D + 1, 0); pos < limit; ++pos) {
