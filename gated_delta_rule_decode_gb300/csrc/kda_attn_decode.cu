@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
             amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
             // the row times 2^(14 - ex): its largest element in 2^14..2^15
             int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-            ex = ex < -100 ? -100 : ex > 126 ? 126 : ex;
+            ex = ex < -100 ? -100 : ex > 127 ? 127 : ex;  // (above 127: infinities and NaN stay what they are)
             const float mul = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
             const float back = __uint_as_float((uint32_t)(127 - 14 + ex) << 23) * p.scale * kLog2e;
 #pragma unroll
