@@ -26,9 +26,11 @@
 //
 // P in bf16 is rounded to 8 bits, which averages out over many keys but not
 // over few.  Where a weight of the block may exceed 1/4 of its row's sum so
-// far, the tile's P takes a second bf16 term (in the other half of the score
-// columns) and a second product: rows that one or a few keys dominate keep 16
-// bits.  Sums of P are taken in fp32 before rounding.
+// far, the row's P takes a second bf16 term (in the other half of the score
+// columns; zero for the tile's other rows) and the tile a second product: rows
+// that one or a few keys dominate keep 16 bits.  A row decides by its own
+// weights alone, so later tokens do not change its bits.  Sums of P are taken
+// in fp32 before rounding.
 //
 // Measured: 16 384 tokens, 16 heads over 2, d = 128: 879 us, 1.25 PFLOP/s (797
 // without second terms); 6021 tokens in 7 prompts, 32 heads over 8: 159 us.  The
@@ -384,7 +386,9 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
             const float use = m == -INFINITY ? 0.f : m;
             // a weight above 1 / kShare of the sum (of which it is a part)?
             const float top = ex2((fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) - use) * sl2);
-            const bool two = __any_sync(~0u, valid && top * (kShare - 1.f) > l);
+            const bool mine = top * (kShare - 1.f) > l;
+            const uint32_t keep = mine ? ~0u : 0u;
+            const bool two = __any_sync(~0u, valid && mine);
             const float2 k2 = make_float2(sl2, sl2), b2 = make_float2(-use * sl2, -use * sl2);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             auto weights = [&](auto with_two) {
@@ -398,10 +402,10 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
                         x.y = ex2(x.y);
                         sum[c & 1] = add2(sum[c & 1], x);
                         pk[c] = pack_bf16(x.x, x.y);
-                        // the second term: what the rounding left, or zero (another warp of
+                        // the second term: what the rounding left, or zero (another row of
                         // the tile may have one, and the product takes all rows)
                         rest[c] = with_two ? pack_bf16(x.x - __uint_as_float(pk[c] << 16),
-                                                       x.y - __uint_as_float(pk[c] & 0xffff0000u))
+                                                       x.y - __uint_as_float(pk[c] & 0xffff0000u)) & keep
                                            : 0u;
                     }
                     tc::st16u(s_addr + 16 * i, pk);
