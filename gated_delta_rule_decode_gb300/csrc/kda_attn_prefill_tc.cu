@@ -43,6 +43,12 @@
 // sequence's end are zeroed in shared memory, and a non-finite value is zeroed
 // and remembered; if there was one, the epilogue adds those values to exactly
 // the rows that see them.
+//
+// Infinite values that every row sees stay in the products, where the second
+// term (zero, or of either sign) would turn them into NaN.  An output that comes
+// out not finite although its row's sum is a number is therefore settled by the
+// values themselves: a warp that has one looks over the keys that all its rows
+// see.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -149,6 +155,35 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, volatil
 
 __device__ __forceinline__ bool nonfinite2(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// What the values of keys 0..last at 32 channels (v: key 0, the first of them)
+// make of the outputs of rows that see them all: +inf, -inf or NaN where some
+// are not finite.  By a whole warp; `number`: the row's sum of weights is one.
+__device__ __forceinline__ void settle(const __nv_bfloat16 *v, int64_t stride, int last, bool number, float (&o)[32]) {
+    const int lane = threadIdx.x & 31;
+    uint32_t seen = 0;  // of the lane's 8 channels: bits 0.. +inf, 8.. -inf, 16.. NaN
+#pragma unroll 1
+    for (int key = lane >> 2; key <= last; key += 8) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(v + key * stride + 8 * (lane & 3));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t h = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+            if ((h & 0x7f80u) == 0x7f80u) seen |= 1u << (e + ((h & 0x7fu) ? 16 : h >> 15 ? 8 : 0));
+        }
+    }
+#pragma unroll
+    for (int at = 4; at < 32; at <<= 1) seen |= __shfl_xor_sync(~0u, seen, at);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const uint32_t of = __shfl_sync(~0u, seen, u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const bool up = (of >> e) & 1u, down = (of >> (8 + e)) & 1u, nan = (of >> (16 + e)) & 1u;
+            if (number && (up || down || nan)) o[8 * u + e] = nan || (up && down) ? NAN : up ? INFINITY : -INFINITY;
+        }
+    }
 }
 
 template <int HD>
@@ -430,13 +465,21 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
             const int64_t orow = ((int64_t)(t0 + tok) * p.Hq + kvh * p.G + gi);
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + orow * HD;
             const bool bad = *reinterpret_cast<volatile int *>(&v_bad) != 0;
+            const bool number = valid && l > 0.f && l <= 3.402823466e38f;
 #pragma unroll 1
             for (int c = 0; c < HD; c += 32) {
-                float o[32];
+                __syncwarp();  // (the rows that are not written rejoin for the next load)
+                float o[32], zero[4] = {0.f, 0.f, 0.f, 0.f};
                 tc::ld32(o_addr + c, o);
                 tc::wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= inv;
+                for (int e = 0; e < 32; ++e) {
+                    o[e] *= inv;
+                    zero[e & 3] = fmaf(o[e], 0.f, zero[e & 3]);  // NaN where one is not finite
+                }
+                if (__any_sync(~0u, number && (zero[0] + zero[1]) + (zero[2] + zero[3]) != 0.f))
+                    settle(static_cast<const __nv_bfloat16 *>(p.v) + (int64_t)t0 * p.v_stride + (int64_t)kvh * HD + c,
+                           p.v_stride, a0, number, o);
                 if (!valid) continue;
                 if (bad) {  // the values that were set aside, for the rows that see them
                     for (int key = a0 + 1; key <= tok; ++key) {
