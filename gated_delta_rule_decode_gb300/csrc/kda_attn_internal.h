@@ -69,15 +69,23 @@ struct CacheEvictParams {
 // ceil(len / per) (extra >= 1) of them: the last s whose first unit is <= u, by
 // a 32-way search of a converged warp on cu_seqlens alone (two dependent reads
 // for 1024 sequences).  Also gives the unit's index within the sequence.
-// Reads cu[0..num_seqs - 1] only, whatever the offsets hold.
+// Reads cu[0..num_seqs] only, whatever the offsets hold.
+// Offsets that fall set KDA_DEVERR_SEQLENS where they are met.  All the units'
+// searches together miss none: a search compares the ends of the parts that it
+// narrows down, and while those do not fall, every part owns a unit and is
+// searched for it, down to the single sequences.
 __device__ __forceinline__ int seq_of_unit(const int32_t *cu, int num_seqs, int per, int extra, int64_t u,
-                                           int64_t &local) {
+                                           int32_t *err, int64_t &local) {
     const int lane = threadIdx.x & 31;
     int a = 0, n = num_seqs, first = 0;  // candidates a..a + n - 1, and the first unit of a
     do {
         const int step = (n + 31) / 32, m = a + lane * step;
         int64_t at = 0;
-        if (lane * step < n) at = (int64_t)(cu[m] / per) + (int64_t)m * extra;
+        if (lane * step < n) {
+            const int from = cu[m], to = cu[min(m + step, a + n)];
+            at = (int64_t)(from / per) + (int64_t)m * extra;
+            if (to < from && err) atomicOr(err, KDA_DEVERR_SEQLENS);
+        }
         const unsigned in = __ballot_sync(~0u, lane * step < n && (lane == 0 || at <= u));
         const int k = 31 - __clz(in);
         first = __shfl_sync(~0u, (int)(u - at), k);

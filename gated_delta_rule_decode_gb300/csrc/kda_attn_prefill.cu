@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads) prefill_fp32_kernel(const AttnPrefil
     // the last tiles of a sequence have the most keys: they start first
     const int64_t unit = (int64_t)((gridDim.x - 1 - blockIdx.x) / (unsigned)p.Hq);
     int64_t tile;
-    const int s = seq_of_unit(p.cu_seqlens, p.num_seqs, BM, 1, unit, tile);
+    const int s = seq_of_unit(p.cu_seqlens, p.num_seqs, BM, 1, unit, p.err_flag, tile);
     int t0, t1;
     if (!seq_range(p.cu_seqlens, s, p.total_tokens, p.err_flag, t0, t1)) return;
     if (tile < 0 || tile * BM >= t1 - t0) return;

@@ -204,7 +204,7 @@ prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap
     const int64_t unit = (int64_t)((gridDim.x - 1 - blockIdx.x) / (unsigned)p.Hkv);
     const int TT = kRows / p.G;  // tokens of a tile
     int64_t pair;
-    const int s = seq_of_unit(p.cu_seqlens, p.num_seqs, 2 * TT, 1, unit, pair);
+    const int s = seq_of_unit(p.cu_seqlens, p.num_seqs, 2 * TT, 1, unit, p.err_flag, pair);
     int t0, t1;
     if (!seq_range(p.cu_seqlens, s, p.total_tokens, p.err_flag, t0, t1)) return;
     const int len = t1 - t0;

@@ -127,7 +127,7 @@ struct PageRows {
 
 __device__ __forceinline__ bool page_of_unit(const CacheAppendParams &p, int64_t unit, PageRows &r) {
     int64_t c = 0;
-    const int s = seq_of_unit(p.cu_seqlens, p.num_seqs, kPage, 2, unit, c);
+    const int s = seq_of_unit(p.cu_seqlens, p.num_seqs, kPage, 2, unit, p.err_flag, c);
     int t0, t1;
     const int64_t start = p.start_pos[s];
     if (!seq_range(p.cu_seqlens, s, p.total_tokens, p.err_flag, t0, t1)) return false;

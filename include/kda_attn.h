@@ -94,6 +94,8 @@ KDA_API int kda_attn_prefill(const kda_attn_dims *dims, int32_t num_seqs, const 
  * Places past the sequence's new end are not written.  A page is written for
  * one sequence only in a call (a page shared between sequences is full).
  *
+ *   cu_seqlens  as in kda_attn_prefill; with offsets that set
+ *               KDA_DEVERR_SEQLENS some of the call's tokens are written, others not
  *   k, v        dtype [total_tokens][Hkv][d], tokens k_stride, v_stride apart
  *   start_pos   i32 [num_seqs], >= 0 (a negative one skips the sequence)
  *   block_table i32 [num_seqs][max_pages]
