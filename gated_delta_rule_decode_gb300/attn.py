@@ -7,6 +7,10 @@ and draft windows (:func:`decode`) and the eviction of its lightest pages
 functions check shapes, dtypes and devices, pass raw device pointers and the
 current CUDA stream, and raise ``KdaError`` on a negative status; all
 arithmetic runs in the library's kernels.
+
+What a call allocates (results and scratch) comes from the memory of the stream
+that it runs on, ``stream`` where that is given: use such results on another
+stream as any tensor of that stream (wait for it, ``record_stream``).
 """
 from __future__ import annotations
 
@@ -15,7 +19,7 @@ from typing import NamedTuple
 
 import torch
 
-from .kda import KdaError, _check, _dtype_code, _need, lib  # noqa: F401
+from .kda import KdaError, _check, _dtype_code, _empty, _need, lib  # noqa: F401
 
 PAGE_TOKENS = 64
 KDA_DEVERR_PAGE = 256
@@ -164,12 +168,12 @@ def prefill(q, k, v, cu_seqlens, out=None, *, lse=None, return_lse=False, scale=
     n = cu_seqlens.shape[0] - 1
     _ok(cu_seqlens, "cu_seqlens", (n + 1,), _I32T)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+        out = _empty((T, Hq, d), dt, q.device, stream)
     else:
         _ok(out, "out", (T, Hq, d), dt)
     if lse is None:
         if return_lse:
-            lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
+            lse = _empty((T, Hq), _F32, q.device, stream)
     else:
         _ok(lse, "lse", (T, Hq), _F32)
     dims = make_dims(Hq, Hkv, d, code, scale)
@@ -225,12 +229,12 @@ def decode(q, cache: KVCache, seq_lens, block_table, out=None, *, lse=None, retu
     _ok(seq_lens, "seq_lens", (B,), _I32T)
     _ok(block_table, "block_table", (B, width), _I32T)
     if out is None:
-        out = torch.empty((B, D, Hq, d), dtype=dt, device=q.device)
+        out = _empty((B, D, Hq, d), dt, q.device, stream)
     else:
         _ok(out, "out", (B, D, Hq, d), dt)
     if lse is None:
         if return_lse:
-            lse = torch.empty((B, D, Hq), dtype=_F32, device=q.device)
+            lse = _empty((B, D, Hq), _F32, q.device, stream)
     else:
         _ok(lse, "lse", (B, D, Hq), _F32)
     if weight_in is not None:
@@ -238,14 +242,12 @@ def decode(q, cache: KVCache, seq_lens, block_table, out=None, *, lse=None, retu
     if weight_out is not None:
         _ok(weight_out, "weight_out", (B, width), _F32)
     elif return_weight or weight_in is not None:
-        weight_out = torch.empty((B, width), dtype=_F32, device=q.device)
+        weight_out = _empty((B, width), _F32, q.device, stream)
     dims = make_dims(Hq, Hkv, d, code, scale)
     pd = ctypes.byref(dims)
     if workspace is None:
         need = _lib.kda_attn_decode_workspace_bytes(pd, B, D, width, 0 if weight_out is None else 1)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _empty((need,), torch.uint8, q.device, stream)
     else:
         need = workspace.numel() * workspace.element_size()
     _check(_lib.kda_attn_decode(pd, ctypes.byref(c), B, D, _ptr(q), qs, _ptr(seq_lens), _ptr(block_table), width,
@@ -270,8 +272,8 @@ def evict(seq_lens, block_table, weight, budget: int, sink: int = 1, recent: int
     if in_place:
         lens, table, w = seq_lens, block_table, weight
     else:
-        lens, table, w = torch.empty_like(seq_lens), torch.empty_like(block_table), torch.empty_like(weight)
-    freed, count = torch.empty_like(block_table), torch.empty_like(seq_lens)
+        lens, table, w = (_empty(t.shape, t.dtype, t.device, stream) for t in (seq_lens, block_table, weight))
+    freed, count = (_empty(t.shape, t.dtype, t.device, stream) for t in (block_table, seq_lens))
     _check(_lib.kda_cache_evict(B, width, int(budget), int(sink), int(recent), _ptr(seq_lens), _ptr(block_table),
                                 _ptr(weight), _ptr(lens), _ptr(table), _ptr(w), _ptr(freed), _ptr(count),
                                 _ptr(err_flag), _stream_handle(stream)), "kda_cache_evict")

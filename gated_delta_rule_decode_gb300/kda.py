@@ -170,6 +170,15 @@ def _stream_handle(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory of the stream that writes it: another stream's may still be in use
+    there, and may be handed out again before this one is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
     """Device scratch for one call; when the call runs on a stream other than
     the current one, the allocator is told so it is not reused too early."""
