@@ -5,6 +5,10 @@ device pointers and the current CUDA stream to the C ABI declared in
 ``include/kda.h``, and raises ``KdaError`` on a negative status.  All
 arithmetic runs in the library's CUDA kernels; there is no CPU or PyTorch
 fallback, and importing this module fails loudly if the library is missing.
+
+What a call allocates (results, records, scratch) comes from the memory of the
+stream that it runs on, ``stream`` where that is given: use such results on
+another stream as any tensor of that stream (wait for it, ``record_stream``).
 """
 from __future__ import annotations
 
@@ -180,12 +184,8 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
 
 
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """Device scratch for one call; when the call runs on a stream other than
-    the current one, the allocator is told so it is not reused too early."""
-    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+    """Device scratch for one call."""
+    return _empty((nbytes,), torch.uint8, device, stream)
 
 
 def _need(t: torch.Tensor, name: str, shape, dtype=None):
@@ -229,7 +229,7 @@ def decode(q, k, v, g, b, slot_ids, pool, out=None, *, eps=1e-6, scale=None,
         _need(t, name, shp, d)
     _need(pool, "pool", (pool.shape[0], H, dv, dk), torch.float32)
     if out is None:
-        out = torch.empty((B, H, dv), dtype=dt, device=q.device)
+        out = _empty((B, H, dv), dt, q.device, stream)
     _need(out, "out", (B, H, dv), dt)
     dims = make_dims(H, dk, dv, _dtype_code(q), eps, scale)
     args = (ctypes.byref(dims), B, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(b), _ptr(slot_ids),
@@ -263,7 +263,7 @@ def decode_fused(q, k, v, g, b, z, slot_ids, pool, conv_state, conv_w, norm_w, o
                             ("norm_w", norm_w, (dv,), torch.float32)):
         _need(t, name, shp, d)
     if out is None:
-        out = torch.empty((B, H, dv), dtype=dt, device=q.device)
+        out = _empty((B, H, dv), dt, q.device, stream)
     _need(out, "out", (B, H, dv), dt)
     dims = make_dims(H, dk, dv, _dtype_code(q), eps, scale)
     io = KdaFusedIo(conv_state.data_ptr(), conv_w.data_ptr(), z.data_ptr(), norm_w.data_ptr(),
@@ -305,7 +305,7 @@ def prefill_fused(q, k, v, g, b, z, cu_seqlens, slot_ids, pool, conv_state, conv
                             ("norm_w", norm_w, (dv,), torch.float32)):
         _need(t, name, shp, d)
     if out is None:
-        out = torch.empty((T, H, dv), dtype=dt, device=q.device)
+        out = _empty((T, H, dv), dt, q.device, stream)
     _need(out, "out", (T, H, dv), dt)
     code = _dtype_code(q)
     need = prefill_workspace_bytes(H, dk, dv, code, n, T)
@@ -323,13 +323,14 @@ def prefill_fused(q, k, v, g, b, z, cu_seqlens, slot_ids, pool, conv_state, conv
     return out
 
 
-def alloc_records(B, D, H, dk, dv, dtype, device):
-    """Allocate a ReplaySSM record set (dict of tensors) for (B, D)."""
+def alloc_records(B, D, H, dk, dv, dtype, device, stream=None):
+    """Allocate a ReplaySSM record set (dict of tensors) for (B, D), of the
+    memory of ``stream`` (the current one when omitted)."""
     return dict(
-        k_hat=torch.empty((B, D, H, dk), dtype=torch.float32, device=device),
-        v=torch.empty((B, D, H, dv), dtype=dtype, device=device),
-        g=torch.empty((B, D, H, dk), dtype=torch.float32, device=device),
-        beta=torch.empty((B, D, H), dtype=torch.float32, device=device))
+        k_hat=_empty((B, D, H, dk), torch.float32, device, stream),
+        v=_empty((B, D, H, dv), dtype, device, stream),
+        g=_empty((B, D, H, dk), torch.float32, device, stream),
+        beta=_empty((B, D, H), torch.float32, device, stream))
 
 
 def _records_struct(rec) -> KdaRecords:
@@ -361,10 +362,10 @@ def verify_record(q, k, v, g, b, slot_ids, pool, out=None, records=None, *,
         _need(t, name, shp, d)
     _need(pool, "pool", (pool.shape[0], H, dv, dk), torch.float32)
     if out is None:
-        out = torch.empty((B, D, H, dv), dtype=dt, device=q.device)
+        out = _empty((B, D, H, dv), dt, q.device, stream)
     _need(out, "out", (B, D, H, dv), dt)
     if records is None:
-        records = alloc_records(B, D, H, dk, dv, dt, q.device)
+        records = alloc_records(B, D, H, dk, dv, dt, q.device, stream)
     rs = _records_struct(records)
     dims = make_dims(H, dk, dv, _dtype_code(q), eps, scale)
     need = int(_lib.kda_verify_workspace_bytes(ctypes.byref(dims), B, D))
@@ -400,11 +401,12 @@ def replay_commit(records, num_accepted, slot_ids, pool, *, err_flag=None,
     _check(_lib.kda_replay_commit(*args), "kda_replay_commit")
 
 
-def alloc_records_u(B, D, H, dk, dv, device):
-    """Allocate a u-record set (dict of fp32 tensors) for (B, D)."""
-    return dict(k_hat=torch.empty((B, D, H, dk), dtype=torch.float32, device=device),
-                g=torch.empty((B, D, H, dk), dtype=torch.float32, device=device),
-                u=torch.empty((B, D, H, dv), dtype=torch.float32, device=device))
+def alloc_records_u(B, D, H, dk, dv, device, stream=None):
+    """Allocate a u-record set (dict of fp32 tensors) for (B, D), of the memory
+    of ``stream`` (the current one when omitted)."""
+    return dict(k_hat=_empty((B, D, H, dk), torch.float32, device, stream),
+                g=_empty((B, D, H, dk), torch.float32, device, stream),
+                u=_empty((B, D, H, dv), torch.float32, device, stream))
 
 
 def _records_u_struct(rec) -> KdaRecordsU:
@@ -422,10 +424,10 @@ def _verify_u_args(q, k, v, g, b, slot_ids, pool, out, records, workspace, eps, 
         _need(t, name, shp, d)
     _need(pool, "pool", (pool.shape[0], H, dv, dk), torch.float32)
     if out is None:
-        out = torch.empty((B, D, H, dv), dtype=dt, device=q.device)
+        out = _empty((B, D, H, dv), dt, q.device, stream)
     _need(out, "out", (B, D, H, dv), dt)
     if records is None:
-        records = alloc_records_u(B, D, H, dk, dv, q.device)
+        records = alloc_records_u(B, D, H, dk, dv, q.device, stream)
     dims = make_dims(H, dk, dv, _dtype_code(q), eps, scale)
     need = int(_lib.kda_verify_workspace_bytes(ctypes.byref(dims), B, D))
     if workspace is None and need > 0:
@@ -518,7 +520,7 @@ def prefill_chunked(q, k, v, g, b, cu_seqlens, slot_ids, pool, out=None, *,
         _need(t, name, shp, d)
     _need(pool, "pool", (pool.shape[0], H, dv, dk), torch.float32)
     if out is None:
-        out = torch.empty((T, H, dv), dtype=dt, device=q.device)
+        out = _empty((T, H, dv), dt, q.device, stream)
     _need(out, "out", (T, H, dv), dt)
     code = _dtype_code(q)
     need = prefill_workspace_bytes(H, dk, dv, code, n, T)
