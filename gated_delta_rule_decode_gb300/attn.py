@@ -87,18 +87,39 @@ def make_dims(q_heads: int, kv_heads: int, head_dim: int, dtype_code: int, scale
 # A small call's time is the host's, so the checks below take their quick way
 # first and look for what to say only when it fails.
 
-def _ok(t: torch.Tensor, name: str, shape: tuple, dtype):
-    """Checks a contiguous CUDA tensor."""
-    if not (t.is_cuda and t.shape == shape and t.dtype is dtype and t.is_contiguous()):
+def _gpu(t: torch.Tensor, name: str, stream) -> int:
+    """The GPU of a call's first tensor, which the call's stream has to be of:
+    the kernels run there, and every other tensor has to be there too."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    at = torch.cuda.current_device()
+    if dev != at or (stream is not None and stream.device_index != dev):
+        raise ValueError(f"{name} is on cuda:{dev}, the current GPU is cuda:{at}"
+                         + (f", the stream is of cuda:{stream.device_index}" if stream is not None else ""))
+    return dev
+
+
+def _elsewhere(t: torch.Tensor, name: str, dev: int):
+    if t.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call runs on cuda:{dev}")
+
+
+def _ok(t: torch.Tensor, name: str, shape: tuple, dtype, dev: int):
+    """Checks a contiguous tensor on GPU `dev`."""
+    if not (t.get_device() == dev and t.shape == shape and t.dtype is dtype and t.is_contiguous()):
+        _elsewhere(t, name, dev)
         _need(t, name, shape, dtype)
 
 
-def _rows(t: torch.Tensor, name: str, shape: tuple, dtype) -> int:
+def _rows(t: torch.Tensor, name: str, shape: tuple, dtype, dev: int) -> int:
     """Checks a tensor of token rows that may lie apart (a slice of a fused
     projection) and returns the distance between tokens in elements."""
     H, d = shape[-2], shape[-1]
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        _elsewhere(t, name, dev)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dtype:
@@ -125,23 +146,31 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_handle(stream):
+def _flag(err_flag, dev: int):
+    if err_flag is None:
+        return None
+    if err_flag.get_device() != dev or err_flag.dtype is not _I32T or err_flag.numel() < 1:
+        raise ValueError(f"err_flag must be an int32 tensor on cuda:{dev}")
+    return err_flag.data_ptr()
+
+
+def _stream_handle(stream, dev: int):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(dev)
     return torch.cuda.current_stream().cuda_stream
 
 
-def _check_cache(c: KVCache):
+def _check_cache(c: KVCache, dev: int):
     k, v, ks, vs = c
     N, Hkv, page, d = k.shape
     if page != PAGE_TOKENS:
         raise ValueError(f"k_pages has {page} positions per page, expected {PAGE_TOKENS}")
-    _ok(k, "k_pages", (N, Hkv, PAGE_TOKENS, d), _F8)
-    _ok(v, "v_pages", (N, Hkv, d, PAGE_TOKENS), _F8)
-    _ok(ks, "k_scale", (N, Hkv), _F32)
-    _ok(vs, "v_scale", (N, Hkv), _F32)
+    _ok(k, "k_pages", (N, Hkv, PAGE_TOKENS, d), _F8, dev)
+    _ok(v, "v_pages", (N, Hkv, d, PAGE_TOKENS), _F8, dev)
+    _ok(ks, "k_scale", (N, Hkv), _F32, dev)
+    _ok(vs, "v_scale", (N, Hkv), _F32, dev)
     return Hkv, d, KdaKvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), N)
 
 
@@ -164,21 +193,24 @@ def prefill(q, k, v, cu_seqlens, out=None, *, lse=None, return_lse=False, scale=
     T, Hq, d = q.shape
     Hkv, dt = k.shape[1], q.dtype
     code = _dtype_code(q)
-    qs, ks, vs = (_rows(q, "q", (T, Hq, d), dt), _rows(k, "k", (T, Hkv, d), dt), _rows(v, "v", (T, Hkv, d), dt))
+    dev = _gpu(q, "q", stream)
+    flag = _flag(err_flag, dev)
+    qs, ks, vs = (_rows(q, "q", (T, Hq, d), dt, dev), _rows(k, "k", (T, Hkv, d), dt, dev),
+                  _rows(v, "v", (T, Hkv, d), dt, dev))
     n = cu_seqlens.shape[0] - 1
-    _ok(cu_seqlens, "cu_seqlens", (n + 1,), _I32T)
+    _ok(cu_seqlens, "cu_seqlens", (n + 1,), _I32T, dev)
     if out is None:
         out = _empty((T, Hq, d), dt, q.device, stream)
     else:
-        _ok(out, "out", (T, Hq, d), dt)
+        _ok(out, "out", (T, Hq, d), dt, dev)
     if lse is None:
         if return_lse:
             lse = _empty((T, Hq), _F32, q.device, stream)
     else:
-        _ok(lse, "lse", (T, Hq), _F32)
+        _ok(lse, "lse", (T, Hq), _F32, dev)
     dims = make_dims(Hq, Hkv, d, code, scale)
     _check(_lib.kda_attn_prefill(ctypes.byref(dims), n, _ptr(cu_seqlens), T, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
-                                 _ptr(out), _ptr(lse), _ptr(err_flag), _stream_handle(stream)), "kda_attn_prefill")
+                                 _ptr(out), _ptr(lse), flag, _stream_handle(stream, dev)), "kda_attn_prefill")
     return (out, lse) if return_lse else out
 
 
@@ -189,17 +221,19 @@ def append(cache: KVCache, k, v, cu_seqlens, start_pos, block_table, *, err_flag
     k, v: [T, Hkv, d]; cu_seqlens: [n + 1] int32; start_pos: [n] int32;
     block_table: [n, max_pages] int32.
     """
-    Hkv, d, c = _check_cache(cache)
+    dev = _gpu(k, "k", stream)
+    flag = _flag(err_flag, dev)
+    Hkv, d, c = _check_cache(cache, dev)
     T, dt = k.shape[0], k.dtype
     code = _dtype_code(k)
-    ks, vs = _rows(k, "k", (T, Hkv, d), dt), _rows(v, "v", (T, Hkv, d), dt)
+    ks, vs = _rows(k, "k", (T, Hkv, d), dt, dev), _rows(v, "v", (T, Hkv, d), dt, dev)
     n, width = block_table.shape
-    _ok(cu_seqlens, "cu_seqlens", (n + 1,), _I32T)
-    _ok(start_pos, "start_pos", (n,), _I32T)
-    _ok(block_table, "block_table", (n, width), _I32T)
+    _ok(cu_seqlens, "cu_seqlens", (n + 1,), _I32T, dev)
+    _ok(start_pos, "start_pos", (n,), _I32T, dev)
+    _ok(block_table, "block_table", (n, width), _I32T, dev)
     dims = make_dims(Hkv, Hkv, d, code)
     _check(_lib.kda_cache_append(ctypes.byref(dims), ctypes.byref(c), n, _ptr(cu_seqlens), T, _ptr(k), ks, _ptr(v), vs,
-                                 _ptr(start_pos), _ptr(block_table), width, _ptr(err_flag), _stream_handle(stream)),
+                                 _ptr(start_pos), _ptr(block_table), width, flag, _stream_handle(stream, dev)),
            "kda_cache_append")
 
 
@@ -220,27 +254,29 @@ def decode(q, cache: KVCache, seq_lens, block_table, out=None, *, lse=None, retu
     page weights [B, max_pages] fp32: ``weight_in`` (zero without it) plus the
     attention weight that this call's rows gave to each page.
     """
-    Hkv, d, c = _check_cache(cache)
+    dev = _gpu(q, "q", stream)
+    flag = _flag(err_flag, dev)
+    Hkv, d, c = _check_cache(cache, dev)
     B, D, Hq, _ = q.shape
     dt = q.dtype
     code = _dtype_code(q)
-    qs = _rows(q, "q", (B, D, Hq, d), dt)
+    qs = _rows(q, "q", (B, D, Hq, d), dt, dev)
     width = block_table.shape[1]
-    _ok(seq_lens, "seq_lens", (B,), _I32T)
-    _ok(block_table, "block_table", (B, width), _I32T)
+    _ok(seq_lens, "seq_lens", (B,), _I32T, dev)
+    _ok(block_table, "block_table", (B, width), _I32T, dev)
     if out is None:
         out = _empty((B, D, Hq, d), dt, q.device, stream)
     else:
-        _ok(out, "out", (B, D, Hq, d), dt)
+        _ok(out, "out", (B, D, Hq, d), dt, dev)
     if lse is None:
         if return_lse:
             lse = _empty((B, D, Hq), _F32, q.device, stream)
     else:
-        _ok(lse, "lse", (B, D, Hq), _F32)
+        _ok(lse, "lse", (B, D, Hq), _F32, dev)
     if weight_in is not None:
-        _ok(weight_in, "weight_in", (B, width), _F32)
+        _ok(weight_in, "weight_in", (B, width), _F32, dev)
     if weight_out is not None:
-        _ok(weight_out, "weight_out", (B, width), _F32)
+        _ok(weight_out, "weight_out", (B, width), _F32, dev)
     elif return_weight or weight_in is not None:
         weight_out = _empty((B, width), _F32, q.device, stream)
     dims = make_dims(Hq, Hkv, d, code, scale)
@@ -249,10 +285,12 @@ def decode(q, cache: KVCache, seq_lens, block_table, out=None, *, lse=None, retu
         need = _lib.kda_attn_decode_workspace_bytes(pd, B, D, width, 0 if weight_out is None else 1)
         workspace = _empty((need,), torch.uint8, q.device, stream)
     else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
         need = workspace.numel() * workspace.element_size()
     _check(_lib.kda_attn_decode(pd, ctypes.byref(c), B, D, _ptr(q), qs, _ptr(seq_lens), _ptr(block_table), width,
                                 _ptr(out), _ptr(lse), _ptr(weight_in), _ptr(weight_out), _ptr(workspace), need,
-                                _ptr(err_flag), _stream_handle(stream)), "kda_attn_decode")
+                                flag, _stream_handle(stream, dev)), "kda_attn_decode")
     got = (out,) + ((lse,) if return_lse else ()) + ((weight_out,) if weight_out is not None else ())
     return got if len(got) > 1 else out
 
@@ -265,10 +303,12 @@ def evict(seq_lens, block_table, weight, budget: int, sink: int = 1, recent: int
     seq_lens: [B] int32; block_table: [B, max_pages] int32; weight:
     [B, max_pages] fp32.  With ``in_place`` these three are updated.
     """
+    dev = _gpu(seq_lens, "seq_lens", stream)
+    flag = _flag(err_flag, dev)
     B, width = block_table.shape
-    _ok(seq_lens, "seq_lens", (B,), _I32T)
-    _ok(block_table, "block_table", (B, width), _I32T)
-    _ok(weight, "weight", (B, width), _F32)
+    _ok(seq_lens, "seq_lens", (B,), _I32T, dev)
+    _ok(block_table, "block_table", (B, width), _I32T, dev)
+    _ok(weight, "weight", (B, width), _F32, dev)
     if in_place:
         lens, table, w = seq_lens, block_table, weight
     else:
@@ -276,5 +316,5 @@ def evict(seq_lens, block_table, weight, budget: int, sink: int = 1, recent: int
     freed, count = (_empty(t.shape, t.dtype, t.device, stream) for t in (block_table, seq_lens))
     _check(_lib.kda_cache_evict(B, width, int(budget), int(sink), int(recent), _ptr(seq_lens), _ptr(block_table),
                                 _ptr(weight), _ptr(lens), _ptr(table), _ptr(w), _ptr(freed), _ptr(count),
-                                _ptr(err_flag), _stream_handle(stream)), "kda_cache_evict")
+                                flag, _stream_handle(stream, dev)), "kda_cache_evict")
     return Evicted(lens, table, w, freed, count)
