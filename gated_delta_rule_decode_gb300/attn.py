@@ -162,6 +162,11 @@ def _stream_handle(stream, dev: int):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _like(t: torch.Tensor, stream) -> torch.Tensor:
+    """Memory like t's, of the call's stream (quicker than :func:`_empty`)."""
+    return torch.empty_like(t) if stream is None else _empty(t.shape, t.dtype, t.device, stream)
+
+
 def _check_cache(c: KVCache, dev: int):
     k, v, ks, vs = c
     N, Hkv, page, d = k.shape
@@ -312,8 +317,8 @@ def evict(seq_lens, block_table, weight, budget: int, sink: int = 1, recent: int
     if in_place:
         lens, table, w = seq_lens, block_table, weight
     else:
-        lens, table, w = (_empty(t.shape, t.dtype, t.device, stream) for t in (seq_lens, block_table, weight))
-    freed, count = (_empty(t.shape, t.dtype, t.device, stream) for t in (block_table, seq_lens))
+        lens, table, w = _like(seq_lens, stream), _like(block_table, stream), _like(weight, stream)
+    freed, count = _like(block_table, stream), _like(seq_lens, stream)
     _check(_lib.kda_cache_evict(B, width, int(budget), int(sink), int(recent), _ptr(seq_lens), _ptr(block_table),
                                 _ptr(weight), _ptr(lens), _ptr(table), _ptr(w), _ptr(freed), _ptr(count),
                                 flag, _stream_handle(stream, dev)), "kda_cache_evict")
