@@ -165,15 +165,7 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
             const Unit un = locate(p, HR, c, u0 + fetched + lane);
             const int h = un.hr / RB;
             const int id = p.block_table[(int64_t)un.n * p.max_pages + un.page];
-            PageMeta e{-1, 0.f, 0.f};
-            if (id >= 0 && id < p.num_pages) {
-                e.block = id * p.Hkv + h;
-                e.ks = p.k_scale[e.block];
-                e.vs = p.v_scale[e.block];
-            } else if (p.err_flag) {
-                atomicOr(p.err_flag, KDA_DEVERR_PAGE);
-            }
-            meta[(fetched + lane) % kMeta] = e;
+            meta[(fetched + lane) % kMeta] = page_meta(p, id, h);
         }
         const int from = (int)min((int64_t)31, count - 1 - fetched);
         fetch_cur.n = __shfl_sync(~0u, c.n, from);

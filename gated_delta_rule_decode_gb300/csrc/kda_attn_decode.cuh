@@ -120,6 +120,27 @@ struct PageMeta {
     int block;
     float ks, vs;
 };
+
+// A page that is not in the cache, or whose value scale is not a power of two
+// (only its exponent is used) or key scale not a positive number, counts as
+// unseen and sets the error flag.
+__device__ __forceinline__ PageMeta page_meta(const AttnDecodeParams &p, int id, int h) {
+    PageMeta e{-1, 0.f, 0.f};
+    int err = 0;
+    if (id >= 0 && id < p.num_pages) {
+        const int block = id * p.Hkv + h;
+        e.ks = p.k_scale[block];
+        e.vs = p.v_scale[block];
+        const uint32_t bits = __float_as_uint(e.vs);
+        const bool power = (bits & 0x7fffffu) == 0 && bits - 0x800000u < 0x7f000000u;  // 2^-126..2^127
+        if (power && e.ks > 0.f && e.ks <= 3.402823466e38f) e.block = block;
+        else err = KDA_DEVERR_SCALE;
+    } else {
+        err = KDA_DEVERR_PAGE;
+    }
+    if (err != 0 && p.err_flag) atomicOr(p.err_flag, err);
+    return e;
+}
 constexpr int kMeta = 64;  // entries per worker: two batches of 32 units
 
 struct Unit {

@@ -175,15 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                     const Unit un = locate(p, HR, c, u0 + fetched + lane);
                     const int h = un.hr / RB;
                     const int id = p.block_table[(int64_t)un.n * p.max_pages + un.page];
-                    PageMeta e{-1, 0.f, 0.f};
-                    if (id >= 0 && id < p.num_pages) {
-                        e.block = id * p.Hkv + h;
-                        e.ks = p.k_scale[e.block];
-                        e.vs = p.v_scale[e.block];
-                    } else if (p.err_flag) {
-                        atomicOr(p.err_flag, KDA_DEVERR_PAGE);
-                    }
-                    meta[(fetched + lane) % kMeta] = e;
+                    meta[(fetched + lane) % kMeta] = page_meta(p, id, h);
                 }
                 const int from = min(kBatch - 1, count - 1 - fetched);
                 fetch_cur.n = __shfl_sync(~0u, c.n, from);
@@ -555,9 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                     if (nan) {  // the NaN values that this row sees
                         asm volatile("" ::: "memory");
                         for (int pos = max(un.len - p.D + 1, 0); pos < limit; ++pos) {
-                            const int id = p.block_table[(int64_t)un.n * p.max_pages + pos / kPage];
-                            if (id < 0 || id >= p.num_pages) continue;
-                            const unsigned char *vb = p.v_pages + ((int64_t)id * p.Hkv + h) * C::kHalf +
+                            const int block = page_meta(p, p.block_table[(int64_t)un.n * p.max_pages + pos / kPage], h).block;
+                            if (block < 0) continue;
+                            const unsigned char *vb = p.v_pages + (int64_t)block * C::kHalf +
                                                       (pg * (HD / 2) + c) * kPage + pos % kPage;
 #pragma unroll
                             for (int e = 0; e < 16; ++e)

@@ -37,8 +37,11 @@ extern "C" {
 
 /* Further bits OR-ed into *err_flag. */
 enum {
-    KDA_DEVERR_PAGE = 256 /* a block-table entry outside 0..num_pages-1, or a
-                             sequence longer than its table row              */
+    KDA_DEVERR_PAGE = 256, /* a block-table entry outside 0..num_pages-1, or a
+                              sequence longer than its table row             */
+    KDA_DEVERR_SCALE = 512 /* a v_scale that is not a power of two in
+                              2^-126..2^127, or a k_scale that is not a
+                              positive number                                */
 };
 
 typedef struct kda_attn_dims {
@@ -117,8 +120,10 @@ KDA_API int kda_cache_append(const kda_attn_dims *dims, const kda_kv_cache *cach
  *   q           dtype [batch][draft_len][Hq][d], tokens q_stride apart
  *   seq_lens    i32 [batch], the window included
  *   block_table i32 [batch][max_pages]; an entry outside the cache sets
- *               KDA_DEVERR_PAGE and its positions count as unseen; of a
- *               sequence longer than its row the rest counts as unseen
+ *               KDA_DEVERR_PAGE and its positions count as unseen, as do
+ *               those of a page and head whose scales set
+ *               KDA_DEVERR_SCALE; a sequence longer than its row sets
+ *               KDA_DEVERR_PAGE and is taken to end with the row
  *   out         dtype [batch][draft_len][Hq][d]
  *   lse         f32 [batch][draft_len][Hq], natural log; may be NULL
  *   weight_out  f32 [batch][max_pages]; may be NULL.  Written with

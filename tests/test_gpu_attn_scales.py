@@ -3,6 +3,7 @@ the output keeps its precision whatever the ratio of the pages' value scales."""
 import math
 
 import pytest
+import torch
 
 from test_gpu_attn_decode import _check, _run, _setup
 
@@ -64,3 +65,32 @@ def test_the_same_where_sequences_are_cut(D, hq, hkv, d, dtype):
         else:
             got = _run(q, cache, n, table, return_weight=True)
         _check(q, cache, n, table, got)
+
+
+@pytest.mark.parametrize("D,hq,hkv,d,dtype", [(1, 8, 2, 64, "bf16"), (2, 4, 2, 32, "f32"), (7, 16, 2, 128, "bf16")])
+@pytest.mark.parametrize("of,scale", [(3, 0.75), (3, 1.5), (3, 0.0), (3, -0.5), (3, math.inf), (3, math.nan),
+                                      (3, 2.0 ** -127), (3, 3.4e38), (2, 0.0), (2, -1.0), (2, math.inf), (2, math.nan)])
+def test_scales_that_cannot_be_used_are_flagged(D, hq, hkv, d, dtype, of, scale):
+    """Value scales (3) are used by their exponent, key scales (2) as a factor: a
+    page and head with another counts as unseen."""
+    from gated_delta_rule_decode_gb300 import attn
+    q, cache, n, table = _setup([300, 130], D, hq, hkv, d, dtype, seed=44)
+    page, h = int(table[0, 2]), 1
+    good = cache[of][page, h].item()
+    cache[of][page, h] = scale
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = _run(q, cache, n, table, return_weight=True, err_flag=flag)
+    assert flag.item() == attn.KDA_DEVERR_SCALE
+    G = hq // hkv
+    cache[of][page, h] = good
+    seen, gone = _run(q, cache, n, table, return_weight=True), table.clone()
+    gone[0, 2] = -1
+    unseen = _run(q, cache, n, gone, return_weight=True)
+    for x, a, b in zip(got[:2], seen, unseen):  # the other head sees it
+        assert torch.equal(x[1], a[1])
+        assert torch.equal(x[0, :, :G], a[0, :, :G]) and torch.equal(x[0, :, G:], b[0, :, G:])
+    for extreme in (2.0 ** -126, 2.0 ** 100):
+        cache[3][page, h] = extreme
+        flag.zero_()
+        _check(q, cache, n, table, _run(q, cache, n, table, err_flag=flag))
+        assert flag.item() == 0
