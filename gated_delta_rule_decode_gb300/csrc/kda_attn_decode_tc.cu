@@ -538,6 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                 const bool nan = v_nan != 0;
 #pragma unroll 1
                 for (int c = 0; c < HD / 2; c += 16) {
+                    __syncwarp();  // (the rows that are not written rejoin for the next load)
                     float o[16];
                     tc::ld16(o_addr + c, o);
                     tc::wait_ld();
