@@ -20,12 +20,19 @@ namespace {
 // a CTA per task, which holds the page's rows in registers and turns values into
 // rows of positions through shared memory; decode steps take a CTA per page and
 // a warp per task, which goes over the one or few rows twice.  Measured: 32 355
-// tokens in 8 prompts, 8 heads, d = 128, 41.5 us, 4.8 TB/s, bound by the integer
+// tokens in 8 prompts, 8 heads, d = 128, 41.9 us, 4.7 TB/s, bound by the integer
 // pipe beside HBM; a token for each of 256 sequences 8.3 us, a chain of five
 // dependent reads (26.6 us with a CTA per task and bisection).
+//
+// The rule: at 1, 2, 4, 7, 8 and 16 tokens for each of 256 sequences (8 heads,
+// d = 128, cold caches) a CTA per task took 23, 23, 25, 27, 27 and 27 us, a warp
+// per task 11, 13, 17, 33, 29 and 50; for each of 64 both 11, 11 and 13 up to 4,
+// then 13 against 19; for each of 16, 8.9 throughout against 8.8, 8.8, 10.9, 19.
+// So 4.  The call knows the mean alone: 255 single tokens and a chunk of 500
+// (mean 3) take a warp per task 76 us, a CTA per task 23.
 constexpr int kAppendThreads = 128;
 constexpr int kStepWarps = 8;
-constexpr int64_t kFewTokens = 8;
+constexpr int64_t kFewTokens = 4;
 
 __device__ __forceinline__ float pow2_need(float amax) {
     // smallest e >= -126 with amax <= 1.75 * 2^8 * 2^e

@@ -23,7 +23,7 @@ def _case(lens, start, d, heads, dtype, seed, width=8):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d,heads", [(32, 3), (64, 2), (128, 5)])
-@pytest.mark.parametrize("each", [2, 7, 8])
+@pytest.mark.parametrize("each", [2, 3, 4, 7, 8])
 def test_windows(each, d, heads, dtype):
     """Windows that begin a page, end it and cross into the next."""
     start = [0, 1, 30, 57, 58, 59, 60, 61, 62, 63, 64, 121, 127]
@@ -32,17 +32,18 @@ def test_windows(each, d, heads, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_one_chunk_among_single_tokens(dtype):
-    lens = [1] * 40
-    lens[7] = 200
-    lens[20] = 0
-    _case(lens, [(13 * i) % 200 for i in range(40)], 64, 2, dtype, seed=61)
+    for n in (40, 80):  # a mean above and below 4: both kernels
+        lens = [1] * n
+        lens[7] = 200
+        lens[20] = 0
+        _case(lens, [(13 * i) % 200 for i in range(n)], 64, 2, dtype, seed=61)
 
 
 @pytest.mark.parametrize("n", [33, 65, 1100])
 @pytest.mark.parametrize("few", [True, False])
 def test_many_sequences(n, few):
     lens = [(5 * i) % 4 if few else (29 * i) % 40 for i in range(n)]  # empty ones among them
-    assert (sum(lens) <= 8 * n) == few
+    assert (sum(lens) <= 4 * n) == few
     _case(lens, [(17 * i) % 90 for i in range(n)], 32, 1, "bf16", seed=n, width=3)
 
 
