@@ -10,10 +10,8 @@
 //    one per worker, so ragged batches and single long sequences balance
 //    alike.  A worker is a CTA of MT warps; an item that a worker holds
 //    entirely is finished by it, one that is cut leaves partial results
-//    (o, m, l) that join_kernel adds up in a fixed order.  There are a few
-//    times as many workers as fit the GPU at once: SMs do not get the same
-//    share of the memory bandwidth, and those that are served faster take
-//    more of them.
+//    (o, m, l) that join_kernel adds up in a fixed order.  There is one worker
+//    per place on the GPU (see make_layout).
 //  * The G query heads of a kv head and the window's tokens are the rows of
 //    one tile, so a page is read once for all of them.
 //  * Each worker keeps a ring of shared-memory slots filled by bulk copies; a
@@ -38,11 +36,10 @@
 //    fp32 round-to-nearest, because the tensor cores truncate when they add.
 //
 // Measured (d = 128, bf16): 64 sequences of up to 32 768 positions, 32 heads
-// over 8, 378 us, 5.7 TB/s; one
-// sequence of 102 400, 50 us (41 in this kernel, the rest the join), 7 pages a
-// worker.  Above 16 rows a warp's conversions are repeated by each of MT warps:
-// bf16 calls go to kda_attn_decode_tc.cu there (7 tokens x 8 heads, 32 sequences
-// of up to 8192: 207 us here, 108 there); fp32 and d = 32 stay.
+// over 8, 381 us, 5.6 TB/s; one sequence of 102 400, 51 us (the join's share
+// about 9), 7 pages a worker.  Above 16 rows a warp's conversions are repeated by
+// each of MT warps: bf16 calls go to kda_attn_decode_tc.cu there (see
+// make_layout); fp32 and d = 32 stay.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -731,6 +728,12 @@ Layout make_layout(int64_t batch, int D, int Hq, int Hkv, int d, int dtype, int6
     auto align64 = [](int64_t x) { return (x + 63) / 64 * 64; };
     const int rows = D * (Hq / Hkv);
     Layout l{};
+    // On tcgen05 and on the warps' products, us at 20, 32, 40 and 64 rows of a kv head
+    // (same lengths): d = 128, 32 sequences of up to 8192 positions 99, 115, 105, 134 and
+    // 105, 126, 163, 211; 64 of up to 900 68, 68, 68, 64 and 81, 82, 109, 95; 8 of up to
+    // 2048 29, 29, 29, 31 and 38, 50, 54, 64.  d = 64: 83, 96, 87, 107 and 70, 86, 107,
+    // 146; 60, 60, 58, 56 and 52, 54, 74, 66; 25, 25, 27, 27 and 29, 40, 46, 54: up to
+    // 32 rows of 64 channels full batches would gain 10 to 20 %, small ones lose as much.
     if (dtype == KDA_DT_BF16 && d >= 64 && rows > 16) {
         l.R = 128;
     } else {
