@@ -24,7 +24,6 @@ from .kda import KdaError, _check, _dtype_code, _empty, _need, lib  # noqa: F401
 PAGE_TOKENS = 64
 KDA_DEVERR_PAGE = 256
 KDA_DEVERR_SCALE = 512
-MAX_DRAFT = 16
 
 EXPORTED = ("kda_attn_prefill", "kda_cache_append", "kda_attn_decode", "kda_attn_decode_workspace_bytes",
             "kda_cache_evict")

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "kda_attn_internal.h"
+#include "kda_attn_math.cuh"
 #include "kda_bulk.cuh"
 
 namespace kda {
@@ -31,12 +32,6 @@ struct Layout {
 };
 
 Layout make_layout(int64_t batch, int D, int Hq, int Hkv, int d, int dtype, int64_t max_pages, bool with_weight);
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // 2^e up to 2^127, through fp32's subnormal values down to 0.
 __device__ __forceinline__ float pow2(int e) {
@@ -91,10 +86,6 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t u) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 __device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
 __device__ __forceinline__ void store2(__nv_bfloat16 *p, float a, float b) {
     *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(a, b);

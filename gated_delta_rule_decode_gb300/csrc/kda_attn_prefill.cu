@@ -16,21 +16,13 @@
 #include <stdint.h>
 
 #include "kda_attn_internal.h"
+#include "kda_attn_math.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int BM = 32, BN = 64, kThreads = 128;
 constexpr int RM = 4;  // rows of a thread
-
-__device__ __forceinline__ float2 fma2(const float2 &a, const float2 &b, const float2 &c) {
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(*reinterpret_cast<uint64_t *>(&d))
-        : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)),
-          "l"(*reinterpret_cast<const uint64_t *>(&c)));
-    return d;
-}
 
 template <int HD>
 struct Tiles {
