@@ -122,9 +122,7 @@ __device__ __forceinline__ PageMeta page_meta(const AttnDecodeParams &p, int id,
         const int block = id * p.Hkv + h;
         e.ks = p.k_scale[block];
         e.vs = p.v_scale[block];
-        const uint32_t bits = __float_as_uint(e.vs);
-        const bool power = (bits & 0x7fffffu) == 0 && bits - 0x800000u < 0x7f000000u;  // 2^-126..2^127
-        if (power && e.ks > 0.f && e.ks <= 3.402823466e38f) e.block = block;
+        if (power_of_two(e.vs) && e.ks > 0.f && e.ks <= 3.402823466e38f) e.block = block;
         else err = KDA_DEVERR_SCALE;
     } else {
         err = KDA_DEVERR_PAGE;

@@ -105,6 +105,13 @@ __device__ __forceinline__ bool seq_range(const int32_t *cu, int s, int64_t tota
     return false;
 }
 
+// A scale that the cache's arithmetic by exponents can use: a power of two in
+// 2^-126..2^126, whose inverse is one too.
+__device__ __forceinline__ bool power_of_two(float s) {
+    const uint32_t bits = __float_as_uint(s);
+    return (bits & 0x7fffffu) == 0 && bits - 0x800000u < 0x7e800000u;
+}
+
 // Raises a kernel's dynamic shared memory limit on the current device, once per
 // device (`done`: a static of the caller, one per kernel).
 inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &done) {

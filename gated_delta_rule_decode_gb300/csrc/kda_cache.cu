@@ -43,7 +43,7 @@ __device__ __forceinline__ float pow2_need(float amax) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// 1 / s for a power of two s in 2^-126..2^120.
+// 1 / s for a power of two s in 2^-126..2^126.
 __device__ __forceinline__ float pow2_inverse(float s) {
     const uint32_t e = __float_as_uint(s) >> 23;
     return __uint_as_float((254u - e) << 23);
@@ -156,6 +156,13 @@ __device__ __forceinline__ bool page_ok(const CacheAppendParams &p, int64_t page
     return false;
 }
 
+// The scale of a page's earlier positions (0 where it has none).
+__device__ __forceinline__ bool scale_ok(const CacheAppendParams &p, int off, float old) {
+    if (off == 0 || power_of_two(old)) return true;
+    if (p.err_flag && (threadIdx.x & 31) == 0) atomicOr(p.err_flag, KDA_DEVERR_SCALE);
+    return false;
+}
+
 // Rescales the page's first `off` positions; threads tid of n.
 template <int HD>
 __device__ __forceinline__ void rescale_rows(unsigned char *dst, bool is_v, int off, float ratio, int tid, int n) {
@@ -198,6 +205,7 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 8 : 5) append
     if (!page_ok(p, pr.page)) return;
     float *scale = (is_v ? p.v_scale : p.k_scale) + pr.page * p.Hkv + h;
     const float old = off > 0 ? *scale : 0.f;
+    if (!scale_ok(p, off, old)) return;
     uint32_t bits = 0;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
@@ -290,6 +298,7 @@ __global__ void __launch_bounds__(32 * kStepWarps) append_step_kernel(const Cach
         const T *src = static_cast<const T *>(is_v ? p.v : p.k) + pr.tok * stride + (int64_t)h * HD + piece * N;
         float *scale = (is_v ? p.v_scale : p.k_scale) + pr.page * p.Hkv + h;
         const float old = off > 0 ? *scale : 0.f;
+        if (!scale_ok(p, off, old)) continue;
         float amax = 0.f;
         for (int r = r0; r < pr.rows; r += RW) amax = fmaxf(amax, piece_max<T>(*reinterpret_cast<const uint4 *>(src + r * stride)));
 #pragma unroll

@@ -39,9 +39,9 @@ extern "C" {
 enum {
     KDA_DEVERR_PAGE = 256, /* a block-table entry outside 0..num_pages-1, or a
                               sequence longer than its table row             */
-    KDA_DEVERR_SCALE = 512 /* a v_scale that is not a power of two in
-                              2^-126..2^127, or a k_scale that is not a
-                              positive number                                */
+    KDA_DEVERR_SCALE = 512 /* a scale that is not a power of two in
+                              2^-126..2^126 (a k_scale that is read: not a
+                              positive number)                               */
 };
 
 typedef struct kda_attn_dims {
@@ -103,7 +103,9 @@ KDA_API int kda_attn_prefill(const kda_attn_dims *dims, int32_t num_seqs, const 
  *   start_pos   i32 [num_seqs], >= 0 (a negative one skips the sequence)
  *   block_table i32 [num_seqs][max_pages]
  * A page outside the cache, or a row too short for the new end, sets
- * KDA_DEVERR_PAGE and that page's tokens are not written.
+ * KDA_DEVERR_PAGE and that page's tokens are not written; a scale of earlier
+ * positions that is no such power of two sets KDA_DEVERR_SCALE, and that page's
+ * keys (or values) of that head are not written.
  */
 KDA_API int kda_cache_append(const kda_attn_dims *dims, const kda_kv_cache *cache, int32_t num_seqs,
                              const int32_t *cu_seqlens, int64_t total_tokens, const void *k,

@@ -69,7 +69,7 @@ def test_the_same_where_sequences_are_cut(D, hq, hkv, d, dtype):
 
 @pytest.mark.parametrize("D,hq,hkv,d,dtype", [(1, 8, 2, 64, "bf16"), (2, 4, 2, 32, "f32"), (7, 16, 2, 128, "bf16")])
 @pytest.mark.parametrize("of,scale", [(3, 0.75), (3, 1.5), (3, 0.0), (3, -0.5), (3, math.inf), (3, math.nan),
-                                      (3, 2.0 ** -127), (3, 3.4e38), (2, 0.0), (2, -1.0), (2, math.inf), (2, math.nan)])
+                                      (3, 2.0 ** -127), (3, 2.0 ** 127), (3, 3.4e38), (2, 0.0), (2, -1.0), (2, math.inf), (2, math.nan)])
 def test_scales_that_cannot_be_used_are_flagged(D, hq, hkv, d, dtype, of, scale):
     """Value scales (3) are used by their exponent, key scales (2) as a factor: a
     page and head with another counts as unseen."""

@@ -54,3 +54,32 @@ def test_prompts_of_many_sequences(n, dtype, hq, hkv):
     q, k, v, cu = _inputs(lens, hq, hkv, 32, dtype, seed=n)
     out, lse = _attn().prefill(q.cuda(), k.cuda(), v.cuda(), cu.cuda(), return_lse=True)
     _check_prompt(q, k, v, cu, out, lse)
+
+
+@pytest.mark.parametrize("lens", [[1, 3, 2], [70, 64, 1]])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.75, 0.0, -1.0, float("inf"), float("nan"), 2.0 ** -127, 2.0 ** 127])
+def test_scales_of_earlier_positions_that_cannot_be_used(scale, dtype, lens):
+    """Flagged, and that page and head stay as they are; the scale of a page without earlier positions is free."""
+    a = _attn()
+    g = gen(91)
+    heads, d, width = 2, 64, 4
+    T = sum(lens)
+    cache = make_cache(g, 3 * width, heads, d)
+    k, v = randn(g, T, heads, d).to(DT[dtype]), randn(g, T, heads, d).to(DT[dtype])
+    table = torch.randperm(3 * width, generator=g).reshape(3, width).int()
+    cu, start = cu_of(lens), torch.tensor([5, 64, 100], dtype=torch.int32)
+    want = _want(cache, k, v, cu, start, table)
+    bad = [x.clone() for x in cache]
+    first, fresh, last = int(table[0, 0]), int(table[1, 1]), int(table[2, 1])
+    bad[2][first, 1] = scale  # keys of sequence 0's first page
+    bad[3][last, 0] = scale   # values of sequence 2's
+    bad[2][fresh], bad[3][fresh] = scale, scale
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = _append(bad, k, v, cu, start, table, err_flag=flag)
+    assert flag.item() == a.KDA_DEVERR_SCALE
+    for i, page, h in ((0, first, 1), (1, last, 0)):
+        assert torch.equal(got[i][page, h], cache[i][page, h])
+        assert torch.equal(got[i + 2][page, h].view(torch.int32), bad[i + 2][page, h].view(torch.int32))
+        got[i][page, h], got[i + 2][page, h] = torch.from_numpy(want[i])[page, h], float(want[i + 2][page, h])
+    _compare(got, want)
