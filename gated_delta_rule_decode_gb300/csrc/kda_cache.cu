@@ -20,7 +20,7 @@ namespace {
 // a CTA per task, which holds the page's rows in registers and turns values into
 // rows of positions through shared memory; decode steps take a CTA per page and
 // a warp per task, which goes over the one or few rows twice.  Measured: 32 355
-// tokens in 8 prompts, 8 heads, d = 128, 41.9 us, 4.7 TB/s, bound by the integer
+// tokens in 8 prompts, 8 heads, d = 128, 41.0 us, 4.8 TB/s, bound by the integer
 // pipe beside HBM; a token for each of 256 sequences 8.3 us, a chain of five
 // dependent reads (26.6 us with a CTA per task and bisection).
 //
