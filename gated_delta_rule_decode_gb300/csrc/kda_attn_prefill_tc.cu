@@ -32,9 +32,9 @@
 // weights alone, so later tokens do not change its bits.  Sums of P are taken
 // in fp32 before rounding.
 //
-// Measured: 16 384 tokens, 16 heads over 2, d = 128: 892 us, 1.23 PFLOP/s (of an
+// Measured: 16 384 tokens, 16 heads over 2, d = 128: 890 us, 1.24 PFLOP/s (of an
 // earlier 879, second terms were 82); 6021 tokens in 7 prompts, 32 heads over 8:
-// 167 us.  The chain softmax - PV - QK of a tile bounds it: about 2200 cycles of
+// 168 us.  The chain softmax - PV - QK of a tile bounds it: about 2200 cycles of
 // softmax and 1040 of products, against 2080 of products in the step of both tiles.
 //
 // Masked values: a weight of zero times a NaN or an infinity would poison a
