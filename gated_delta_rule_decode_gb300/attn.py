@@ -3,7 +3,11 @@
 Attention over packed prompts (:func:`prefill`), an 8-bit paged key/value
 cache (:class:`KVCache`, :func:`append`), attention over it for single tokens
 and draft windows (:func:`decode`) and the eviction of its lightest pages
-(:func:`evict`), as declared in ``include/kda_attn.h``.  As in :mod:`kda`,
+(:func:`evict`); in front of them the norm and rotation of queries and keys
+(:class:`Rotary`, :func:`norm_rotate`); for long contexts attention of batches
+that share prefixes (:func:`decode_shared`), and attention over the pages that
+a cheap score selects (:class:`KeySummary`, :func:`summarise`, :func:`select`,
+:func:`decode_selected`), as declared in ``include/kda_attn.h``.  As in :mod:`kda`,
 functions check shapes, dtypes and devices, pass raw device pointers and the
 current CUDA stream, and raise ``KdaError`` on a negative status; all
 arithmetic runs in the library's kernels.
@@ -15,6 +19,8 @@ stream as any tensor of that stream (wait for it, ``record_stream``).
 from __future__ import annotations
 
 import ctypes
+import math
+from fractions import Fraction
 from typing import NamedTuple
 
 import torch
@@ -26,7 +32,8 @@ KDA_DEVERR_PAGE = 256
 KDA_DEVERR_SCALE = 512
 
 EXPORTED = ("kda_attn_prefill", "kda_cache_append", "kda_attn_decode", "kda_attn_decode_workspace_bytes",
-            "kda_cache_evict")
+            "kda_cache_evict", "kda_norm_rotate", "kda_attn_decode_shared", "kda_attn_decode_shared_workspace_bytes",
+            "kda_cache_summarise", "kda_cache_select", "kda_cache_select_workspace_bytes", "kda_attn_decode_selected")
 
 
 class KdaAttnDims(ctypes.Structure):
@@ -37,6 +44,10 @@ class KdaAttnDims(ctypes.Structure):
 class KdaKvCache(ctypes.Structure):
     _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64)]
+
+
+class KdaKeySummary(ctypes.Structure):
+    _fields_ = [("bounds", ctypes.c_void_p), ("unit", ctypes.c_void_p)]
 
 
 class KVCache(NamedTuple):
@@ -55,8 +66,29 @@ class Evicted(NamedTuple):
     freed_count: torch.Tensor  # [B] int32
 
 
+class Rotary(NamedTuple):
+    """The rotation of :func:`norm_rotate` (see :func:`rotary`)."""
+    turns: torch.Tensor  # [rotary_dim / 2] int64: turns per position in units of 2^-64, modulo one
+    interleaved: bool = False  # pairs (2 i, 2 i + 1), else (i, i + rotary_dim / 2)
+    factor: float = 1.0  # of the rotated channels
+
+
+class KeySummary(NamedTuple):
+    """Per page, kv head and channel the largest and smallest key, in whole numbers of one unit."""
+    bounds: torch.Tensor  # [num_pages, Hkv, 2, d] int8
+    unit: torch.Tensor    # [num_pages, Hkv] fp32, a power of two
+
+
+class Selected(NamedTuple):
+    """The pages that :func:`select` chose for each kv head."""
+    seq_lens: torch.Tensor     # [B] int32: positions of the selected pages
+    block_table: torch.Tensor  # [B, Hkv, budget] int32, -1 behind the last
+    index: torch.Tensor        # [B, Hkv, budget] int32: places in the sequence's row, -1 behind the last
+
+
 _VP, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-_PD, _PC = ctypes.POINTER(KdaAttnDims), ctypes.POINTER(KdaKvCache)
+_F = ctypes.c_float
+_PD, _PC, _PS = ctypes.POINTER(KdaAttnDims), ctypes.POINTER(KdaKvCache), ctypes.POINTER(KdaKeySummary)
 
 
 def _declare(lib):
@@ -66,16 +98,25 @@ def _declare(lib):
                                     _VP, _VP]
     lib.kda_attn_decode_workspace_bytes.argtypes = [_PD, _I32, _I32, _I32, _I32]
     lib.kda_cache_evict.argtypes = [_I32, _I32, _I32, _I32, _I32] + [_VP] * 10
+    lib.kda_norm_rotate.argtypes = [_PD, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _I32, _I32, _F, _VP, _VP, _F, _VP, _I64, _VP,
+                                    _I64, _VP]
+    lib.kda_attn_decode_shared.argtypes = [_PD, _PC, _I32, _I32, _VP, _I64, _VP, _VP, _I32, _I32, _VP, _VP, _VP, _VP, _VP,
+                                           _SZ, _VP, _VP]
+    lib.kda_attn_decode_shared_workspace_bytes.argtypes = [_PD, _I32, _I32, _I32, _I32]
+    lib.kda_cache_summarise.argtypes = [_PD, _PC, _PS, _I32, _VP, _I64, _VP, _VP, _I32, _VP, _VP]
+    lib.kda_cache_select.argtypes = [_PD, _PS, _I64, _I32, _I32, _VP, _I64, _VP, _VP, _I32, _I32, _I32, _I32, _VP, _VP, _VP,
+                                     _VP, _SZ, _VP, _VP]
+    lib.kda_cache_select_workspace_bytes.argtypes = [_PD, _I32, _I32]
+    lib.kda_attn_decode_selected.argtypes = [_PD, _PC, _I32, _I32, _VP, _I64, _VP, _VP, _I32, _VP, _VP, _VP, _SZ, _VP, _VP]
     for name in EXPORTED:
-        getattr(lib, name).restype = ctypes.c_int
-    lib.kda_attn_decode_workspace_bytes.restype = _SZ
+        getattr(lib, name).restype = _SZ if name.endswith("_bytes") else ctypes.c_int
     return lib
 
 
 _lib = _declare(lib())
 
 
-_F32, _I32T, _F8 = torch.float32, torch.int32, torch.float8_e4m3fn
+_F32, _I32T, _F8, _I8, _I64T = torch.float32, torch.int32, torch.float8_e4m3fn, torch.int8, torch.int64
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -177,6 +218,22 @@ def _check_cache(c: KVCache, dev: int):
     _ok(ks, "k_scale", (N, Hkv), _F32, dev)
     _ok(vs, "v_scale", (N, Hkv), _F32, dev)
     return Hkv, d, KdaKvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), N)
+
+
+def _check_summary(s: KeySummary, pages: int, Hkv: int, d: int, dev: int):
+    _ok(s.bounds, "bounds", (pages, Hkv, 2, d), _I8, dev)
+    _ok(s.unit, "unit", (pages, Hkv), _F32, dev)
+    return KdaKeySummary(s.bounds.data_ptr(), s.unit.data_ptr())
+
+
+def _workspace(workspace, size, like: torch.Tensor, dev: int, stream):
+    """(the caller's workspace, or one of the call's stream of size() bytes; its bytes)"""
+    if workspace is None:
+        need = size()
+        return _empty((need,), torch.uint8, like.device, stream), need
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def alloc_cache(num_pages: int, kv_heads: int, head_dim: int, device="cuda") -> KVCache:
@@ -323,3 +380,210 @@ def evict(seq_lens, block_table, weight, budget: int, sink: int = 1, recent: int
                                 _ptr(weight), _ptr(lens), _ptr(table), _ptr(w), _ptr(freed), _ptr(count),
                                 flag, _stream_handle(stream, dev)), "kda_cache_evict")
     return Evicted(lens, table, w, freed, count)
+
+
+# 2^192 / (2 pi), rounded
+_TURN = 999031769477504631556283515717616693813654938713089696784
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, stretch: float = 1.0, trained: int | None = None,
+                       slow: float = 1.0, fast: float = 32.0) -> torch.Tensor:
+    """Angles per position, base^(-2 i / rotary_dim) for i < rotary_dim / 2, fp64 on the host.
+
+    ``stretch`` > 1 adapts them to a context that many times longer than the one
+    of the training: all are divided by it, or, where that one's length
+    ``trained`` is given, only those that turn less than ``slow`` times in it;
+    those that turn more than ``fast`` times stay, and between the two the share
+    that is divided falls linearly with the number of turns.
+    """
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError(f"rotary_dim must be even, not {rotary_dim}")
+    if not (base > 0 and stretch > 0):
+        raise ValueError("base and stretch must be positive")
+    f = torch.tensor([float(base) ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)], dtype=torch.float64)
+    if stretch == 1.0:
+        return f
+    if trained is None:
+        return f / stretch
+    if not 0 <= slow < fast:
+        raise ValueError("slow must be below fast")
+    keep = ((trained * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+    return f * keep + f / stretch * (1 - keep)
+
+
+def rotary(frequencies, *, interleaved: bool = False, factor: float = 1.0, device="cuda") -> Rotary:
+    """Lays out the rotation by ``frequencies`` (angles per position, one per pair of channels, on the host)."""
+    fixed = []
+    for f in torch.as_tensor(frequencies, dtype=torch.float64).tolist():
+        if not math.isfinite(f):
+            raise ValueError(f"frequency {f}")
+        whole = round(Fraction(f) * _TURN / (1 << 128)) % (1 << 64)
+        fixed.append(whole - (1 << 64) if whole >> 63 else whole)
+    return Rotary(torch.tensor(fixed, dtype=torch.int64, device=device), bool(interleaved), float(factor))
+
+
+def norm_rotate(q, k, positions, rotary: Rotary, q_out=None, k_out=None, *, q_weight=None, k_weight=None, eps=1e-6,
+                stream=None):
+    """Norm of each query and key head (where its weight is given), then the rotation by ``positions``.
+
+    q: [T, Hq, d]; k: [T, Hkv, d] (rows may lie apart, as slices of one
+    projection); positions: [T] int32; q_weight, k_weight: [d] fp32.  q_out and
+    k_out may lie apart too, and may be q and k themselves.  Returns (q_out, k_out).
+    """
+    T, Hq, d = q.shape
+    Hkv, dt = k.shape[1], q.dtype
+    code = _dtype_code(q)
+    dev = _gpu(q, "q", stream)
+    qs, ks = _rows(q, "q", (T, Hq, d), dt, dev), _rows(k, "k", (T, Hkv, d), dt, dev)
+    _ok(positions, "positions", (T,), _I32T, dev)
+    turns, interleaved, factor = rotary
+    _ok(turns, "turns", (turns.shape[0],), _I64T, dev)
+    if 2 * turns.shape[0] > d:
+        raise ValueError(f"the rotation is of {2 * turns.shape[0]} channels, the heads have {d}")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _ok(w, name, (d,), _F32, dev)
+    if q_out is None:
+        q_out, qo = _empty((T, Hq, d), dt, q.device, stream), Hq * d
+    else:
+        qo = _rows(q_out, "q_out", (T, Hq, d), dt, dev)
+    if k_out is None:
+        k_out, ko = _empty((T, Hkv, d), dt, q.device, stream), Hkv * d
+    else:
+        ko = _rows(k_out, "k_out", (T, Hkv, d), dt, dev)
+    dims = make_dims(Hq, Hkv, d, code)
+    _check(_lib.kda_norm_rotate(ctypes.byref(dims), T, _ptr(q), qs, _ptr(k), ks, _ptr(positions), _ptr(turns),
+                                2 * turns.shape[0], 1 if interleaved else 0, factor, _ptr(q_weight), _ptr(k_weight), eps,
+                                _ptr(q_out), qo, _ptr(k_out), ko, _stream_handle(stream, dev)), "kda_norm_rotate")
+    return q_out, k_out
+
+
+def decode_shared_workspace_bytes(q_heads, kv_heads, head_dim, dtype_code, batch, draft_len, max_pages, groups) -> int:
+    """Bytes of workspace that :func:`decode_shared` needs."""
+    dims = make_dims(q_heads, kv_heads, head_dim, dtype_code)
+    return _lib.kda_attn_decode_shared_workspace_bytes(ctypes.byref(dims), batch, draft_len, max_pages, groups)
+
+
+def _decode_args(q, cache, seq_lens, block_table, table_shape, out, lse, return_lse, stream):
+    """What the forms of :func:`decode` check and allocate alike."""
+    dev = _gpu(q, "q", stream)
+    Hkv, d, c = _check_cache(cache, dev)
+    B, D, Hq, _ = q.shape
+    dt = q.dtype
+    code = _dtype_code(q)
+    qs = _rows(q, "q", (B, D, Hq, d), dt, dev)
+    _ok(seq_lens, "seq_lens", (B,), _I32T, dev)
+    _ok(block_table, "block_table", table_shape(B, Hkv), _I32T, dev)
+    if out is None:
+        out = _empty((B, D, Hq, d), dt, q.device, stream)
+    else:
+        _ok(out, "out", (B, D, Hq, d), dt, dev)
+    if lse is None:
+        if return_lse:
+            lse = _empty((B, D, Hq), _F32, q.device, stream)
+    else:
+        _ok(lse, "lse", (B, D, Hq), _F32, dev)
+    return dev, c, (Hq, Hkv, d, code), qs, out, lse
+
+
+def decode_shared(q, cache: KVCache, seq_lens, block_table, group_start, shared_pages, out=None, *, lse=None,
+                  return_lse=False, workspace=None, scale=None, err_flag=None, stream=None):
+    """:func:`decode` for sequences that share prefixes, which are read once for all of them.
+
+    group_start: [groups + 1] int32: sequences group_start[g] to
+    group_start[g + 1] - 1 are a group; shared_pages: [groups] int32: so many
+    entries of their block table rows, from the first, name the same pages.
+    Returns out [B, D, Hq, d], then with ``return_lse`` lse [B, D, Hq] fp32.
+    """
+    width, groups = block_table.shape[1], shared_pages.shape[0]
+    dev, c, dims, qs, out, lse = _decode_args(q, cache, seq_lens, block_table, lambda B, Hkv: (B, width), out, lse,
+                                              return_lse, stream)
+    flag = _flag(err_flag, dev)
+    _ok(group_start, "group_start", (groups + 1,), _I32T, dev)
+    _ok(shared_pages, "shared_pages", (groups,), _I32T, dev)
+    dims = make_dims(*dims, scale)
+    pd = ctypes.byref(dims)
+    B, D = q.shape[:2]
+    workspace, have = _workspace(
+        workspace, lambda: _lib.kda_attn_decode_shared_workspace_bytes(pd, B, D, width, groups), q, dev, stream)
+    _check(_lib.kda_attn_decode_shared(pd, ctypes.byref(c), B, D, _ptr(q), qs, _ptr(seq_lens), _ptr(block_table), width,
+                                       groups, _ptr(group_start), _ptr(shared_pages), _ptr(out), _ptr(lse), _ptr(workspace),
+                                       have, flag, _stream_handle(stream, dev)), "kda_attn_decode_shared")
+    return (out, lse) if return_lse else out
+
+
+def alloc_summary(cache: KVCache) -> KeySummary:
+    """Summaries for the pages of ``cache``, not yet filled."""
+    N, Hkv, _, d = cache.k_pages.shape
+    dev = cache.k_pages.device
+    return KeySummary(torch.zeros((N, Hkv, 2, d), dtype=_I8, device=dev), torch.ones((N, Hkv), dtype=_F32, device=dev))
+
+
+def summarise(cache: KVCache, summary: KeySummary, cu_seqlens, total_tokens: int, start_pos, block_table, *, err_flag=None,
+              stream=None):
+    """Renews the summaries of the pages that an :func:`append` of ``total_tokens`` tokens with the same
+    cu_seqlens, start_pos and block_table wrote."""
+    dev = _gpu(cu_seqlens, "cu_seqlens", stream)
+    flag = _flag(err_flag, dev)
+    Hkv, d, c = _check_cache(cache, dev)
+    s = _check_summary(summary, cache.k_pages.shape[0], Hkv, d, dev)
+    n, width = block_table.shape
+    _ok(cu_seqlens, "cu_seqlens", (n + 1,), _I32T, dev)
+    _ok(start_pos, "start_pos", (n,), _I32T, dev)
+    _ok(block_table, "block_table", (n, width), _I32T, dev)
+    dims = make_dims(Hkv, Hkv, d, 0)
+    _check(_lib.kda_cache_summarise(ctypes.byref(dims), ctypes.byref(c), ctypes.byref(s), n, _ptr(cu_seqlens), int(total_tokens),
+                                    _ptr(start_pos), _ptr(block_table), width, flag, _stream_handle(stream, dev)),
+           "kda_cache_summarise")
+
+
+def select(q, summary: KeySummary, seq_lens, block_table, budget: int, sink: int = 1, recent: int = 2, *, workspace=None,
+           err_flag=None, stream=None) -> Selected:
+    """The ``budget`` pages of each sequence and kv head that promise the window's rows the most, the first
+    ``sink`` and last ``recent`` pages among them (all pages of sequences with no more than ``budget``).
+
+    q: [B, D, Hq, d]; seq_lens: [B] int32; block_table: [B, max_pages] int32.
+    """
+    dev = _gpu(q, "q", stream)
+    flag = _flag(err_flag, dev)
+    B, D, Hq, d = q.shape
+    N, Hkv = summary.unit.shape
+    s = _check_summary(summary, N, Hkv, d, dev)
+    code = _dtype_code(q)
+    qs = _rows(q, "q", (B, D, Hq, d), q.dtype, dev)
+    width, budget = block_table.shape[1], int(budget)
+    _ok(seq_lens, "seq_lens", (B,), _I32T, dev)
+    _ok(block_table, "block_table", (B, width), _I32T, dev)
+    if budget < 1:
+        raise ValueError(f"budget must be positive, not {budget}")
+    lens = _like(seq_lens, stream)
+    table, index = (_empty((B, Hkv, budget), _I32T, q.device, stream) for _ in range(2))
+    dims = make_dims(Hq, Hkv, d, code)
+    pd = ctypes.byref(dims)
+    workspace, have = _workspace(workspace, lambda: _lib.kda_cache_select_workspace_bytes(pd, B, width), q, dev, stream)
+    _check(_lib.kda_cache_select(pd, ctypes.byref(s), N, B, D, _ptr(q), qs, _ptr(seq_lens), _ptr(block_table), width, budget,
+                                 int(sink), int(recent), _ptr(lens), _ptr(table), _ptr(index), _ptr(workspace), have, flag,
+                                 _stream_handle(stream, dev)), "kda_cache_select")
+    return Selected(lens, table, index)
+
+
+def decode_selected(q, cache: KVCache, selected: Selected, out=None, *, lse=None, return_lse=False, workspace=None,
+                    scale=None, err_flag=None, stream=None):
+    """:func:`decode` over the selected pages of each kv head.
+
+    Returns out [B, D, Hq, d], then with ``return_lse`` lse [B, D, Hq] fp32 (over the selected positions).
+    """
+    table = selected.block_table
+    width = table.shape[2]
+    dev, c, dims, qs, out, lse = _decode_args(q, cache, selected.seq_lens, table, lambda B, Hkv: (B, Hkv, width), out, lse,
+                                              return_lse, stream)
+    flag = _flag(err_flag, dev)
+    dims = make_dims(*dims, scale)
+    pd = ctypes.byref(dims)
+    B, D = q.shape[:2]
+    workspace, have = _workspace(
+        workspace, lambda: _lib.kda_attn_decode_workspace_bytes(pd, B, D, width, 0), q, dev, stream)
+    _check(_lib.kda_attn_decode_selected(pd, ctypes.byref(c), B, D, _ptr(q), qs, _ptr(selected.seq_lens), _ptr(table), width,
+                                         _ptr(out), _ptr(lse), _ptr(workspace), have, flag, _stream_handle(stream, dev)),
+           "kda_attn_decode_selected")
+    return (out, lse) if return_lse else out

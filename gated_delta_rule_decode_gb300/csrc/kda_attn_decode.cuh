@@ -1,4 +1,4 @@
-// What the two cache attention kernels (kda_attn_decode.cu, kda_attn_decode_tc.cu)
+// What the two cache attention kernels (kda_attn_decode_rows.cuh, kda_attn_decode_tc.cu)
 // share: how the batch's pages are cut into workers' ranges, the workspace, and
 // small conversions.
 #pragma once
@@ -18,6 +18,9 @@ constexpr int kSms = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Warps per SM, by registers and by shared memory (the rings).
+__host__ __device__ constexpr int warps_per_sm(int NB) { return NB == 1 ? 12 : 8; }
+
 // How a call is run, and its workspace, in floats: for each item (sequence, kv
 // head, block of R rows) the workers of its first and last page (desc), the cut
 // items' partial results, two per worker (the range's first item, the range's
@@ -27,11 +30,15 @@ struct Layout {
     int64_t desc, part_m, part_l, part_o, lse2, page_w, total;
     int64_t items, workers;
     int32_t R, RB, PR;  // rows of an item, row blocks, rows of a partial result
-    int32_t NB, MT;     // tiles of a worker of kda_attn_decode.cu; MT = 0: kda_attn_decode_tc.cu
+    int32_t NB, MT;     // tiles of a worker of kda_attn_decode_rows.cuh; MT = 0: kda_attn_decode_tc.cu
     int32_t whole;      // a worker per item: short rows of the block table, no item is cut, no join
 };
 
 Layout make_layout(int64_t batch, int D, int Hq, int Hkv, int d, int dtype, int64_t max_pages, bool with_weight);
+// The same for `batch` chunks of up to `rows` rows, no more than fit an item.
+Layout make_parts_layout(int64_t batch, int rows, int Hkv, int d, int dtype, int64_t max_pages);
+// Attention of chunks (p.chunks), their parts left for a join; d and dtype as in the layout.
+cudaError_t launch_parts(const AttnDecodeParams &p, const Layout &lay, int d, int dtype, cudaStream_t st);
 
 // 2^e up to 2^127, through fp32's subnormal values down to 0.
 __device__ __forceinline__ float pow2(int e) {
@@ -91,11 +98,47 @@ __device__ __forceinline__ void store2(__nv_bfloat16 *p, float a, float b) {
     *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(a, b);
 }
 
+// The length of sequence n as far as its row of the block table goes.
+__device__ __forceinline__ int capped_len(const AttnDecodeParams &p, int n) {
+    const int cap = p.max_pages * kPage, len = p.seq_lens[n];
+    return len < 0 ? 0 : len > cap ? cap : len;
+}
+
+// PARTS: the batch's entries are chunks, not whole sequences.
+template <bool PARTS = false>
 __device__ __forceinline__ int pages_of(const AttnDecodeParams &p, int n, int &len) {
-    const int cap = p.max_pages * kPage;
-    len = p.seq_lens[n];
-    len = len < 0 ? 0 : len > cap ? cap : len;
+    len = PARTS ? p.chunks[n].len : capped_len(p, n);
     return (len + kPage - 1) / kPage;
+}
+
+template <bool PARTS>
+__device__ __forceinline__ int rows_of(const AttnDecodeParams &p, int n) {
+    return PARTS ? p.chunks[n].rows : p.D * p.G;
+}
+template <bool PARTS>
+__device__ __forceinline__ int64_t first_token(const AttnDecodeParams &p, int n) {
+    return PARTS ? (int64_t)p.chunks[n].tok0 : (int64_t)n * p.D;
+}
+// Positions that row `row` of entry n (of length len) sees.
+template <bool PARTS>
+__device__ __forceinline__ int limit_of(const AttnDecodeParams &p, int n, int len, int row) {
+    if constexpr (PARTS) {
+        const AttnChunk &c = p.chunks[n];
+        const int tok = c.tok0 + row / p.G;
+        const int at = capped_len(p, tok / p.D) - p.D + 1 + tok % p.D - c.base;
+        return at <= 0 ? len : min(at, len);
+    } else {
+        return len - p.D + 1 + row / p.G;
+    }
+}
+// Positions that every row of entry n sees.
+template <bool PARTS>
+__device__ __forceinline__ int seen_of(const AttnDecodeParams &p, int n, int len) {
+    return PARTS ? p.chunks[n].seen : len - p.D + 1;
+}
+template <bool PARTS>
+__device__ __forceinline__ int page_id(const AttnDecodeParams &p, int n, int h, int page) {
+    return PARTS ? p.block_table[p.chunks[n].table + page] : p.block_table[n * p.table_seq + h * p.table_head + page];
 }
 
 // Where a unit (one page of one item) lies: sequence n with its first unit at
@@ -137,10 +180,11 @@ struct Unit {
 };
 
 // Moves the cursor to the sequence that holds unit u >= cursor.base.
+template <bool PARTS>
 __device__ __forceinline__ Unit locate(const AttnDecodeParams &p, int HR, Cursor &c, int64_t u) {
     Unit r;
     while (true) {
-        r.pages = pages_of(p, c.n, r.len);
+        r.pages = pages_of<PARTS>(p, c.n, r.len);
         const int64_t end = c.base + (int64_t)r.pages * HR;
         if (u < end || c.n + 1 >= p.batch) break;
         c.base = end;
@@ -183,7 +227,7 @@ __device__ __forceinline__ void write_empty(const AttnDecodeParams &p, int n, in
 // the cursor of its start (in shared memory, after the call's barrier; unset
 // for an empty range).  W: the workers with a range, no more than units.  Also
 // writes the rows of sequences without pages, which have no unit.
-template <typename T, int HD, int WARPS>
+template <typename T, int HD, int WARPS, bool PARTS>
 __device__ __forceinline__ void find_range(const AttnDecodeParams &p, int HR, bool whole, int64_t *warp_sum, Cursor *start,
                                            int64_t &U, int64_t &W, int64_t &u0, int64_t &u1) {
     constexpr int kThreads = 32 * WARPS;
@@ -192,15 +236,15 @@ __device__ __forceinline__ void find_range(const AttnDecodeParams &p, int HR, bo
     if (whole) {  // units are counted within the sequence
         const int n = (int)(w / HR), hr = (int)(w % HR);
         int len;
-        const int pages = pages_of(p, n, len);
+        const int pages = pages_of<PARTS>(p, n, len);
         U = W = 1;
         u0 = (int64_t)hr * pages;
         u1 = u0 + pages;
         if (tid == 0) {
             *start = Cursor{n, 0};
-            if (hr == 0 && p.err_flag && p.seq_lens[n] > p.max_pages * kPage) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
+            if (!PARTS && hr == 0 && p.err_flag && p.seq_lens[n] > p.max_pages * kPage) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
         }
-        if (pages == 0 && hr == 0) write_empty<T, HD>(p, n, tid, kThreads);
+        if (!PARTS && pages == 0 && hr == 0) write_empty<T, HD>(p, n, tid, kThreads);
         __syncthreads();
         return;
     }
@@ -209,8 +253,8 @@ __device__ __forceinline__ void find_range(const AttnDecodeParams &p, int HR, bo
     int64_t mine = 0;
     for (int n = nb; n < ne; ++n) {
         int len;
-        mine += (int64_t)pages_of(p, n, len) * HR;
-        if (w == 0 && p.err_flag && p.seq_lens[n] > p.max_pages * kPage) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
+        mine += (int64_t)pages_of<PARTS>(p, n, len) * HR;
+        if (!PARTS && w == 0 && p.err_flag && p.seq_lens[n] > p.max_pages * kPage) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
     }
     int64_t incl = mine;
 #pragma unroll
@@ -234,10 +278,10 @@ __device__ __forceinline__ void find_range(const AttnDecodeParams &p, int HR, bo
     u1 = w < W ? U * (w + 1) / W : 0;
     if (mine > 0 && u0 >= excl && u0 < excl + mine) {
         Cursor c{nb, excl};
-        locate(p, HR, c, u0);
+        locate<PARTS>(p, HR, c, u0);
         *start = c;
     }
-    for (int n = blockIdx.x; n < p.batch; n += gridDim.x) {
+    for (int n = blockIdx.x; !PARTS && n < p.batch; n += gridDim.x) {
         if (p.seq_lens[n] > 0 && p.max_pages > 0) continue;
         write_empty<T, HD>(p, n, tid, kThreads);
     }
@@ -256,6 +300,7 @@ __device__ __forceinline__ void write_desc(float *ws, const Layout &lay, const U
 
 // Many rows on tcgen05 (bf16, d = 64 or 128).
 cudaError_t launch_tc(const AttnDecodeParams &p, const Layout &lay, int d, cudaStream_t st);
+cudaError_t launch_tc_parts(const AttnDecodeParams &p, const Layout &lay, int d, cudaStream_t st);
 
 }  // namespace dec
 }  // namespace kda

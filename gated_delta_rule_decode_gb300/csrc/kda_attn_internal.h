@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kda_attn.h"
 
@@ -38,6 +39,18 @@ struct CacheAppendParams {
     int32_t num_seqs, Hkv, max_pages;
 };
 
+// Rows that attend a run of pages together, where a sequence is attended in
+// parts (its shared prefix, the rest): rows row / G of tokens tok0.., the run
+// starts at position `base` of their sequences and has `len` positions.  Rows
+// that see none of it (see dec::limit_of) are computed as if they saw all of it
+// and passed over afterwards.
+struct AttnChunk {
+    int64_t table;  // of the run's first page in block_table
+    int32_t tok0, rows, base, len;
+    int32_t seen;   // positions that all rows see which see any
+    int32_t pad;
+};
+
 struct AttnDecodeParams {
     const unsigned char *k_pages, *v_pages;
     const float *k_scale, *v_scale;
@@ -51,8 +64,55 @@ struct AttnDecodeParams {
     float *weight_out;
     void *workspace;
     int32_t *err_flag;
+    const AttnChunk *chunks;  // parts: takes the place of sequences, `batch` of them; results stay apart:
+    float2 *part_ml;          // (m, l) per row, `out` fp32 and not divided by l
+    int64_t table_seq, table_head;  // entries between the table rows of sequences, and of a sequence's kv heads (0: one for all)
     int32_t batch, D, Hq, Hkv, G, max_pages;
     float scale;
+};
+
+struct AttnSharedParams {
+    AttnDecodeParams call;  // the whole batch
+    const int32_t *group_start, *shared_pages;
+    int32_t groups;
+};
+
+struct NormRotateParams {
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;  // elements between tokens
+    const int32_t *positions;
+    const uint64_t *turns;  // [rot / 2]
+    const float *q_weight, *k_weight;
+    int64_t total_tokens;
+    int32_t Hq, Hkv, rot, interleaved;
+    float eps, factor;
+};
+
+struct CacheSummariseParams {
+    const unsigned char *k_pages;
+    const float *k_scale;
+    int64_t num_pages;
+    int8_t *bounds;
+    float *unit;
+    const int32_t *cu_seqlens;
+    int64_t total_tokens;
+    const int32_t *start_pos, *block_table;
+    int32_t *err_flag;
+    int32_t num_seqs, Hkv, max_pages;
+};
+
+struct CacheSelectParams {
+    const int8_t *bounds;
+    const float *unit;
+    int64_t num_pages;
+    const void *q;
+    int64_t q_stride;
+    const int32_t *seq_lens, *block_table;
+    int32_t *seq_lens_out, *block_table_out, *index_out;
+    void *workspace;
+    int32_t *err_flag;
+    int32_t batch, D, Hkv, G, max_pages, budget, sink, recent;
 };
 
 struct CacheEvictParams {
@@ -125,6 +185,23 @@ inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_
     return e;
 }
 
+// A launch that may begin while the kernel before it on the stream ends (the
+// kernel waits for that one's results by itself).
+template <typename... Args>
+cudaError_t launch_after(void (*kern)(Args...), dim3 grid, int threads, cudaStream_t st,
+                         std::common_type_t<Args>... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 cudaError_t launch_attn_prefill(const AttnPrefillParams &p, int d, int dtype, cudaStream_t s);
 // Prompts in bf16, on the tensor cores.
 cudaError_t launch_attn_prefill_tc(const AttnPrefillParams &p, int d, cudaStream_t s);
@@ -132,6 +209,13 @@ cudaError_t launch_cache_append(const CacheAppendParams &p, int d, int dtype, cu
 size_t attn_decode_workspace_bytes(int Hq, int Hkv, int d, int dtype, int64_t batch, int D, int64_t max_pages,
                                    bool with_weight);
 cudaError_t launch_attn_decode(const AttnDecodeParams &p, int d, int dtype, cudaStream_t s);
+size_t attn_shared_workspace_bytes(int Hq, int Hkv, int d, int dtype, int64_t batch, int D, int64_t max_pages,
+                                   int64_t groups);
+cudaError_t launch_attn_shared(const AttnSharedParams &p, int d, int dtype, cudaStream_t s);
 cudaError_t launch_cache_evict(const CacheEvictParams &p, cudaStream_t s);
+cudaError_t launch_norm_rotate(const NormRotateParams &p, int d, int dtype, cudaStream_t s);
+cudaError_t launch_cache_summarise(const CacheSummariseParams &p, int d, cudaStream_t s);
+size_t cache_select_workspace_bytes(int Hkv, int64_t batch, int64_t max_pages);
+cudaError_t launch_cache_select(const CacheSelectParams &p, int d, int dtype, cudaStream_t s);
 
 }  // namespace kda

@@ -5,8 +5,10 @@
  * softmax attention, and with it a growing cache of keys and values, in the
  * others.  These entry points serve those blocks: attention over packed
  * prompts, an 8-bit paged key/value cache, attention over that cache for
- * single tokens and draft windows, and the eviction of pages that received
- * little attention.  They follow the conventions of kda.h (device pointers,
+ * single tokens and draft windows (of whole sequences, of batches that share
+ * prefixes, or over the pages that a cheap score selects), the eviction of
+ * pages that received little attention, and the norm and rotation of queries
+ * and keys in front of it all.  They follow the conventions of kda.h (device pointers,
  * 16-byte alignment, asynchronous on `stream`, statuses, *err_flag, no
  * allocation, no atomics on data: the same inputs give the same bits), and
  * like the rest of the library they have no gradients.
@@ -169,6 +171,130 @@ KDA_API int kda_cache_evict(int32_t batch, int32_t max_pages, int32_t budget, in
                             const int32_t *seq_lens, const int32_t *block_table, const float *weight,
                             int32_t *seq_lens_out, int32_t *block_table_out, float *weight_out,
                             int32_t *freed, int32_t *freed_count, int32_t *err_flag, void *stream);
+
+/*
+ * kda_norm_rotate: norm of query and key heads and the rotation by their
+ * positions.  Per token and head, x a row of d channels:
+ *   y = x / sqrt(sum_c x_c^2 / d + eps) * weight     (y = x where weight is NULL)
+ *   (y_a, y_b) -> factor (y_a cos t - y_b sin t, y_a sin t + y_b cos t)
+ * for the pairs i < rotary_dim / 2 of the first rotary_dim channels:
+ * (a, b) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) where interleaved; the
+ * other channels are y.  t = 2 pi positions[token] turns[i] / 2^64: a table of
+ * turns per position in units of 2^-64, modulo one, so that angles are exact to
+ * 2^-24 at every position.  fp32 throughout, rounded once.
+ *
+ *   q, k         dtype [total_tokens][Hq or Hkv][d], tokens q_stride, k_stride apart
+ *   q_out, k_out the same, tokens q_out_stride, k_out_stride apart; each may be
+ *                its input (with its stride)
+ *   positions    i32 [total_tokens], any value
+ *   turns        u64 [rotary_dim / 2]
+ *   q_weight, k_weight  f32 [d], 16-byte aligned; NULL: no norm
+ * dims->scale is not used.  rotary_dim even, 0..d (0: norm alone).
+ */
+KDA_API int kda_norm_rotate(const kda_attn_dims *dims, int64_t total_tokens, const void *q, int64_t q_stride,
+                            const void *k, int64_t k_stride, const int32_t *positions, const uint64_t *turns,
+                            int32_t rotary_dim, int32_t interleaved, float factor, const float *q_weight,
+                            const float *k_weight, float eps, void *q_out, int64_t q_out_stride, void *k_out,
+                            int64_t k_out_stride, void *stream);
+
+/*
+ * kda_attn_decode_shared: kda_attn_decode for sequences that share prefixes.
+ * The sequences group_start[g]..group_start[g+1]-1 are a group: the first
+ * shared_pages[g] entries of their block table rows name the same pages, which
+ * are read from the row of the group's first sequence, once for all of them.
+ * The results are those of kda_attn_decode (the shared pages are full; a
+ * sequence that ends inside them sees them as far as it goes).  Sequences of
+ * no group share nothing.
+ *
+ *   group_start  i32 [num_groups + 1], not decreasing, in 0..batch; offsets
+ *                that are not set KDA_DEVERR_SEQLENS, and the outputs of the
+ *                call are then unspecified
+ *   shared_pages i32 [num_groups]; one outside 0..max_pages sets
+ *                KDA_DEVERR_PAGE and is taken as the nearer of these
+ *   workspace    kda_attn_decode_shared_workspace_bytes(...) bytes, 256-byte
+ *                aligned, contents undefined before and after
+ * The rest as in kda_attn_decode; page weights are not offered (a shared page
+ * is no sequence's to evict).
+ */
+KDA_API int kda_attn_decode_shared(const kda_attn_dims *dims, const kda_kv_cache *cache, int32_t batch,
+                                   int32_t draft_len, const void *q, int64_t q_stride, const int32_t *seq_lens,
+                                   const int32_t *block_table, int32_t max_pages, int32_t num_groups,
+                                   const int32_t *group_start, const int32_t *shared_pages, void *out, float *lse,
+                                   void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/* Workspace of kda_attn_decode_shared; 0 for invalid arguments. */
+KDA_API size_t kda_attn_decode_shared_workspace_bytes(const kda_attn_dims *dims, int32_t batch, int32_t draft_len,
+                                                      int32_t max_pages, int32_t num_groups);
+
+/*
+ * Summaries of the cached keys, for a selection of pages: per page, kv head and
+ * channel the largest and the smallest key, in whole numbers of one unit.
+ *   bounds  i8  [num_pages][Hkv][2][d]  largest, smallest, in -127..127
+ *   unit    f32 [num_pages][Hkv]        a power of two
+ */
+typedef struct kda_key_summary {
+    int8_t *bounds;
+    float *unit;
+} kda_key_summary;
+
+/*
+ * kda_cache_summarise: renews the summaries of the pages that a kda_cache_append
+ * with the same arguments wrote, from the positions that they hold now.  Per
+ * page and head, over the page's positions before the sequence's new end:
+ *   unit     the smallest power of two >= 2^-126 with |key| <= 127 unit
+ *   bounds   max and min of the channel's keys / unit, to the nearest whole
+ *            number, ties to even; a NaN key is passed over (0 for NaN alone)
+ * Errors as in kda_cache_append; a k_scale that is not a power of two, or a unit
+ * above 2^126, sets KDA_DEVERR_SCALE and that page and head is left alone.
+ */
+KDA_API int kda_cache_summarise(const kda_attn_dims *dims, const kda_kv_cache *cache, const kda_key_summary *summary,
+                                int32_t num_seqs, const int32_t *cu_seqlens, int64_t total_tokens,
+                                const int32_t *start_pos, const int32_t *block_table, int32_t max_pages,
+                                int32_t *err_flag, void *stream);
+
+/*
+ * kda_cache_select: the pages of each sequence and kv head that promise the
+ * most.  A sequence of P = ceil(seq_lens / 64) pages keeps them all where
+ * P <= budget; else its first `sink`, its last `recent` and, of the others, the
+ * best by score until there are `budget`; of equal scores the lower index.  With
+ *   u_r   the smallest power of two >= 2^-126 with |q_r| <= 127 u_r (finite elements)
+ *   x_rc  q_rc / u_r to the nearest whole number, ties to even, within
+ *         -127..127; 0 for NaN
+ *   score(page) = max_r u_r unit sum_c max(x_rc hi_c, x_rc lo_c)
+ * over the rows r of the window's tokens and the kv head's query heads (whole
+ * numbers times powers of two: the order of the sum does not matter).
+ *
+ *   q            as in kda_attn_decode
+ *   seq_lens, block_table  as in kda_attn_decode; a page outside the cache sets
+ *                KDA_DEVERR_PAGE, a unit that is not a power of two in
+ *                2^-126..2^126 KDA_DEVERR_SCALE; either scores below all others
+ *   budget       >= sink + recent, sink >= 0, recent >= 1 (>= 2 for draft_len
+ *                > 1: the pages that the window can lie in)
+ *   seq_lens_out     i32 [batch]: seq_lens less 64 per page left out
+ *   block_table_out  i32 [batch][Hkv][budget]: the selected entries in order, then -1
+ *   index_out        i32 [batch][Hkv][budget]: their places in the row, then -1
+ *   workspace    kda_cache_select_workspace_bytes(...) bytes, 256-byte aligned
+ */
+KDA_API int kda_cache_select(const kda_attn_dims *dims, const kda_key_summary *summary, int64_t num_pages,
+                             int32_t batch, int32_t draft_len, const void *q, int64_t q_stride,
+                             const int32_t *seq_lens, const int32_t *block_table, int32_t max_pages, int32_t budget,
+                             int32_t sink, int32_t recent, int32_t *seq_lens_out, int32_t *block_table_out,
+                             int32_t *index_out, void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                             void *stream);
+
+/* Workspace of kda_cache_select; 0 for invalid arguments. */
+KDA_API size_t kda_cache_select_workspace_bytes(const kda_attn_dims *dims, int32_t batch, int32_t max_pages);
+
+/*
+ * kda_attn_decode_selected: kda_attn_decode with a block table of its own for
+ * every kv head, i32 [batch][Hkv][max_pages] (as kda_cache_select leaves it; the
+ * window's positions are the last ones).  Workspace:
+ * kda_attn_decode_workspace_bytes for the same sizes, without weights.
+ */
+KDA_API int kda_attn_decode_selected(const kda_attn_dims *dims, const kda_kv_cache *cache, int32_t batch,
+                                     int32_t draft_len, const void *q, int64_t q_stride, const int32_t *seq_lens,
+                                     const int32_t *block_table, int32_t max_pages, void *out, float *lse,
+                                     void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream);
 
 #ifdef __cplusplus
 }

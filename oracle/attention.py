@@ -178,3 +178,98 @@ def evict(lens, table, weight, budget, sink, recent):
         count[n] = len(out)
         lens[n] -= PAGE * len(out)
     return lens, new_t, new_w, freed, count
+
+
+def rotate(x, pos, turns, interleaved=False, factor=1.0, weight=None, eps=1e-6):
+    """x [T, H, d] -> (y, size): norm (where a weight is given) and rotation by pos * turns / 2^64 turns.
+
+    size bounds what an element is made of: |y_a| + |y_b| of its pair times the factor."""
+    y = np.array(x, np.float64)
+    d, half = y.shape[-1], len(turns)
+    if weight is not None:
+        y = y / np.sqrt((y * y).sum(-1, keepdims=True) / d + eps) * np.asarray(weight, np.float64)
+    out, size = y.copy(), np.abs(y)
+    for t in range(y.shape[0]):
+        for i in range(half):
+            a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+            part = int(pos[t]) * int(turns[i]) % (1 << 64)  # of a turn
+            c, s = (factor * f(2 * math.pi * (part / 2.0 ** 64)) for f in (math.cos, math.sin))
+            out[t, :, a], out[t, :, b] = y[t, :, a] * c - y[t, :, b] * s, y[t, :, a] * s + y[t, :, b] * c
+            size[t, :, a] = size[t, :, b] = abs(factor) * (np.abs(y[t, :, a]) + np.abs(y[t, :, b]))
+    return out, size
+
+
+def unit_of(amax: float) -> float:
+    """The smallest power of two u >= 2^-126 with amax <= 127 u."""
+    u = 2.0 ** -126
+    while amax > 127 * u:
+        u *= 2.0
+    return u
+
+
+def summarise(k_pages, k_scale, bounds, unit, cu, start, table):
+    """(bounds, unit) after renewing the summaries of the pages that an append with these arguments wrote."""
+    bounds, unit = bounds.copy(), unit.copy()
+    for s in range(len(cu) - 1):
+        n = cu[s + 1] - cu[s]
+        if n == 0 or start[s] < 0:
+            continue
+        for c in range(start[s] // PAGE, (start[s] + n - 1) // PAGE + 1):
+            page = table[s][c] if c < len(table[s]) else -1
+            if page < 0 or page >= unit.shape[0]:
+                continue
+            for h in range(unit.shape[1]):
+                k = _VALUES[k_pages[page, h, :start[s] + n - c * PAGE]] * float(k_scale[page, h])
+                there = ~np.isnan(k)
+                none = ~there.any(0)
+                hi = np.where(none, 0.0, np.where(there, k, -np.inf).max(0))
+                lo = np.where(none, 0.0, np.where(there, k, np.inf).min(0))
+                u = unit_of(max(np.abs(hi).max(), np.abs(lo).max()))
+                bounds[page, h, 0], bounds[page, h, 1] = np.rint(hi / u), np.rint(lo / u)
+                unit[page, h] = u
+    return bounds, unit
+
+
+def page_scores(q, bounds, unit, ids, n, h, G):
+    """Scores of the pages `ids` for sequence n and kv head h; -inf for pages outside the summary."""
+    rows = np.asarray(q[n, :, h * G:(h + 1) * G], np.float64).reshape(-1, q.shape[-1])
+    best = np.full(len(ids), -np.inf)
+    for x in rows:
+        fin = np.abs(x[np.isfinite(x)])
+        u = unit_of(fin.max() if fin.size else 0.0)
+        w = np.rint(np.clip(np.nan_to_num(x / u, nan=0.0, posinf=127, neginf=-127), -127, 127))
+        for i, page in enumerate(ids):
+            if 0 <= page < unit.shape[0]:
+                b = bounds[page, h].astype(np.float64)
+                best[i] = max(best[i], np.maximum(w * b[0], w * b[1]).sum() * u * float(unit[page, h]))
+    return best
+
+
+def select(q, bounds, unit, lens, table, budget, sink, recent):
+    """(lens, table, index) of the selected pages, q [B, D, Hq, d]."""
+    B, Hkv = q.shape[0], unit.shape[1]
+    G, width = q.shape[2] // Hkv, table.shape[1]
+    new_l = np.zeros(B, np.int32)
+    new_t, index = np.full((B, Hkv, budget), -1, np.int32), np.full((B, Hkv, budget), -1, np.int32)
+    for n in range(B):
+        length = min(max(int(lens[n]), 0), width * PAGE)
+        P = -(-length // PAGE)
+        new_l[n] = length - max(0, P - budget) * PAGE
+        for h in range(Hkv):
+            take = list(range(P))
+            if P > budget:
+                score = page_scores(q, bounds, unit, table[n, :P], n, h, G)
+                score[:sink] = np.inf
+                score[P - recent:] = np.inf
+                take = sorted(sorted(range(P), key=lambda c: (-score[c], c))[:budget])
+            index[n, h, :len(take)], new_t[n, h, :len(take)] = take, table[n, take]
+    return new_l, new_t, index
+
+
+def decode_selected(q, k_pages, v_pages, k_scale, v_scale, lens, table, scale=None):
+    """:func:`decode` with a table per kv head, [B, Hkv, pages] -> (out, lse, absout, mag)."""
+    Hkv = k_scale.shape[1]
+    G = q.shape[2] // Hkv
+    parts = [decode(q[:, :, h * G:(h + 1) * G], k_pages[:, h:h + 1], v_pages[:, h:h + 1], k_scale[:, h:h + 1],
+                    v_scale[:, h:h + 1], lens, table[:, h], scale)[:4] for h in range(Hkv)]
+    return tuple(np.concatenate(x, 2) for x in zip(*parts))
