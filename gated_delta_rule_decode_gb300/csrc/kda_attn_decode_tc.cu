@@ -390,7 +390,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
         int limit = 0, unit = kNoUnit;  // the exponent that O is counted in
         bool valid = false, ok = true;
         int64_t qrow = 0;
-        int window0 = 0;  // positions that every row sees
         while (wk.next<PARTS>(p, HR)) {
             const int j = wk.tile;
             const int b = j & 1;
@@ -403,7 +402,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
             if (wk.first) {
                 valid = row < rows_all;
                 limit = valid ? limit_of<PARTS>(p, un.n, un.len, row) : 0;
-                window0 = seen_of<PARTS>(p, un.n, un.len);
                 qrow = valid ? (first_token<PARTS>(p, un.n) + row / p.G) * p.Hq + h * p.G + row % p.G : 0;
                 qs = __uint_as_float((uint32_t)(127 - 14 + q_exp[wk.item & 1][r]) << 23) * p.scale * kLog2e;
                 m = -INFINITY;
@@ -438,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                 }
                 const bool have = pg == 0 ? has[0] : has[1];
                 end = have ? limit - (un.page + pg) * kPage : 0;
-                masked = !have || (un.page + pg + 1) * kPage > window0;
+                masked = !have || (un.page + pg + 1) * kPage > seen_of<PARTS>(p, un.n, un.len);
                 // (read twice: the maximum first, then the weights)
                 float mx = -INFINITY;
 #pragma unroll 1
@@ -554,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                     for (int e = 0; e < 16; ++e) o[e] = fo == 0.f ? 0.f : o[e] * in * fo;
                     if (nan) {  // the NaN values that this row sees
                         asm volatile("" ::: "memory");
-                        for (int pos = max(window0, 0); pos < limit; ++pos) {
+                        for (int pos = max(seen_of<PARTS>(p, un.n, un.len), 0); pos < limit; ++pos) {
                             const int block = page_meta(p, page_id<PARTS>(p, un.n, h, pos / kPage), h).block;
                             if (block < 0) continue;
                             const unsigned char *vb = p.v_pages + (int64_t)block * C::kHalf +

@@ -188,11 +188,12 @@ inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_
 // A launch that may begin while the kernel before it on the stream ends (the
 // kernel waits for that one's results by itself).
 template <typename... Args>
-cudaError_t launch_after(void (*kern)(Args...), dim3 grid, int threads, cudaStream_t st,
-                         std::common_type_t<Args>... args) {
+cudaError_t launch_after_smem(void (*kern)(Args...), dim3 grid, int threads, int smem, cudaStream_t st,
+                              std::common_type_t<Args>... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -200,6 +201,12 @@ cudaError_t launch_after(void (*kern)(Args...), dim3 grid, int threads, cudaStre
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename... Args>
+cudaError_t launch_after(void (*kern)(Args...), dim3 grid, int threads, cudaStream_t st,
+                         std::common_type_t<Args>... args) {
+    return launch_after_smem(kern, grid, threads, 0, st, args...);
 }
 
 cudaError_t launch_attn_prefill(const AttnPrefillParams &p, int d, int dtype, cudaStream_t s);

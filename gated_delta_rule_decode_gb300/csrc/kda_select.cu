@@ -129,12 +129,22 @@ cudaError_t launch_summarise(const CacheSummariseParams &p, cudaStream_t st) {
 // ---------------------------------------------------------------- scores
 //
 // A thread scores a page for all rows of its kv head: the page's bounds lie in
-// its registers (staged through shared memory, so that the reads are whole
-// lines), the rows' whole numbers come from shared memory for all threads alike,
-// positive and negative ones apart: max(x hi, x lo) = max(x, 0) hi + min(x, 0) lo,
-// four channels a dp4a.
-constexpr int kScorePages = 128;  // pages (threads) of a block
-constexpr int kScoreRows = 16;    // rows in shared memory together
+// its registers, the rows' whole numbers come from shared memory for all threads
+// alike, positive and negative ones apart: max(x hi, x lo) = max(x, 0) hi +
+// min(x, 0) lo, four channels a dp4a.  A warp goes over groups of 32 pages by
+// itself: bounds come through shared memory, so that the reads are whole lines, and
+// the next group's are asked for as soon as this one's are in registers (their
+// ids and units one group earlier).
+constexpr int kScoreWarps = 4;
+constexpr int64_t kScoreBlocks = 4 * 152 * 3;  // blocks that a call has at least, where it has the pages
+constexpr int kScoreRows = 64;  // rows in shared memory together; more take further rounds over the pages
+
+template <int HD>
+struct ScoreSmem {
+    static constexpr int kPitch = 2 * HD + 16;  // of a page: eight neighbours' pieces lie in different banks
+    static constexpr int kTile = 32 * kPitch;
+    static int bytes(int rows) { return kScoreWarps * kTile + (rows < kScoreRows ? rows : kScoreRows) * 2 * HD; }
+};
 
 __device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t b = __float_as_uint(x == 0.f ? 0.f : x);  // -0 as 0
@@ -159,58 +169,62 @@ __device__ __forceinline__ int64_t held_pages(const int32_t *seq_lens, int n, in
     return (len + kPage - 1) / kPage;
 }
 
+// blockIdx.x: item (sequence, kv head) and which of `splits` shares of its page groups.
 template <typename T, int HD>
-__global__ void __launch_bounds__(kScorePages) score_kernel(const CacheSelectParams p, int chunks) {
-    constexpr int W = HD / 4;          // words of a bound, and of a row's part
-    constexpr int PITCH = 2 * HD + 16; // bytes of a page in shared memory: eight neighbours' pieces lie in different banks
-    __shared__ __align__(16) unsigned char tile[kScorePages * PITCH];
-    __shared__ __align__(16) uint32_t xs[kScoreRows][2][W];
+__global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const CacheSelectParams p, int splits) {
+    using S = ScoreSmem<HD>;
+    constexpr int W = HD / 4;  // words of a bound, and of a row's part
+    extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float x_unit[kScoreRows];
-    __shared__ int ids[kScorePages];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int item = (int)(blockIdx.x / (unsigned)chunks), n = item / p.Hkv, h = item % p.Hkv;
+    const int item = (int)(blockIdx.x / (unsigned)splits), split = (int)(blockIdx.x % (unsigned)splits);
+    const int n = item / p.Hkv, h = item % p.Hkv;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int len;
     const int P = (int)held_pages(p.seq_lens, n, p.max_pages, len);
-    const int page0 = (int)(blockIdx.x % (unsigned)chunks) * kScorePages;
-    if (page0 >= P || P <= p.budget) return;
+    const int first = 32 * (split * kScoreWarps + warp), step = 32 * splits * kScoreWarps;  // the warp's pages
+    if (32 * split * kScoreWarps >= P || P <= p.budget) return;  // (by whole blocks)
+    unsigned char *tile = smem + warp * S::kTile;
+    uint32_t *xs = reinterpret_cast<uint32_t *>(smem + kScoreWarps * S::kTile);  // [row][2][W]
+    const int32_t *table = p.block_table + (int64_t)n * p.max_pages;
+    uint32_t *keys = static_cast<uint32_t *>(p.workspace) + (int64_t)item * p.max_pages;
 
-    int id = -1;
-    float unit = 0.f;
-    int err = 0;
-    if (page0 + tid < P) {
-        id = p.block_table[(int64_t)n * p.max_pages + page0 + tid];
-        if (id < 0 || id >= p.num_pages) {
-            id = -1;
-            err = KDA_DEVERR_PAGE;
-        } else {
-            unit = p.unit[(int64_t)id * p.Hkv + h];
-            if (!power_of_two(unit)) {
-                id = -1;
-                err = KDA_DEVERR_SCALE;
-            }
+    // A page's id, -1 where there is none; its unit, 0 where it has none that can be used.  A page that is not in
+    // the summary, or whose unit is no power of two, scores below all others.
+    auto id_of = [&](int page, bool tell) {
+        if (page >= P) return -1;
+        const int id = table[page];
+        const bool in = id >= 0 && id < p.num_pages;
+        if (!in && tell && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
+        return in ? id : -1;
+    };
+    auto unit_of = [&](int id) { return id < 0 ? 0.f : p.unit[(int64_t)id * p.Hkv + h]; };
+    // Copies 32 pages' bounds, by the whole warp: 16 bytes a lane.  (Where a page has none some other's, which
+    // does not count.)
+    constexpr int PIECES = 2 * HD / 16, AT_ONCE = 32 / PIECES;
+    const int8_t *from = p.bounds + (int64_t)h * (2 * HD) + 16 * (lane % PIECES);
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(tile + (lane / PIECES) * S::kPitch + 16 * (lane % PIECES));
+    const int64_t page_bytes = (int64_t)p.Hkv * (2 * HD);
+    auto copy = [&](int id) {
+        if (p.num_pages == 0) return;
+        const int safe = max(id, 0);
+#pragma unroll
+        for (int i = 0; i < 32; i += AT_ONCE) {
+            const int pg = __shfl_sync(~0u, safe, i + lane / PIECES);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * S::kPitch), "l"(from + pg * page_bytes) : "memory");
         }
-    }
-    if (err != 0 && p.err_flag) atomicOr(p.err_flag, err);
-    ids[tid] = id;
-    __syncthreads();
-    constexpr int PIECES = 2 * HD / 16;  // of a page
-    for (int i = tid; i < kScorePages * PIECES; i += kScorePages) {
-        const int pg = i / PIECES, piece = i % PIECES;
-        if (ids[pg] < 0) continue;
-        const int8_t *src = p.bounds + ((int64_t)ids[pg] * p.Hkv + h) * (2 * HD) + 16 * piece;
-        const uint32_t dst = (uint32_t)__cvta_generic_to_shared(tile + pg * PITCH + 16 * piece);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 
     const int rows = p.D * p.G;
-    uint32_t b[2][W];
-    float best = -INFINITY;
     for (int r0 = 0; r0 < rows; r0 += kScoreRows) {
         const int here = min(kScoreRows, rows - r0);
+        int now = id_of(first + lane, r0 == 0), next = id_of(first + step + lane, r0 == 0);
+        copy(now);
+        float unit = unit_of(now);
         if (r0 > 0) __syncthreads();
         // the rows' whole numbers, a warp a row
-        for (int r = warp; r < here; r += kScorePages / 32) {
+        for (int r = warp; r < here; r += kScoreWarps) {
             const int tok = (r0 + r) / p.G, g = (r0 + r) % p.G;
             const T *src = static_cast<const T *>(p.q) + ((int64_t)n * p.D + tok) * p.q_stride + (int64_t)(h * p.G + g) * HD;
             float x[4] = {0.f, 0.f, 0.f, 0.f}, amax = 0.f;
@@ -233,66 +247,92 @@ __global__ void __launch_bounds__(kScorePages) score_kernel(const CacheSelectPar
                 down |= (uint32_t)(min(v, 0) & 255) << (8 * j);
             }
             if (lane < W) {
-                xs[r][0][lane] = up;
-                xs[r][1][lane] = down;
+                xs[r * 2 * W + lane] = up;
+                xs[r * 2 * W + W + lane] = down;
             }
             if (lane == 0) x_unit[r] = exp2i(e);
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        if (r0 == 0) {
+        for (int page = first; page < P; page += step) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncwarp();
+            uint32_t b[2][W];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < W; j += 4) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(tile + tid * PITCH + i * HD + 4 * j);
+                    const uint4 u = *reinterpret_cast<const uint4 *>(tile + lane * S::kPitch + i * HD + 4 * j);
                     b[i][j] = u.x; b[i][j + 1] = u.y; b[i][j + 2] = u.z; b[i][j + 3] = u.w;
                 }
-        }
-        for (int r = 0; r < here; ++r) {
-            int sum[4] = {0, 0, 0, 0};
+            __syncwarp();
+            if (page + step < P) copy(next);
+            const float next_unit = unit_of(next);
+            const int after = id_of(page + 2 * step + lane, r0 == 0);
+            float best = -INFINITY;
+#pragma unroll 1
+            for (int r = 0; r < here; ++r) {
+                int sum[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < W; j += 4) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(&xs[r][i][j]);
-                    sum[0] = __dp4a((int)u.x, (int)b[i][j], sum[0]);
-                    sum[1] = __dp4a((int)u.y, (int)b[i][j + 1], sum[1]);
-                    sum[2] = __dp4a((int)u.z, (int)b[i][j + 2], sum[2]);
-                    sum[3] = __dp4a((int)u.w, (int)b[i][j + 3], sum[3]);
-                }
-            best = fmaxf(best, (float)((sum[0] + sum[1]) + (sum[2] + sum[3])) * x_unit[r]);
+                    for (int j = 0; j < W; j += 4) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(xs + r * 2 * W + i * W + j);
+                        sum[0] = __dp4a((int)u.x, (int)b[i][j], sum[0]);
+                        sum[1] = __dp4a((int)u.y, (int)b[i][j + 1], sum[1]);
+                        sum[2] = __dp4a((int)u.z, (int)b[i][j + 2], sum[2]);
+                        sum[3] = __dp4a((int)u.w, (int)b[i][j + 3], sum[3]);
+                    }
+                best = fmaxf(best, (float)((sum[0] + sum[1]) + (sum[2] + sum[3])) * x_unit[r]);
+            }
+            if (page + lane < P) {
+                const bool good = now >= 0 && power_of_two(unit);
+                if (now >= 0 && !good && r0 == 0 && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_SCALE);
+                uint32_t key = ordered(good ? best * unit : -INFINITY);
+                if (r0 > 0) key = max(key, keys[page + lane]);
+                keys[page + lane] = key;
+            }
+            now = next;
+            unit = next_unit;
+            next = after;
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");  // (a warp without pages has copies in flight)
+        __syncwarp();
     }
-    if (page0 + tid < P)
-        static_cast<uint32_t *>(p.workspace)[(int64_t)item * p.max_pages + page0 + tid] =
-            ordered(id < 0 ? -INFINITY : best * unit);
 }
 
 // ---------------------------------------------------------------- selection
 //
 // A block per sequence and kv head.  The pages that always stay get the largest
-// key; a radix selection over the scores as ordered integers (8 bits a pass, the
-// histogram in shared memory) finds the score t of the last page that is taken
-// and how many of the pages that score exactly t are; of those the lower indices
-// are.  One pass in index order then writes the taken pages.
-constexpr int kSelectThreads = 256;
+// key.  The score t of the last page that is taken is found by rounds: the range
+// of the scores (as ordered integers, in shared memory) that still can be t, from
+// the smallest to the largest at first, is cut into 1024 bins and the scores
+// counted; the bin in which the taken ones end is the next range, until bins are
+// single values.  Bins of the range itself spread the scores, so that counts
+// seldom meet, and three rounds are the rule.  Of the pages that score exactly t
+// the lower indices are taken.  A thread then writes the taken pages of its run
+// of neighbours, behind those of the runs before.
+constexpr int kSelectThreads = 512;
+constexpr int kSelectCached = 50000;  // pages whose scores fit shared memory; longer rows are read where they are
 
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const CacheSelectParams p) {
-    constexpr int W = kSelectThreads / 32;
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t s_prefix, s_left;
-    __shared__ int warp_a[W], warp_b[W];
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(const CacheSelectParams p, int cached) {
+    constexpr int WARPS = kSelectThreads / 32;
+    extern __shared__ __align__(16) uint32_t held[];
+    constexpr int BIN_BITS = 10, BINS = 1 << BIN_BITS;
+    static_assert(BINS == 2 * kSelectThreads, "two bins a thread");
+    __shared__ __align__(8) int bins[BINS];
+    __shared__ int2 sums[WARPS];
+    __shared__ uint2 ends[WARPS];
+    __shared__ int found[2];
     const int item = blockIdx.x, n = item / p.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int len;
     const int P = (int)held_pages(p.seq_lens, n, p.max_pages, len);
+    const int32_t *table = p.block_table + (int64_t)n * p.max_pages;
+    const int64_t to = (int64_t)item * p.budget;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (item % p.Hkv == 0 && tid == 0) {
         if (p.err_flag && (int64_t)p.seq_lens[n] > (int64_t)p.max_pages * kPage) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
         p.seq_lens_out[n] = len - (P > p.budget ? (P - p.budget) * kPage : 0);
     }
-    const int32_t *table = p.block_table + (int64_t)n * p.max_pages;
-    const int64_t to = (int64_t)item * p.budget;
     if (P <= p.budget) {
         for (int i = tid; i < p.budget; i += kSelectThreads) {
             p.block_table_out[to + i] = i < P ? table[i] : -1;
@@ -300,89 +340,130 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const CacheSelec
         }
         return;
     }
-    const uint32_t *keys = static_cast<const uint32_t *>(p.workspace) + (int64_t)item * p.max_pages;
-    auto key_of = [&](int i) { return i < p.sink || i >= P - p.recent ? ~0u : keys[i]; };
-    uint32_t prefix = 0, left = p.budget;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
-        __syncthreads();
-        const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
-        for (int i = tid; i < P; i += kSelectThreads) {
-            const uint32_t key = key_of(i);
-            if ((key & mask) == prefix) atomicAdd(&hist[255u - ((key >> shift) & 255u)], 1u);
+    const uint32_t *scores = static_cast<const uint32_t *>(p.workspace) + (int64_t)item * p.max_pages;
+    auto score = [&](int i) { return i < p.sink || i >= P - p.recent ? ~0u : scores[i]; };
+    uint32_t lo = ~0u, hi = 0;  // of the pages that need not stay
+    for (int i = tid; i < P; i += kSelectThreads) {
+        const uint32_t key = score(i);
+        if (cached > 0) held[i] = key;
+        if (i >= p.sink && i < P - p.recent) {
+            lo = min(lo, key);
+            hi = max(hi, key);
         }
-        __syncthreads();
-        if (warp == 0) {  // the bin, from the largest down, in which the running count reaches `left`
-            uint32_t c[8], sum = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum += c[j] = hist[lane * 8 + j];
-            uint32_t incl = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t t = __shfl_up_sync(~0u, incl, o);
-                if (lane >= o) incl += t;
-            }
-            uint32_t before = incl - sum;
-            if (before < left && incl >= left) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (before < left && before + c[j] >= left) {
-                        s_prefix = prefix | ((255u - (uint32_t)(lane * 8 + j)) << shift);
-                        s_left = left - before;
-                    }
-                    before += c[j];
-                }
-            }
-        }
-        __syncthreads();
-        prefix = s_prefix;
-        left = s_left;
     }
-    // `left` of the pages that score exactly `prefix` are taken: the first ones
-    int taken = 0, equal = 0;  // before this chunk
-    for (int base = 0; base < P; base += kSelectThreads) {
-        const int i = base + tid;
-        const uint32_t key = i < P ? key_of(i) : 0;
-        const bool eq = i < P && key == prefix, more = i < P && key > prefix;
-        const unsigned me = __ballot_sync(~0u, eq), mm = __ballot_sync(~0u, more);
-        __syncthreads();
-        if (lane == 0) {
-            warp_a[warp] = __popc(me);
-            warp_b[warp] = __popc(mm);
+    lo = __reduce_min_sync(~0u, lo);
+    hi = __reduce_max_sync(~0u, hi);
+    if (lane == 0) ends[warp] = make_uint2(lo, hi);
+    *reinterpret_cast<int2 *>(bins + 2 * tid) = make_int2(0, 0);
+    __syncthreads();
+    const uint2 e = ends[lane % WARPS];
+    lo = __reduce_min_sync(~0u, e.x);
+    hi = __reduce_max_sync(~0u, e.y);
+    auto key_of = [&](int i) { return cached > 0 ? held[i] : score(i); };
+
+    uint32_t t = ~0u;
+    int need = p.budget - p.sink - p.recent;  // of the range, the largest ones
+    while (need > 0) {
+        const int shift = max(0, 32 - __clz(hi - lo) - BIN_BITS);
+        for (int i = p.sink + tid; i < P - p.recent; i += kSelectThreads) {
+            const uint32_t key = key_of(i);
+            if (key >= lo && key <= hi) atomicAdd(&bins[BINS - 1 - ((key - lo) >> shift)], 1);  // the largest first
         }
         __syncthreads();
-        int eq_before = equal, more_before = taken;
-        for (int w = 0; w < W; ++w) {
-            if (w < warp) {
-                eq_before += warp_a[w];
-                more_before += warp_b[w];
-            }
-            equal += warp_a[w];
-            taken += warp_b[w];
+        const int2 c = *reinterpret_cast<const int2 *>(bins + 2 * tid);
+        int incl = c.x + c.y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(~0u, incl, o);
+            if (lane >= o) incl += x;
         }
-        const unsigned below = (1u << lane) - 1u;
-        eq_before += __popc(me & below);
-        more_before += __popc(mm & below);
-        if (more || (eq && eq_before < (int)left)) {
-            const int at = more_before + min(eq_before, (int)left);
+        if (lane == 31) sums[warp].x = incl;
+        __syncthreads();
+        *reinterpret_cast<int2 *>(bins + 2 * tid) = make_int2(0, 0);
+        int before = lane < warp ? sums[lane].x : 0;  // (WARPS <= 32)
+        before = __reduce_add_sync(~0u, before) + incl - c.x - c.y;
+        if (before < need && before + c.x + c.y >= need) {  // the range's end lies in one of the thread's bins
+            const bool second = before + c.x < need;
+            found[0] = BINS - 1 - (2 * tid + (second ? 1 : 0));
+            found[1] = need - before - (second ? c.x : 0);
+        }
+        __syncthreads();
+        need = found[1];
+        lo += (uint32_t)found[0] << shift;
+        if (shift == 0) {
+            t = lo;
+            break;
+        }
+        hi = min(hi, lo + ((1u << shift) - 1u));
+    }
+    __syncthreads();
+    // of the pages that score more all are taken, of those that score t the first
+    const int run = (P + kSelectThreads - 1) / kSelectThreads;
+    const int i0 = min(tid * run, P), i1 = min(i0 + run, P);
+    int equal = 0, more = 0;
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t key = key_of(i);
+        equal += key == t;
+        more += key > t;
+    }
+    int eq_before = equal, more_before = more;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(~0u, eq_before, o), y = __shfl_up_sync(~0u, more_before, o);
+        if (lane >= o) {
+            eq_before += x;
+            more_before += y;
+        }
+    }
+    if (lane == 31) sums[warp] = make_int2(eq_before, more_before);
+    __syncthreads();
+    eq_before -= equal;
+    more_before -= more;
+    int all_more = 0;
+    for (int w = 0; w < WARPS; ++w) {
+        const int2 x = sums[w];
+        if (w < warp) {
+            eq_before += x.x;
+            more_before += x.y;
+        }
+        all_more += x.y;
+    }
+    const int take = p.budget - all_more;  // of score t
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t key = key_of(i);
+        if (key > t || (key == t && eq_before < take)) {
+            const int at = more_before + min(eq_before, take);
             p.block_table_out[to + at] = table[i];
             p.index_out[to + at] = i;
         }
+        eq_before += key == t;
+        more_before += key > t;
     }
 }
 
 template <typename T, int HD>
 cudaError_t launch_select(const CacheSelectParams &p, cudaStream_t st) {
-    const int64_t items = (int64_t)p.batch * p.Hkv, chunks = ((int64_t)p.max_pages + kScorePages - 1) / kScorePages;
+    const int64_t items = (int64_t)p.batch * p.Hkv;
     if (items > 0x7fffffff) return cudaErrorInvalidValue;
     if (p.max_pages <= p.budget) {  // nothing to choose
-        select_kernel<<<(unsigned)items, kSelectThreads, 0, st>>>(p);
+        select_kernel<<<(unsigned)items, kSelectThreads, 0, st>>>(p, 0);
         return cudaGetLastError();
     }
-    if (items * chunks > 0x7fffffff) return cudaErrorInvalidValue;
-    score_kernel<T, HD><<<(unsigned)(items * chunks), kScorePages, 0, st>>>(p, (int)chunks);
-    const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_after(select_kernel, dim3((unsigned)items), kSelectThreads, st, p);
+    // enough shares to fill the GPU, of one group of pages a warp at least
+    const int64_t most = ((int64_t)p.max_pages + 32 * kScoreWarps - 1) / (32 * kScoreWarps);
+    int64_t splits = (kScoreBlocks + items - 1) / items;
+    splits = splits < 1 ? 1 : splits > most ? most : splits;
+    if (items * splits > 0x7fffffff) return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> done{0}, done_select{0};
+    auto score = score_kernel<T, HD>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(score), ScoreSmem<HD>::bytes(kScoreRows), done);
+    if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void *>(select_kernel), kSelectCached * 4, done_select);
+    if (e != cudaSuccess) return e;
+    score<<<(unsigned)(items * splits), 32 * kScoreWarps, ScoreSmem<HD>::bytes(p.D * p.G), st>>>(p, (int)splits);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int cached = p.max_pages <= kSelectCached ? p.max_pages : 0;
+    return launch_after_smem(select_kernel, dim3((unsigned)items), kSelectThreads, cached * 4, st, p, cached);
 }
 
 template <typename T>
