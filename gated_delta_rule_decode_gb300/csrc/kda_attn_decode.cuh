@@ -124,8 +124,13 @@ template <bool PARTS>
 __device__ __forceinline__ int limit_of(const AttnDecodeParams &p, int n, int len, int row) {
     if constexpr (PARTS) {
         const AttnChunk &c = p.chunks[n];
-        const int tok = c.tok0 + row / p.G;
-        const int at = capped_len(p, tok / p.D) - p.D + 1 + tok % p.D - c.base;
+        int at = c.limit;
+        if (at != AttnChunk::kManySequences) {
+            at += row / p.G;
+        } else {
+            const int tok = c.tok0 + row / p.G;
+            at = capped_len(p, tok / p.D) - p.D + 1 + tok % p.D - c.base;
+        }
         return at <= 0 ? len : min(at, len);
     } else {
         return len - p.D + 1 + row / p.G;

@@ -48,7 +48,8 @@ struct AttnChunk {
     int64_t table;  // of the run's first page in block_table
     int32_t tok0, rows, base, len;
     int32_t seen;   // positions that all rows see which see any
-    int32_t pad;
+    int32_t limit;  // positions of the run that the first token sees, each further one a position more; or
+    static constexpr int32_t kManySequences = -0x7fffffff;  // as seq_lens tells
 };
 
 struct AttnDecodeParams {

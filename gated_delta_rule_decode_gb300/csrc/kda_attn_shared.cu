@@ -3,11 +3,13 @@
 //
 //   o = (sum_prefix e^{s_j} v_j + sum_rest e^{s_j} v_j) / (the same sums of e^{s_j})
 //
-// Four launches: plan_kernel lays the batch out as chunks (up to R query rows of
-// one group and its prefix; a sequence's rows and the rest of it), the chunks of
-// the prefixes and those of the rests are attended as items of the cache
-// attention kernels, whose results stay apart as (o, m, l), and merge_kernel
-// adds up all parts of a row in a fixed order.
+// plan_kernel lays the batch out as chunks: up to R query rows of one group and
+// its prefix; a sequence's rows and the rest of it.  The chunks are attended as
+// items of a kernel whose results stay apart as (o, m, l): on tcgen05 (bf16,
+// d = 64 and 128; kda_attn_shared_tc.cu) all in one launch, whose workers' ranges
+// the plan cuts by cost; otherwise by the kernels of kda_attn_decode_rows.cuh,
+// the prefixes' chunks and then the others'.  merge_kernel adds up all parts of
+// a row in a fixed order.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -15,6 +17,7 @@
 
 #include "kda_attn_decode.cuh"
 #include "kda_attn_internal.h"
+#include "kda_attn_shared.cuh"
 
 namespace kda {
 namespace {
@@ -29,48 +32,86 @@ struct SeqPlan {
     int32_t base, first, token, pad;
 };
 
-// The workspace, in bytes: the plan, the results of whole items, and a
-// workspace of each of the two attention launches.
+// The tcgen05 workers' costs, in half blocks of 64 positions of up to 128 rows: a
+// page of a chunk of more rows is two, an item's start and end about kItemCost.
+constexpr int kItemCost = 6;
+constexpr int kFewRows = 16;       // of a kv head, up to which a sequence's rest is for the warps' kernel
+constexpr int kPlanCached = 2048;  // chunks whose costs fit the plan's shared memory
+
+// Where the parts of one of the two attentions are: an item's workers (first,
+// last) in desc, two slots a worker of PR rows each, RB items a chunk and kv head
+// of R rows.
+struct PartsAt {
+    int64_t desc, part_m, part_l, part_o, ml, o;  // bytes
+    int64_t workers, chunks;
+    int32_t R, RB, PR, tokens, per;  // tokens of a chunk; chunks of a sequence's rest
+    int32_t whole;                   // no item is cut
+};
+
+// The workspace, in bytes: the plan, the results of whole items, and the parts.
 struct SharedLayout {
-    int64_t group_chunk, seqs, prefix_chunks, rest_chunks, prefix_ml, rest_ml, prefix_o, rest_o, prefix_ws, rest_ws, total;
-    Layout prefix, rest;
-    int64_t prefix_count, rest_count;
-    int32_t prefix_tokens, rest_tokens, per_seq;  // tokens of a chunk; chunks of a sequence's rest
+    int64_t group_chunk, seqs, chunks, costs, starts, total;
+    PartsAt at[2];  // of the prefixes, of the rest
+    int64_t ws[2];  // off tcgen05: workspaces of the two launches
+    Layout lay[2];
+    int32_t tc[2], workers;
 };
 
 SharedLayout shared_layout(int Hq, int Hkv, int d, int dtype, int64_t batch, int D, int64_t max_pages, int64_t groups) {
-    auto align = [](int64_t x) { return (x + 255) / 256 * 256; };
     const int G = Hq / Hkv;
     SharedLayout l{};
-    // a chunk has the whole tokens that fit an item's rows: of a group of mean size, of a sequence
-    const int64_t mean = (batch + groups - 1) / std::max<int64_t>(groups, 1) * D * G;
-    auto tokens = [&](int64_t rows) {
-        return std::max(1, make_parts_layout(1, (int)std::min<int64_t>(rows, 4096), Hkv, d, dtype, max_pages).R / G);
-    };
-    l.prefix_tokens = tokens(std::max<int64_t>(mean, G));
-    l.rest_tokens = std::min(D, tokens((int64_t)D * G));
-    l.per_seq = (D + l.rest_tokens - 1) / l.rest_tokens;
-    l.prefix_count = groups > 0 ? batch * D / l.prefix_tokens + groups : 0;
-    l.rest_count = batch * l.per_seq;
-    l.prefix = make_parts_layout(l.prefix_count, l.prefix_tokens * G, Hkv, d, dtype, max_pages);
-    l.rest = make_parts_layout(l.rest_count, l.rest_tokens * G, Hkv, d, dtype, max_pages);
-    const int64_t q = batch * D * Hq;
+    // on tcgen05: prefixes, and rests of more rows than a warp's tile (see lay_out)
+    l.tc[0] = dtype == KDA_DT_BF16 && d >= 64;
+    l.tc[1] = l.tc[0] && D * G > kFewRows;
+    l.workers = kSms;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
-        at += align(bytes);
+        at += (bytes + 255) / 256 * 256;
         return here;
     };
+    // a chunk has the whole tokens that fit an item's rows: of a group of mean size, of a sequence
+    const int64_t mean = (batch + groups - 1) / std::max<int64_t>(groups, 1) * D * G;
+    auto tokens = [&](int s, int64_t rows) {
+        if (l.tc[s]) return kPartRows / G;
+        return std::max(1, make_parts_layout(1, (int)std::min<int64_t>(rows, 4096), Hkv, d, dtype, max_pages).R / G);
+    };
+    l.at[0].tokens = tokens(0, std::max<int64_t>(mean, G));
+    l.at[1].tokens = std::min(D, tokens(1, (int64_t)D * G));
+    l.at[1].per = (D + l.at[1].tokens - 1) / l.at[1].tokens;
+    l.at[0].chunks = groups > 0 ? batch * D / l.at[0].tokens + groups : 0;
+    l.at[1].chunks = batch * l.at[1].per;
+    const int64_t count = l.at[0].chunks + l.at[1].chunks, q = batch * D * Hq;
     l.group_chunk = take(groups * 4);
     l.seqs = take(batch * (int64_t)sizeof(SeqPlan));
-    l.prefix_chunks = take(l.prefix_count * (int64_t)sizeof(AttnChunk));
-    l.rest_chunks = take(l.rest_count * (int64_t)sizeof(AttnChunk));
-    l.prefix_ml = take(q * 8);
-    l.rest_ml = take(q * 8);
-    l.prefix_o = take(q * d * 4);
-    l.rest_o = take(q * d * 4);
-    l.prefix_ws = take(l.prefix.total * 4);
-    l.rest_ws = take(l.rest.total * 4);
+    l.chunks = take(count * (int64_t)sizeof(AttnChunk));
+    for (int s = 0; s < 2; ++s) {
+        l.at[s].ml = take(q * 8);
+        l.at[s].o = take(q * d * 4);
+    }
+    if (l.tc[0]) {
+        l.costs = take(count * 8);
+        l.starts = take((l.workers + 1) * (int64_t)sizeof(int4));
+        const int64_t rows = 2 * (int64_t)l.workers * kPartRows;
+        const int64_t desc = take(count * Hkv * 8), part_m = take(rows * 4), part_l = take(rows * 4), part_o = take(rows * d * 4);
+        for (int s = 0; s < 2; ++s) {
+            PartsAt &a = l.at[s];
+            a.desc = desc + (s == 0 ? 0 : l.at[0].chunks * Hkv * 8);
+            a.part_m = part_m; a.part_l = part_l; a.part_o = part_o;
+            a.workers = l.workers; a.R = a.PR = kPartRows; a.RB = 1;
+        }
+    }
+    for (int s = 0; s < 2; ++s) {
+        if (l.tc[s]) continue;
+        PartsAt &a = l.at[s];
+        const Layout y = make_parts_layout(a.chunks, a.tokens * G, Hkv, d, dtype, max_pages);
+        const int64_t ws = take(y.total * 4);
+        a.desc = ws + 4 * y.desc;
+        a.part_m = ws + 4 * y.part_m; a.part_l = ws + 4 * y.part_l; a.part_o = ws + 4 * y.part_o;
+        a.workers = y.workers; a.R = y.R; a.RB = y.RB; a.PR = y.PR; a.whole = y.whole;
+        l.lay[s] = y;
+        l.ws[s] = ws;
+    }
     l.total = at;
     return l;
 }
@@ -106,7 +147,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
     unsigned char *ws = static_cast<unsigned char *>(p.call.workspace);
     int32_t *group_chunk = reinterpret_cast<int32_t *>(ws + lay.group_chunk);
     SeqPlan *seqs = reinterpret_cast<SeqPlan *>(ws + lay.seqs);
-    AttnChunk *prefix = reinterpret_cast<AttnChunk *>(ws + lay.prefix_chunks), *rest = reinterpret_cast<AttnChunk *>(ws + lay.rest_chunks);
+    AttnChunk *prefix = reinterpret_cast<AttnChunk *>(ws + lay.chunks), *rest = prefix + lay.at[0].chunks;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = p.call.D;
 
@@ -116,7 +158,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
         int mine = 0;
         if (g0 + tid < p.groups) {
             const Group g = group_of(p, g0 + tid, true);
-            if (g.pages > 0) mine = (g.count * D + lay.prefix_tokens - 1) / lay.prefix_tokens;
+            if (g.pages > 0) mine = (g.count * D + lay.at[0].tokens - 1) / lay.at[0].tokens;
         }
         int incl = mine;
 #pragma unroll
@@ -134,20 +176,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
         if (g0 + tid < p.groups) group_chunk[g0 + tid] = at;
         __syncthreads();
     }
-    const int used = (int)min((int64_t)before, lay.prefix_count);
+    const int used = (int)min((int64_t)before, lay.at[0].chunks);
 
     // the prefixes' chunks
-    for (int c = tid; c < lay.prefix_count; c += kPlanThreads) {
+    for (int c = tid; c < lay.at[0].chunks; c += kPlanThreads) {
         AttnChunk out{};
         if (c < used) {
             const int gi = last_at_most(group_chunk, p.groups, c);
             const Group g = group_of(p, gi, false);
-            const int t0 = (c - group_chunk[gi]) * lay.prefix_tokens, tokens = min(lay.prefix_tokens, g.count * D - t0);
+            const int t0 = (c - group_chunk[gi]) * lay.at[0].tokens, tokens = min(lay.at[0].tokens, g.count * D - t0);
             if (tokens > 0) {
                 out.table = (int64_t)g.first * p.call.max_pages;
                 out.tok0 = g.first * D + t0;
                 out.rows = tokens * p.call.G;
                 out.len = out.seen = g.pages * kPage;
+                out.limit = AttnChunk::kManySequences;
                 for (int n = out.tok0 / D; n <= (out.tok0 + tokens - 1) / D; ++n) {
                     const int len = capped_len(p.call, n);
                     if (len > 0) out.seen = min(out.seen, max(1, len - D + 1));
@@ -170,25 +213,92 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
             }
         }
         seqs[n] = out;
-        for (int i = 0; i < lay.per_seq; ++i) {
+        for (int i = 0; i < lay.at[1].per; ++i) {
             AttnChunk c{};
-            const int t0 = i * lay.rest_tokens;
+            const int t0 = i * lay.at[1].tokens;
             c.table = (int64_t)n * p.call.max_pages + out.base / kPage;
             c.tok0 = n * D + t0;
-            c.rows = min(lay.rest_tokens, D - t0) * p.call.G;
+            c.rows = min(lay.at[1].tokens, D - t0) * p.call.G;
             c.base = out.base;
             c.len = max(0, len - out.base);
-            c.seen = min(c.len, max(1, len - D + 1 + t0 - out.base));
-            rest[(int64_t)n * lay.per_seq + i] = c;
+            c.limit = len - D + 1 + t0 - out.base;
+            c.seen = min(c.len, max(1, c.limit));
+            rest[(int64_t)n * lay.at[1].per + i] = c;
         }
+    }
+    if (!lay.tc[0]) return;
+
+    // ---- the workers' ranges: the chunks' costs laid end to end, cut evenly
+    __shared__ int64_t cached[kPlanCached];
+    __shared__ int64_t warp_cost[kPlanThreads / 32];
+    __shared__ int4 starts[kSms + 1];
+    const int count = (int)(lay.at[0].chunks + (lay.tc[1] ? lay.at[1].chunks : 0)), Hkv = p.call.Hkv;
+    int64_t *costs = count <= kPlanCached ? cached : reinterpret_cast<int64_t *>(ws + lay.costs);
+    __syncthreads();  // (the chunks are written)
+    auto weight = [&](const AttnChunk &c) { return c.rows > 128 ? 2 : 1; };
+    auto item_cost = [&](const AttnChunk &c) { return c.len > 0 ? kItemCost + (c.len + kPage - 1) / kPage * weight(c) : 0; };
+    int64_t sum = 0;
+    for (int c0 = 0; c0 < count; c0 += kPlanThreads) {
+        const int64_t mine = c0 + tid < count ? (int64_t)item_cost(prefix[c0 + tid]) * Hkv : 0;
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(~0u, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) warp_cost[warp] = incl;
+        __syncthreads();
+        int64_t at = sum + incl - mine;
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            if (w < warp) at += warp_cost[w];
+            sum += warp_cost[w];
+        }
+        if (c0 + tid < count) costs[c0 + tid] = at;  // before the chunk
+        __syncthreads();
+    }
+    // no more workers than have a block of their own (starts that differ), however the cuts are rounded
+    const int W = (int)max((int64_t)1, min((int64_t)lay.workers, sum / (kItemCost + 4)));
+    if (tid <= lay.workers) {
+        int4 start = make_int4(count, 0, 0, 0);
+        if (tid < W && sum > 0) {
+            const int64_t target = sum * tid / W;
+            int lo = 0, hi = count;  // the last chunk with costs[c] <= target
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (costs[mid] <= target) lo = mid;
+                else hi = mid;
+            }
+            const AttnChunk c = prefix[lo];
+            const int64_t rem = target - costs[lo];
+            const int each = item_cost(c), head = (int)(rem / each), in = (int)(rem % each);
+            start = make_int4(lo, head, in <= kItemCost ? 0 : ((in - kItemCost) / weight(c)) & ~1, 0);
+        }
+        starts[tid] = start;
+        reinterpret_cast<int4 *>(ws + lay.starts)[tid] = start;
+    }
+    __syncthreads();
+    // the first and last worker of each item
+    int2 *desc = reinterpret_cast<int2 *>(ws + lay.at[0].desc);  // (the rest's follow the prefixes')
+    for (int64_t i = tid; i < (int64_t)count * Hkv; i += kPlanThreads) {
+        const int c = (int)(i / Hkv), h = (int)(i % Hkv), pages = (prefix[c].len + kPage - 1) / kPage;
+        auto worker_of = [&](int page) {
+            int lo = 0, hi = W;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                const int4 x = starts[mid];
+                if (x.x < c || (x.x == c && (x.y < h || (x.y == h && x.z <= page)))) lo = mid;
+                else hi = mid;
+            }
+            return lo;
+        };
+        desc[i] = pages > 0 ? make_int2(worker_of(0), worker_of(pages - 1)) : make_int2(0, -1);
     }
 }
 
 // A row's parts of one of the two attentions.
 struct Parts {
-    const float *ws;  // of the attention's launch
-    int64_t first;    // worker of the first part; -1: one result, in the rows' arrays
-    int count, row;   // row within the item's partial results
+    int64_t first;   // worker of the first part; -1: one result, at the row
+    int count, row;  // row within the item's partial results
 };
 
 // Adds up the parts of a row: a block takes a row, its groups of HD / 4 threads
@@ -215,21 +325,18 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const AttnSharedPa
     Parts from[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const Layout &l = s == 0 ? lay.prefix : lay.rest;
-        const int tokens = s == 0 ? lay.prefix_tokens : lay.rest_tokens;
+        const PartsAt &a = lay.at[s];
         const int local = s == 0 ? sp.token + t : t;
-        const int64_t chunk = s == 0 ? (int64_t)sp.first + local / tokens : (int64_t)n * lay.per_seq + local / tokens;
-        const int row = (local % tokens) * c.G + gi, rb = row / l.R;
-        const int64_t item = (chunk * c.Hkv + h) * l.RB + rb;
+        const int64_t chunk = (s == 0 ? (int64_t)sp.first : (int64_t)n * a.per) + local / a.tokens;
+        const int row = (local % a.tokens) * c.G + gi, rb = row / a.R;
         Parts &f = from[s];
-        f.ws = reinterpret_cast<const float *>(ws + (s == 0 ? lay.prefix_ws : lay.rest_ws));
-        f.row = row - rb * l.R;
+        f.row = row - rb * a.R;
         f.first = -1;
-        f.count = (s == 0 ? min(sees, sp.base) : sees - sp.base) > 0 && chunk < (s == 0 ? lay.prefix_count : lay.rest_count) ? 1 : 0;
-        if (f.count > 0 && !l.whole) {
-            const int2 desc = *reinterpret_cast<const int2 *>(f.ws + l.desc + 2 * item);
+        f.count = (s == 0 ? min(sees, sp.base) : sees - sp.base) > 0 && chunk < a.chunks ? 1 : 0;
+        if (f.count > 0 && !a.whole) {
+            const int2 desc = *reinterpret_cast<const int2 *>(ws + a.desc + 8 * ((chunk * c.Hkv + h) * a.RB + rb));
             // (a worker that gave up waiting leaves no or stale entries)
-            if (desc.x < 0 || desc.x > desc.y || desc.y >= l.workers) f.count = 0;
+            if (desc.x < 0 || desc.x > desc.y || desc.y >= a.workers) f.count = 0;
             else if (desc.y > desc.x) {
                 f.first = desc.x;
                 f.count = desc.y - desc.x + 1;
@@ -241,18 +348,18 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const AttnSharedPa
     auto at = [&](int x, float &m, float &l, const float *&o) {
         const int s = x < from[0].count ? 0 : 1;
         const Parts f = s == 0 ? from[0] : from[1];
-        const Layout &y = s == 0 ? lay.prefix : lay.rest;
+        const PartsAt &a = lay.at[s];
         if (s == 1) x -= from[0].count;
         if (f.first < 0) {
-            const float2 ml = reinterpret_cast<const float2 *>(ws + (s == 0 ? lay.prefix_ml : lay.rest_ml))[qrow];
+            const float2 ml = reinterpret_cast<const float2 *>(ws + a.ml)[qrow];
             m = ml.x;
             l = ml.y;
-            o = reinterpret_cast<const float *>(ws + (s == 0 ? lay.prefix_o : lay.rest_o)) + qrow * HD;
+            o = reinterpret_cast<const float *>(ws + a.o) + qrow * HD;
         } else {  // part x lies in slot 2 (w + x), the first in slot 2 w + 1
-            const int64_t k = (2 * (f.first + x) + (x == 0 ? 1 : 0)) * y.PR + f.row;
-            m = f.ws[y.part_m + k];
-            l = f.ws[y.part_l + k];
-            o = f.ws + y.part_o + k * HD;
+            const int64_t k = (2 * (f.first + x) + (x == 0 ? 1 : 0)) * a.PR + f.row;
+            m = reinterpret_cast<const float *>(ws + a.part_m)[k];
+            l = reinterpret_cast<const float *>(ws + a.part_l)[k];
+            o = reinterpret_cast<const float *>(ws + a.part_o) + k * HD;
         }
     };
     float m = -INFINITY;
@@ -317,22 +424,38 @@ size_t attn_shared_workspace_bytes(int Hq, int Hkv, int d, int dtype, int64_t ba
 cudaError_t launch_attn_shared(const AttnSharedParams &p, int d, int dtype, cudaStream_t st) {
     const AttnDecodeParams &c = p.call;
     const SharedLayout lay = shared_layout(c.Hq, c.Hkv, d, dtype, c.batch, c.D, c.max_pages, p.groups);
-    if ((int64_t)c.batch * c.D * c.Hq > 0x7fffffff || lay.prefix_count > 0x7fffffff) return cudaErrorInvalidValue;
+    if ((int64_t)c.batch * c.D * c.Hq > 0x7fffffff || lay.at[0].chunks + lay.at[1].chunks > 0x7fffffff) return cudaErrorInvalidValue;
     unsigned char *ws = static_cast<unsigned char *>(c.workspace);
     plan_kernel<<<1, kPlanThreads, 0, st>>>(p, lay);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    for (int s = 0; s < 2; ++s) {
-        const bool prefix = s == 0;
-        if (c.max_pages == 0 || (prefix ? lay.prefix_count : lay.rest_count) == 0) continue;
+    const AttnChunk *chunks = reinterpret_cast<const AttnChunk *>(ws + lay.chunks);
+    auto floats = [&](int64_t at) { return reinterpret_cast<float *>(ws + at); };
+    if (lay.tc[0] && c.max_pages > 0) {
         AttnDecodeParams q = c;
-        q.chunks = reinterpret_cast<const AttnChunk *>(ws + (prefix ? lay.prefix_chunks : lay.rest_chunks));
-        q.part_ml = reinterpret_cast<float2 *>(ws + (prefix ? lay.prefix_ml : lay.rest_ml));
-        q.out = ws + (prefix ? lay.prefix_o : lay.rest_o);
+        q.chunks = chunks;
+        PartsPlan plan{};
+        plan.starts = reinterpret_cast<const int4 *>(ws + lay.starts);
+        plan.part = floats(0);
+        plan.part_m = lay.at[0].part_m / 4; plan.part_l = lay.at[0].part_l / 4; plan.part_o = lay.at[0].part_o / 4;
+        plan.prefix_o = floats(lay.at[0].o); plan.rest_o = floats(lay.at[1].o);
+        plan.prefix_ml = reinterpret_cast<float2 *>(ws + lay.at[0].ml);
+        plan.rest_ml = reinterpret_cast<float2 *>(ws + lay.at[1].ml);
+        plan.first_rest = (int32_t)lay.at[0].chunks;
+        plan.rows = kPartRows;
+        e = launch_parts_tc(q, plan, lay.workers, d, st);
+        if (e != cudaSuccess) return e;
+    }
+    for (int s = 0; s < 2; ++s) {
+        if (lay.tc[s] || c.max_pages == 0 || lay.at[s].chunks == 0) continue;
+        AttnDecodeParams q = c;
+        q.chunks = chunks + (s == 0 ? 0 : lay.at[0].chunks);
+        q.part_ml = reinterpret_cast<float2 *>(ws + lay.at[s].ml);
+        q.out = ws + lay.at[s].o;
         q.lse = nullptr;
-        q.workspace = ws + (prefix ? lay.prefix_ws : lay.rest_ws);
-        q.batch = (int32_t)(prefix ? lay.prefix_count : lay.rest_count);
-        e = launch_parts(q, prefix ? lay.prefix : lay.rest, d, dtype, st);
+        q.workspace = ws + lay.ws[s];
+        q.batch = (int32_t)lay.at[s].chunks;
+        e = launch_parts(q, lay.lay[s], d, dtype, st);
         if (e != cudaSuccess) return e;
     }
     return dtype == KDA_DT_BF16 ? launch_merge<__nv_bfloat16>(p, lay, d, st) : launch_merge<float>(p, lay, d, st);

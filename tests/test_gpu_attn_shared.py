@@ -3,7 +3,7 @@ whole sequences (the shared pages are named by every row of the group)."""
 import pytest
 import torch
 
-from attn_long_testutil import bounds
+from attn_long_testutil import bounds, query_terms
 from attn_testutil import check, gen, make_cache, np64, randn, to_device
 from oracle import attention as ref
 
@@ -50,7 +50,13 @@ def _want(case, q, dtype, lens=None):
     k, v, ks, vs = case[0]
     lens = case[1].numpy() if lens is None else lens
     out, lse, absout, mag, _ = ref.decode(np64(q), k.numpy(), v.numpy(), np64(ks), np64(vs), lens, case[2].numpy())
-    return (out, lse) + bounds(out, absout, mag, q.shape[-1], dtype)
+    return (out, lse) + bounds(out, absout, mag, q.shape[-1], dtype, _terms(case, q, dtype, lens))
+
+
+def _terms(case, q, dtype, lens, scale=None):
+    if dtype != BF or q.shape[-1] < 64:
+        return 0.0
+    return query_terms(np64(q), case[0][0].numpy(), np64(case[0][2]), lens, case[2].numpy(), scale)
 
 
 def _compare(case, q, dtype):
@@ -219,9 +225,29 @@ def test_given_results_scale_and_workspace():
     k, v, ks, vs = case[0]
     want, want_lse, absout, mag, _ = ref.decode(np64(q.bfloat16()), k.numpy(), v.numpy(), np64(ks), np64(vs), case[1].numpy(),
                                                 case[2].numpy(), scale=0.3)
-    tol, tol_lse = bounds(want, absout, mag, 64, BF)
+    tol, tol_lse = bounds(want, absout, mag, 64, BF, _terms(case, q.bfloat16(), BF, case[1].numpy(), 0.3))
     check(out, want, tol, "out")
     check(lse, want_lse, tol_lse, "lse")
     assert a.decode_shared(fused[:0, :, :8], c, lens[:0], table[:0], start[:1] * 0, shared[:0]).shape == (0, 2, 8, 64)
     with pytest.raises(a.KdaError):
         a.decode_shared(fused[:, :, :8], c, lens, table, start, shared, workspace=ws[:-256].clone())
+
+
+def test_queries_of_all_sizes():
+    """Elements far below the row's largest, subnormal and huge rows, and infinities and NaN, which are the row's alone."""
+    g = gen(16)
+    case = _case(g, [(20, [1400, 1290, 1300])], 1, 128)
+    q = randn(g, 3, 2, 10, 128) * torch.exp2(torch.randint(-20, 1, (3, 2, 10, 128), generator=g).float())
+    q[0, 0, 1] *= 2.0 ** -110
+    q[1, 0, 2] = 0
+    q[1, 1, 3] *= 2.0 ** 60
+    q = q.bfloat16()
+    case[0][2].mul_(0).add_(2.0 ** -8)  # (one scale, so that the large row's weights are not all on one key by its page's scale)
+    _compare(case, q, BF)
+    bad = q.clone()
+    bad[0, 1, 4, 7], bad[2, 0, 5, 9] = float("nan"), float("-inf")
+    out, _, flag = _run(case, bad)
+    good, _, _ = _run(case, q)
+    rows = torch.zeros(3, 2, 10, dtype=torch.bool)
+    rows[0, 1, 4] = rows[2, 0, 5] = True
+    assert flag == 0 and torch.isnan(out[rows]).all() and torch.equal(out[~rows], good[~rows])
