@@ -111,35 +111,47 @@ __device__ __forceinline__ int pages_of(const AttnDecodeParams &p, int n, int &l
     return (len + kPage - 1) / kPage;
 }
 
+// What an item of entry n needs to know of it.
+struct Entry {
+    AttnChunk chunk;  // PARTS
+    int n, len;
+};
 template <bool PARTS>
-__device__ __forceinline__ int rows_of(const AttnDecodeParams &p, int n) {
-    return PARTS ? p.chunks[n].rows : p.D * p.G;
+__device__ __forceinline__ Entry entry_of(const AttnDecodeParams &p, int n, int len) {
+    Entry e;
+    if constexpr (PARTS) e.chunk = p.chunks[n];
+    e.n = n;
+    e.len = len;
+    return e;
 }
 template <bool PARTS>
-__device__ __forceinline__ int64_t first_token(const AttnDecodeParams &p, int n) {
-    return PARTS ? (int64_t)p.chunks[n].tok0 : (int64_t)n * p.D;
+__device__ __forceinline__ int rows_of(const AttnDecodeParams &p, const Entry &e) {
+    return PARTS ? e.chunk.rows : p.D * p.G;
 }
-// Positions that row `row` of entry n (of length len) sees.
 template <bool PARTS>
-__device__ __forceinline__ int limit_of(const AttnDecodeParams &p, int n, int len, int row) {
-    if constexpr (PARTS) {
-        const AttnChunk &c = p.chunks[n];
-        int at = c.limit;
-        if (at != AttnChunk::kManySequences) {
-            at += row / p.G;
-        } else {
-            const int tok = c.tok0 + row / p.G;
-            at = capped_len(p, tok / p.D) - p.D + 1 + tok % p.D - c.base;
-        }
-        return at <= 0 ? len : min(at, len);
+__device__ __forceinline__ int64_t first_token(const AttnDecodeParams &p, const Entry &e) {
+    return PARTS ? (int64_t)e.chunk.tok0 : (int64_t)e.n * p.D;
+}
+// Positions that row `row` sees.
+__device__ __forceinline__ int limit_of(const AttnDecodeParams &p, const AttnChunk &c, int row) {
+    int at = c.limit;
+    if (at != AttnChunk::kManySequences) {
+        at += row / p.G;
     } else {
-        return len - p.D + 1 + row / p.G;
+        const int tok = c.tok0 + row / p.G;
+        at = capped_len(p, tok / p.D) - p.D + 1 + tok % p.D - c.base;
     }
+    return at <= 0 ? c.len : min(at, c.len);
 }
-// Positions that every row of entry n sees.
 template <bool PARTS>
-__device__ __forceinline__ int seen_of(const AttnDecodeParams &p, int n, int len) {
-    return PARTS ? p.chunks[n].seen : len - p.D + 1;
+__device__ __forceinline__ int limit_of(const AttnDecodeParams &p, const Entry &e, int row) {
+    if constexpr (PARTS) return limit_of(p, e.chunk, row);
+    else return e.len - p.D + 1 + row / p.G;
+}
+// Positions that every row sees.
+template <bool PARTS>
+__device__ __forceinline__ int seen_of(const AttnDecodeParams &p, const Entry &e) {
+    return PARTS ? e.chunk.seen : e.len - p.D + 1;
 }
 template <bool PARTS>
 __device__ __forceinline__ int page_id(const AttnDecodeParams &p, int n, int h, int page) {
@@ -305,7 +317,6 @@ __device__ __forceinline__ void write_desc(float *ws, const Layout &lay, const U
 
 // Many rows on tcgen05 (bf16, d = 64 or 128).
 cudaError_t launch_tc(const AttnDecodeParams &p, const Layout &lay, int d, cudaStream_t st);
-cudaError_t launch_tc_parts(const AttnDecodeParams &p, const Layout &lay, int d, cudaStream_t st);
 
 }  // namespace dec
 }  // namespace kda

@@ -183,8 +183,9 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
         const int h = un.hr / RB, rb = un.hr % RB;
         const int pages_here = (int)min((int64_t)(un.pages - un.page), count - i);
         const int row0 = rb * R + mt * 8 * NB;  // the warp's first row
-        const int rows_all = rows_of<PARTS>(p, un.n);
-        const int64_t tok0 = first_token<PARTS>(p, un.n);
+        const Entry en = entry_of<PARTS>(p, un.n, un.len);
+        const int rows_all = rows_of<PARTS>(p, en);
+        const int64_t tok0 = first_token<PARTS>(p, en);
         // operand: row g of each tile; accumulators: rows 2 t and 2 t + 1
         uint32_t qb[TERMS][NB][KS][2];
         float qs[NB][2];
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
             for (int e = 0; e < 2; ++e) {
                 qs[nb][e] = __shfl_sync(~0u, back, 4 * (2 * t + e));
                 const int re = row0 + 8 * nb + 2 * t + e;
-                limit[nb][e] = re < rows_all ? limit_of<PARTS>(p, un.n, un.len, re) : 0;
+                limit[nb][e] = re < rows_all ? limit_of<PARTS>(p, en, re) : 0;
             }
         }
         float o[NB][DT][4];
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(32 * MT, warps_per_sm(NB) / MT) decode_attn_ke
                 unit[nb][e] = kNoUnit;
             }
         }
-        const int window0 = seen_of<PARTS>(p, un.n, un.len);  // first position that some row does not see
+        const int window0 = seen_of<PARTS>(p, en);  // first position that some row does not see
 
         for (int pi = 0; pi < pages_here; ++pi, ++i) {
             const int page = un.page + pi;
@@ -547,7 +548,8 @@ cudaError_t launch_main(const AttnDecodeParams &p, const Layout &lay, cudaStream
 
 template <typename T, int HD, bool PARTS>
 cudaError_t launch_items(const AttnDecodeParams &p, const Layout &lay, cudaStream_t st) {
-    if (lay.MT == 0) return PARTS ? launch_tc_parts(p, lay, HD, st) : launch_tc(p, lay, HD, st);
+    if constexpr (!PARTS)
+        if (lay.MT == 0) return launch_tc(p, lay, HD, st);
     if (lay.NB == 1) return launch_main<T, HD, 1, 1, PARTS>(p, lay, st);
     if (lay.MT == 1) return launch_main<T, HD, 2, 1, PARTS>(p, lay, st);
     if (lay.MT == 2) return launch_main<T, HD, 2, 2, PARTS>(p, lay, st);

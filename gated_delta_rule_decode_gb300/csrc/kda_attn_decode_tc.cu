@@ -90,12 +90,11 @@ struct Walk {
         cur = c; u0 = u; count = n; i = 0; left = 0; item = -1; tile = -1; pages = 0;
     }
     // Moves to the next tile; un.page is its first page.
-    template <bool PARTS>
     __device__ __forceinline__ bool next(const AttnDecodeParams &p, int HR) {
         i += pages;
         if (i >= count) return false;
         if (left == 0) {
-            un = locate<PARTS>(p, HR, cur, u0 + i);
+            un = locate<false>(p, HR, cur, u0 + i);
             left = min(un.pages - un.page, count - i);
             first = true;
             page0 = un.page;
@@ -112,7 +111,7 @@ struct Walk {
     }
 };
 
-template <int HD, bool PARTS>
+template <int HD>
 __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnDecodeParams p, const Layout lay) {
     using C = Cfg<HD>;
     using T = __nv_bfloat16;
@@ -152,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
         v_nan = 0;
     }
     int64_t U, W, u0, u1;
-    find_range<T, HD, kWarps, PARTS>(p, HR, lay.whole, exchange, &start, U, W, u0, u1);
+    find_range<T, HD, kWarps, false>(p, HR, lay.whole, exchange, &start, U, W, u0, u1);
     if (u0 >= u1) return;
     if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, kTmem);
     tc::fence_before_sync();
@@ -173,9 +172,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
             if (i >= fetched) {
                 Cursor c = fetch_cur;
                 if (lane < kBatch && fetched + lane < count) {
-                    const Unit un = locate<PARTS>(p, HR, c, u0 + fetched + lane);
+                    const Unit un = locate<false>(p, HR, c, u0 + fetched + lane);
                     const int h = un.hr / RB;
-                    const int id = page_id<PARTS>(p, un.n, h, un.page);
+                    const int id = page_id<false>(p, un.n, h, un.page);
                     meta[(fetched + lane) % kMeta] = page_meta(p, id, h);
                 }
                 const int from = min(kBatch - 1, count - 1 - fetched);
@@ -223,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
         };
         bool ok = true, pfirst = false;
         int pitem = 0;
-        while (ok && wk.next<PARTS>(p, HR)) {
+        while (ok && wk.next(p, HR)) {
             const int j = wk.tile;
             const int b = j & 1;
             ok = warp_wait(&bars.k_ready[b], j >> 1, &abort_flag);
@@ -247,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
         // ---------------- conversion
         const int ct = tid - kConvWarp * 32;  // 0..kConv - 1
         bool ok = true;
-        while (ok && wk.next<PARTS>(p, HR)) {
+        while (ok && wk.next(p, HR)) {
             const int j = wk.tile;
             const int b = j & 1;
             // the buffers' last readers are QK(j - 2) and PV(j - 2); the keys need not wait
@@ -264,8 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                     if (!ok) break;
                 }
                 const int h = wk.un.hr / RB;
-                const int rows_all = rows_of<PARTS>(p, wk.un.n);
-                const int64_t tok0 = first_token<PARTS>(p, wk.un.n);
+                const int rows_all = p.D * p.G;
+                const int64_t tok0 = (int64_t)wk.un.n * p.D;
 #pragma unroll 1
                 for (int x = ct; x < 256; x += kConv) {
                     const int r = x >> 1, half = x & 1;  // two threads per row
@@ -335,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
             // values: 16 positions of a channel at a time
             if (j >= 2) ok = warp_wait(&bars.v_free[b], (j >> 1) - 1, &abort_flag);
             if (!ok) break;
-            const int window0 = seen_of<PARTS>(p, wk.un.n, wk.un.len);
+            const int window0 = wk.un.len - p.D + 1;
 #pragma unroll 1
             for (int pg = 0; pg < 2; ++pg) {
                 unsigned char *dst = sv + b * C::kOp + pg * HD * 128;
@@ -390,19 +389,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
         int limit = 0, unit = kNoUnit;  // the exponent that O is counted in
         bool valid = false, ok = true;
         int64_t qrow = 0;
-        while (wk.next<PARTS>(p, HR)) {
+        while (wk.next(p, HR)) {
             const int j = wk.tile;
             const int b = j & 1;
             const Unit &un = wk.un;
             const int rb = un.hr % RB, h = un.hr / RB, row = rb * 128 + r;
-            const int rows_all = rows_of<PARTS>(p, un.n);
+            const int rows_all = p.D * p.G;
             const bool active = rb * 128 + quad * 32 < rows_all;  // some row of this warp exists
             if (!warp_wait(&bars.s_full[b], j >> 1, &abort_flag)) ok = false;
             tc::fence_after_sync();
             if (wk.first) {
                 valid = row < rows_all;
-                limit = valid ? limit_of<PARTS>(p, un.n, un.len, row) : 0;
-                qrow = valid ? (first_token<PARTS>(p, un.n) + row / p.G) * p.Hq + h * p.G + row % p.G : 0;
+                limit = valid ? un.len - p.D + 1 + row / p.G : 0;
+                qrow = valid ? ((int64_t)un.n * p.D + row / p.G) * p.Hq + h * p.G + row % p.G : 0;
                 qs = __uint_as_float((uint32_t)(127 - 14 + q_exp[wk.item & 1][r]) << 23) * p.scale * kLog2e;
                 m = -INFINITY;
                 l = 0.f;
@@ -436,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                 }
                 const bool have = pg == 0 ? has[0] : has[1];
                 end = have ? limit - (un.page + pg) * kPage : 0;
-                masked = !have || (un.page + pg + 1) * kPage > seen_of<PARTS>(p, un.n, un.len);
+                masked = !have || (un.page + pg + 1) * kPage > un.len - p.D + 1;
                 // (read twice: the maximum first, then the weights)
                 float mx = -INFINITY;
 #pragma unroll 1
@@ -515,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                 }
                 tc::wait_st();
                 l += rs;
-                if (!PARTS && p.weight_out != nullptr && valid && pg < wk.pages)
+                if (p.weight_out != nullptr && valid && pg < wk.pages)
                     ws[lay.page_w + qrow * p.max_pages + un.page + pg] = rs > 0.f ? log2f(rs) + use : -INFINITY;
             }
             tc::fence_before_sync();
@@ -535,11 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                 pair_sync();
                 const float total = l0 + l1;
                 const float in = pow2(unit) * (1.f / (float)(1 << kBias));
-                const float fo = total == 0.f ? 0.f : whole && !PARTS ? 1.f / total : 1.f;
+                const float fo = total == 0.f ? 0.f : whole ? 1.f / total : 1.f;
                 const int64_t slot = 2 * (int64_t)blockIdx.x + (from_start ? 1 : 0);
                 T *dst = static_cast<T *>(p.out) + qrow * HD + pg * (HD / 2);
-                float *part = (PARTS && whole ? static_cast<float *>(p.out) + qrow * HD : ws + lay.part_o + (slot * lay.PR + r) * HD) +
-                              pg * (HD / 2);
+                float *part = ws + lay.part_o + (slot * lay.PR + r) * HD + pg * (HD / 2);
                 const bool nan = v_nan != 0;
 #pragma unroll 1
                 for (int c = 0; c < HD / 2; c += 16) {
@@ -552,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                     for (int e = 0; e < 16; ++e) o[e] = fo == 0.f ? 0.f : o[e] * in * fo;
                     if (nan) {  // the NaN values that this row sees
                         asm volatile("" ::: "memory");
-                        for (int pos = max(seen_of<PARTS>(p, un.n, un.len), 0); pos < limit; ++pos) {
-                            const int block = page_meta(p, page_id<PARTS>(p, un.n, h, pos / kPage), h).block;
+                        for (int pos = max(un.len - p.D + 1, 0); pos < limit; ++pos) {
+                            const int block = page_meta(p, page_id<false>(p, un.n, h, pos / kPage), h).block;
                             if (block < 0) continue;
                             const unsigned char *vb = p.v_pages + (int64_t)block * C::kHalf +
                                                       (pg * (HD / 2) + c) * kPage + pos % kPage;
@@ -562,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                                 if ((vb[e * kPage] & 0x7f) == 0x7f) o[e] = NAN;
                         }
                     }
-                    if (whole && !PARTS) {
+                    if (whole) {
 #pragma unroll
                         for (int e = 0; e < 16; e += 8)
                             *reinterpret_cast<uint4 *>(dst + c + e) =
@@ -575,9 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
                     }
                 }
                 if (valid && ok && pg == 0) {
-                    if (PARTS && whole) {
-                        p.part_ml[qrow] = make_float2(m, total);
-                    } else if (whole) {
+                    if (whole) {
                         const float lse2 = total == 0.f ? -INFINITY : m + log2f(total);
                         if (p.lse) p.lse[qrow] = lse2 * kLn2;
                         if (p.weight_out) ws[lay.lse2 + qrow] = lse2;
@@ -600,9 +596,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_tc_kernel(const AttnD
     if (tid == 0 && abort_flag && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_TIMEOUT);
 }
 
-template <int HD, bool PARTS>
+template <int HD>
 cudaError_t launch_dim(const AttnDecodeParams &p, const Layout &lay, cudaStream_t st) {
-    auto kern = decode_attn_tc_kernel<HD, PARTS>;
+    auto kern = decode_attn_tc_kernel<HD>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), Cfg<HD>::kBytes, done);
     if (e != cudaSuccess) return e;
@@ -615,11 +611,7 @@ cudaError_t launch_dim(const AttnDecodeParams &p, const Layout &lay, cudaStream_
 namespace dec {
 
 cudaError_t launch_tc(const AttnDecodeParams &p, const Layout &lay, int d, cudaStream_t st) {
-    return d == 128 ? launch_dim<128, false>(p, lay, st) : launch_dim<64, false>(p, lay, st);
-}
-
-cudaError_t launch_tc_parts(const AttnDecodeParams &p, const Layout &lay, int d, cudaStream_t st) {
-    return d == 128 ? launch_dim<128, true>(p, lay, st) : launch_dim<64, true>(p, lay, st);
+    return d == 128 ? launch_dim<128>(p, lay, st) : launch_dim<64>(p, lay, st);
 }
 
 }  // namespace dec

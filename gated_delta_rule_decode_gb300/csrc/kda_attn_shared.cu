@@ -144,6 +144,8 @@ __device__ __forceinline__ int last_at_most(const int32_t *a, int n, int x) {
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedParams p, const SharedLayout lay) {
     __shared__ int warp_sum[kPlanThreads / 32];
+    __shared__ int sizes[kPlanCached];  // of the chunks: pages, and whether they are of more than 128 rows
+    auto size_of = [](const AttnChunk &c) { return 2 * ((c.len + kPage - 1) / kPage) + (c.rows > 128 ? 1 : 0); };
     unsigned char *ws = static_cast<unsigned char *>(p.call.workspace);
     int32_t *group_chunk = reinterpret_cast<int32_t *>(ws + lay.group_chunk);
     SeqPlan *seqs = reinterpret_cast<SeqPlan *>(ws + lay.seqs);
@@ -178,8 +180,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
     }
     const int used = (int)min((int64_t)before, lay.at[0].chunks);
 
-    // the prefixes' chunks
-    for (int c = tid; c < lay.at[0].chunks; c += kPlanThreads) {
+    // the prefixes' chunks, a warp each: a lane a sequence
+    __syncthreads();
+    for (int c = warp; c < lay.at[0].chunks; c += kPlanThreads / 32) {
         AttnChunk out{};
         if (c < used) {
             const int gi = last_at_most(group_chunk, p.groups, c);
@@ -191,13 +194,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
                 out.rows = tokens * p.call.G;
                 out.len = out.seen = g.pages * kPage;
                 out.limit = AttnChunk::kManySequences;
-                for (int n = out.tok0 / D; n <= (out.tok0 + tokens - 1) / D; ++n) {
+                for (int n = out.tok0 / D + lane; n <= (out.tok0 + tokens - 1) / D; n += 32) {
                     const int len = capped_len(p.call, n);
                     if (len > 0) out.seen = min(out.seen, max(1, len - D + 1));
                 }
             }
         }
-        prefix[c] = out;
+        out.seen = __reduce_min_sync(~0u, out.seen);
+        if (lane == 0) {
+            prefix[c] = out;
+            if (c < kPlanCached) sizes[c] = size_of(out);
+        }
     }
     // the sequences, and the chunks of what follows their prefixes
     for (int n = tid; n < p.call.batch; n += kPlanThreads) {
@@ -224,6 +231,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
             c.limit = len - D + 1 + t0 - out.base;
             c.seen = min(c.len, max(1, c.limit));
             rest[(int64_t)n * lay.at[1].per + i] = c;
+            const int64_t at = lay.at[0].chunks + (int64_t)n * lay.at[1].per + i;
+            if (at < kPlanCached) sizes[at] = size_of(c);
         }
     }
     if (!lay.tc[0]) return;
@@ -235,11 +244,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
     const int count = (int)(lay.at[0].chunks + (lay.tc[1] ? lay.at[1].chunks : 0)), Hkv = p.call.Hkv;
     int64_t *costs = count <= kPlanCached ? cached : reinterpret_cast<int64_t *>(ws + lay.costs);
     __syncthreads();  // (the chunks are written)
-    auto weight = [&](const AttnChunk &c) { return c.rows > 128 ? 2 : 1; };
-    auto item_cost = [&](const AttnChunk &c) { return c.len > 0 ? kItemCost + (c.len + kPage - 1) / kPage * weight(c) : 0; };
+    auto size = [&](int c) { return c < kPlanCached ? sizes[c] : size_of(prefix[c]); };
+    auto weight = [](int size) { return 1 + (size & 1); };
+    auto item_cost = [&](int size) { return size > 1 ? kItemCost + (size >> 1) * weight(size) : 0; };
     int64_t sum = 0;
     for (int c0 = 0; c0 < count; c0 += kPlanThreads) {
-        const int64_t mine = c0 + tid < count ? (int64_t)item_cost(prefix[c0 + tid]) * Hkv : 0;
+        const int64_t mine = c0 + tid < count ? (int64_t)item_cost(size(c0 + tid)) * Hkv : 0;
         int64_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -268,7 +278,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
                 if (costs[mid] <= target) lo = mid;
                 else hi = mid;
             }
-            const AttnChunk c = prefix[lo];
+            const int c = size(lo);
             const int64_t rem = target - costs[lo];
             const int each = item_cost(c), head = (int)(rem / each), in = (int)(rem % each);
             start = make_int4(lo, head, in <= kItemCost ? 0 : ((in - kItemCost) / weight(c)) & ~1, 0);
@@ -280,7 +290,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
     // the first and last worker of each item
     int2 *desc = reinterpret_cast<int2 *>(ws + lay.at[0].desc);  // (the rest's follow the prefixes')
     for (int64_t i = tid; i < (int64_t)count * Hkv; i += kPlanThreads) {
-        const int c = (int)(i / Hkv), h = (int)(i % Hkv), pages = (prefix[c].len + kPage - 1) / kPage;
+        const int c = (int)(i / Hkv), h = (int)(i % Hkv), pages = size(c) >> 1;
         auto worker_of = [&](int page) {
             int lo = 0, hi = W;
             while (hi - lo > 1) {
@@ -295,109 +305,87 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
     }
 }
 
-// A row's parts of one of the two attentions.
-struct Parts {
-    int64_t first;   // worker of the first part; -1: one result, at the row
-    int count, row;  // row within the item's partial results
-};
-
-// Adds up the parts of a row: a block takes a row, its groups of HD / 4 threads
-// every GR-th part, in order; the groups' sums are added in order.
+// Adds up the parts of the rows, in order: HD / 4 lanes a row, four parts' loads in
+// flight together.  A part is (m, l, o) of one of the two attentions, at the row
+// where one worker had all of it, else in the workers' slots.
 constexpr int kMergeThreads = 128;
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const AttnSharedParams p, const SharedLayout lay) {
-    constexpr int TPR = HD / 4, GR = kMergeThreads / TPR;
-    __shared__ float wmax[kMergeThreads / 32];
-    __shared__ float4 so[GR][TPR];
-    __shared__ float sl[GR];
+    constexpr int TPR = HD / 4, ROWS = kMergeThreads / TPR;
     const AttnDecodeParams &c = p.call;
-    const int64_t qrow = blockIdx.x;
+    const int64_t qrow = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+    const int c4 = threadIdx.x % TPR;
+    if (qrow >= (int64_t)c.batch * c.D * c.Hq) return;
     const int hq = (int)(qrow % c.Hq), h = hq / c.G, gi = hq % c.G;
     const int64_t tok = qrow / c.Hq;
-    const int n = (int)(tok / c.D), t = (int)(tok % c.D), tid = threadIdx.x;
+    const int n = (int)(tok / c.D), t = (int)(tok % c.D);
     const unsigned char *ws = static_cast<const unsigned char *>(c.workspace);
+    const int sees = capped_len(c, n) - c.D + 1 + t;  // positions in all
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const SeqPlan sp = reinterpret_cast<const SeqPlan *>(ws + lay.seqs)[n];
-    const int sees = capped_len(c, n) - c.D + 1 + t;  // positions in all
 
-    // where the two attentions left the row's results
-    Parts from[2];
+    // where the two attentions left the row's results: parts (one: at the row), the first part's worker, the row
+    // within the item's partial results
+    int count[2], first[2], row[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const PartsAt &a = lay.at[s];
         const int local = s == 0 ? sp.token + t : t;
         const int64_t chunk = (s == 0 ? (int64_t)sp.first : (int64_t)n * a.per) + local / a.tokens;
-        const int row = (local % a.tokens) * c.G + gi, rb = row / a.R;
-        Parts &f = from[s];
-        f.row = row - rb * a.R;
-        f.first = -1;
-        f.count = (s == 0 ? min(sees, sp.base) : sees - sp.base) > 0 && chunk < a.chunks ? 1 : 0;
-        if (f.count > 0 && !a.whole) {
+        const int r = (local % a.tokens) * c.G + gi, rb = r / a.R;
+        row[s] = r - rb * a.R;
+        first[s] = 0;
+        count[s] = (s == 0 ? min(sees, sp.base) : sees - sp.base) > 0 && chunk < a.chunks ? 1 : 0;
+        if (count[s] > 0 && !a.whole) {
             const int2 desc = *reinterpret_cast<const int2 *>(ws + a.desc + 8 * ((chunk * c.Hkv + h) * a.RB + rb));
             // (a worker that gave up waiting leaves no or stale entries)
-            if (desc.x < 0 || desc.x > desc.y || desc.y >= a.workers) f.count = 0;
-            else if (desc.y > desc.x) {
-                f.first = desc.x;
-                f.count = desc.y - desc.x + 1;
+            first[s] = desc.x;
+            count[s] = desc.x < 0 || desc.x > desc.y || desc.y >= a.workers ? 0 : desc.y - desc.x + 1;
+        }
+    }
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const PartsAt &a = lay.at[s];
+        const float *part_m = reinterpret_cast<const float *>(ws + a.part_m), *part_l = reinterpret_cast<const float *>(ws + a.part_l);
+        const float *part_o = reinterpret_cast<const float *>(ws + a.part_o);
+        constexpr int BATCH = 4;
+        for (int x0 = 0; x0 < count[s]; x0 += BATCH) {
+            float pm[BATCH], pl[BATCH];
+            float4 v[BATCH];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int x = min(x0 + b, count[s] - 1);
+                if (count[s] == 1) {
+                    const float2 ml = reinterpret_cast<const float2 *>(ws + a.ml)[qrow];
+                    pm[b] = ml.x;
+                    pl[b] = ml.y;
+                    v[b] = reinterpret_cast<const float4 *>(ws + a.o)[qrow * TPR + c4];
+                } else {  // part x lies in slot 2 (w + x), the first in slot 2 w + 1
+                    const int64_t k = (2 * ((int64_t)first[s] + x) + (x == 0 ? 1 : 0)) * a.PR + row[s];
+                    pm[b] = part_m[k];
+                    pl[b] = part_l[k];
+                    v[b] = reinterpret_cast<const float4 *>(part_o)[k * TPR + c4];
+                }
+            }
+            float most = m;
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) most = fmaxf(most, pl[b] == 0.f ? m : pm[b]);
+            const float use = most == -INFINITY ? 0.f : most, fix = ex2(m - use);
+            l *= fix;
+            o.x *= fix; o.y *= fix; o.z *= fix; o.w *= fix;
+            m = most;
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                if (x0 + b >= count[s] || pl[b] == 0.f) continue;  // (a part whose pages are not in the cache has l = 0)
+                const float f = ex2(pm[b] - use);
+                l = fmaf(f, pl[b], l);
+                o.x = fmaf(f, v[b].x, o.x); o.y = fmaf(f, v[b].y, o.y);
+                o.z = fmaf(f, v[b].z, o.z); o.w = fmaf(f, v[b].w, o.w);
             }
         }
-    }
-    const int parts = from[0].count + from[1].count;
-    // (m, l) and the output of part x
-    auto at = [&](int x, float &m, float &l, const float *&o) {
-        const int s = x < from[0].count ? 0 : 1;
-        const Parts f = s == 0 ? from[0] : from[1];
-        const PartsAt &a = lay.at[s];
-        if (s == 1) x -= from[0].count;
-        if (f.first < 0) {
-            const float2 ml = reinterpret_cast<const float2 *>(ws + a.ml)[qrow];
-            m = ml.x;
-            l = ml.y;
-            o = reinterpret_cast<const float *>(ws + a.o) + qrow * HD;
-        } else {  // part x lies in slot 2 (w + x), the first in slot 2 w + 1
-            const int64_t k = (2 * (f.first + x) + (x == 0 ? 1 : 0)) * a.PR + f.row;
-            m = reinterpret_cast<const float *>(ws + a.part_m)[k];
-            l = reinterpret_cast<const float *>(ws + a.part_l)[k];
-            o = reinterpret_cast<const float *>(ws + a.part_o) + k * HD;
-        }
-    };
-    float m = -INFINITY;
-    for (int x = tid; x < parts; x += kMergeThreads) {
-        float pm, pl;
-        const float *o;
-        at(x, pm, pl, o);
-        m = fmaxf(m, pm);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    if ((tid & 31) == 0) wmax[tid >> 5] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMergeThreads / 32; ++i) m = fmaxf(m, wmax[i]);
-    const float use = m == -INFINITY ? 0.f : m;
-    const int c4 = tid % TPR, gr = tid / TPR;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x = gr; x < parts; x += GR) {
-        float pm, pl;
-        const float *po;
-        at(x, pm, pl, po);
-        if (pl == 0.f) continue;  // (a part whose pages are not in the cache)
-        const float4 v = *reinterpret_cast<const float4 *>(po + 4 * c4);
-        const float f = ex2(pm - use);
-        l = fmaf(f, pl, l);
-        o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y);
-        o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
-    }
-    so[gr][c4] = o;
-    if (c4 == 0) sl[gr] = l;
-    __syncthreads();
-    if (gr != 0) return;
-    for (int i = 1; i < GR; ++i) {
-        const float4 v = so[i][c4];
-        o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-        l += sl[i];
     }
     const float f = l == 0.f ? 0.f : 1.f / l;
     T *dst = static_cast<T *>(c.out) + qrow * HD + 4 * c4;
@@ -408,7 +396,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const AttnSharedPa
 
 template <typename T>
 cudaError_t launch_merge(const AttnSharedParams &p, const SharedLayout &lay, int d, cudaStream_t st) {
-    const dim3 grid((unsigned)((int64_t)p.call.batch * p.call.D * p.call.Hq));
+    const int64_t rows = (int64_t)p.call.batch * p.call.D * p.call.Hq, each = kMergeThreads / (d / 4);
+    const dim3 grid((unsigned)((rows + each - 1) / each));
     if (d == 128) return launch_after(merge_kernel<T, 128>, grid, kMergeThreads, st, p, lay);
     if (d == 64) return launch_after(merge_kernel<T, 64>, grid, kMergeThreads, st, p, lay);
     return launch_after(merge_kernel<T, 32>, grid, kMergeThreads, st, p, lay);

@@ -120,6 +120,8 @@ struct Items {
             chunk.rows = uniform(x.rows);
             chunk.seen = uniform(x.seen);
             chunk.tok0 = uniform(x.tok0);
+            chunk.base = uniform(x.base);
+            chunk.limit = uniform(x.limit);
             chunk.table = x.table;
             pages = (chunk.len + kPage - 1) / kPage;
             if (page < pages) break;
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
             const int row = 128 * half + r;
             const bool valid = row < it.chunk.rows;
             const bool active = 128 * half + 32 * quad < it.chunk.rows;  // some row of this warp exists
-            const int limit = valid ? limit_of<true>(p, it.chunk_no, it.chunk.len, row) : 0;
+            const int limit = valid ? limit_of(p, it.chunk, row) : 0;
             const int window0 = it.chunk.seen;
             float m = -INFINITY, l = 0.f, qs = 0.f;
             int unit = kNoUnit;  // the exponent that O is counted in
