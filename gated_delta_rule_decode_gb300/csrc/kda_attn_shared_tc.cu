@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
 #pragma unroll
                                 for (int pg = 0; pg < 2; ++pg)
                                     if (page[pg] >= 0)
-                                        tma_load_2d(sk + slot * C::kKeys + pg * C::kHalf, &keys, 0, page[pg] * kPage, &S.k_full[slot]);
+                                        tma_load_3d(sk + slot * C::kKeys + pg * C::kHalf, &keys, 0, 0, page[pg], &S.k_full[slot]);
                             }
                             __syncwarp();
                             continue;
@@ -748,12 +748,14 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
     if (tid == 0 && S.abort_flag && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_TIMEOUT);
 }
 
-// The keys as rows of d bytes, a page and kv head 64 of them.
+// The keys: rows of d bytes, 64 of a page and kv head, all of these (a row's number
+// can pass 32 bits).
 template <int HD>
 bool make_map(CUtensorMap *map, const AttnDecodeParams &p) {
-    const cuuint64_t dims[2] = {(cuuint64_t)HD, (cuuint64_t)(p.num_pages * p.Hkv * kPage)}, strides[1] = {(cuuint64_t)HD};
-    const cuuint32_t box[2] = {(cuuint32_t)HD, (cuuint32_t)kPage}, elem[2] = {1, 1};
-    return tensor_map_encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<unsigned char *>(p.k_pages), dims, strides, box, elem,
+    const cuuint64_t dims[3] = {(cuuint64_t)HD, (cuuint64_t)kPage, (cuuint64_t)(p.num_pages * p.Hkv)};
+    const cuuint64_t strides[2] = {(cuuint64_t)HD, (cuuint64_t)(HD * kPage)};
+    const cuuint32_t box[3] = {(cuuint32_t)HD, (cuuint32_t)kPage, 1}, elem[3] = {1, 1, 1};
+    return tensor_map_encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<unsigned char *>(p.k_pages), dims, strides, box, elem,
                                   CU_TENSOR_MAP_INTERLEAVE_NONE, HD == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

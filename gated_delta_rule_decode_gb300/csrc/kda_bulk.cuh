@@ -139,6 +139,15 @@ __device__ __forceinline__ void tma_load_2d(void *dst_smem, const void *map, int
         : "memory");
 }
 
+// The same of a 3-D map.
+__device__ __forceinline__ void tma_load_3d(void *dst_smem, const void *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst_smem)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
 // Shared -> global 2-D tensor store (box of the tensor map at (x, y)) in the
 // thread's bulk group.
 __device__ __forceinline__ void tma_store_2d(const void *map, int x, int y, const void *src_smem) {

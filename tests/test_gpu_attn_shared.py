@@ -251,3 +251,21 @@ def test_queries_of_all_sizes():
     rows = torch.zeros(3, 2, 10, dtype=torch.bool)
     rows[0, 1, 4] = rows[2, 0, 5] = True
     assert flag == 0 and torch.isnan(out[rows]).all() and torch.equal(out[~rows], good[~rows])
+
+
+@pytest.mark.parametrize("dtype,D,d", [(BF, 1, 128), (BF, 7, 128), (BF, 7, 64), (F32, 1, 64)])
+def test_queries_that_are_no_numbers_stay_in_their_rows(dtype, D, d):
+    g = gen(33)
+    case = _case(g, [(3, [500, 700, 260]), (0, [130])], 2, d)
+    q = randn(g, 4, D, 8, d).to(dtype)
+    want, want_lse, _ = _run(case, q)
+    odd = q.clone()
+    odd[0, 0, 1, 3] = float("nan")
+    odd[2, D - 1, 6, 0] = float("inf")
+    odd[3, 0, 0, d - 1] = float("-inf")
+    out, lse, flag = _run(case, odd)
+    assert flag == 0
+    rows = torch.zeros(4, D, 8, dtype=torch.bool, device="cuda")
+    rows[0, 0, 1] = rows[2, D - 1, 6] = rows[3, 0, 0] = True
+    assert out[rows].isnan().all()
+    assert torch.equal(out[~rows], want[~rows]) and torch.equal(lse[~rows], want_lse[~rows])
