@@ -13,14 +13,15 @@
 //
 //   task k is a block on tile k % 2:   ... PV(k), QK(k + 2), PV(k + 1), QK(k + 3) ...
 //
-//   warps 0-3, 4-7  softmax of tile 0 and 1: thread = row, a page's 64 scores in
-//                   registers, the weights go back over them as fp16; an item's
-//                   query rows and results
-//   warps 8, 9      products of tile 0 and 1
-//   warps 10, 11    look up pages, issue the copies of keys, of values (and prefetches
+//   warps 0-7, 8-15 softmax of tile 0 and 1: thread = row and page of the block, whose
+//                   weights go back over its scores as fp16.  The two threads of a row
+//                   tell each other their largest score, and keep the same maximum and
+//                   unit; an item's query rows and results
+//   warps 16, 17    products of tile 0 and 1
+//   warps 18, 19    look up pages, issue the copies of keys, of values (and prefetches
 //                   into L2 before them).  Every copy costs its warp 400 to 800 cycles
 //                   of waiting and issuing: one warp for both bounded a block (3500)
-//   warps 12-19     conversion of values
+//   warps 20-27     conversion of values
 //
 // The chunks are cut into workers' ranges by the plan (kda_attn_shared.cu); a
 // worker is one CTA on one SM.  Tensor memory: S of both tiles (P over them) and
@@ -42,13 +43,18 @@ namespace {
 
 using namespace dec;
 
-constexpr int kThreads = 640;
-constexpr int kMmaWarp = 8, kLoadWarp = 10;
-constexpr int kConvWarp = 12, kConvWarps = 8;
+constexpr int kThreads = 896;
+constexpr int kSoftWarps = 16;
+constexpr int kMmaWarp = 16, kLoadWarp = 18;
+constexpr int kConvWarp = 20, kConvWarps = 8;
 constexpr int kKeyBlocks = 4;  // in flight
-constexpr int kFetch = 16, kMetaRing = 64;  // page look-ups at a time, and kept
+// Page look-ups at a time, and kept: when one group is looked up, the softmax may be six blocks behind.
+constexpr int kFetch = 16, kMetaRing = 32;
+static_assert(kFetch + 2 * (kKeyBlocks + 2) <= kMetaRing, "no entry is overwritten before it is read");
 constexpr uint32_t kTmem = 512;
 constexpr float kLazy = 8.f;
+constexpr int kSoftRegs = 80, kOtherRegs = 56;
+static_assert(32 * kSoftWarps * kSoftRegs + (kThreads - 32 * kSoftWarps) * kOtherRegs <= kThreads * 72, "registers of a launched CTA");
 constexpr int kBias = 7;  // log2 of the weights' fp16 scale
 
 template <int HD>
@@ -73,8 +79,7 @@ struct Small {
     int abort_flag;
     volatile int v_nan;  // a NaN was set aside among the values that not every row sees
     int8_t q_exp[256];
-    float other_m[128], other_l[128];  // tile 1's, for the rows' results
-    int16_t other_unit[128];
+    float met[2][2][128];         // by tile, page and row: what the threads of a row tell each other
     PageMeta meta[kMetaRing];     // by the keys' warp
     int8_t v_there[kMetaRing];    // by the values' warp: the page is in the cache
 };
@@ -178,10 +183,10 @@ __device__ __forceinline__ void mma_e4m3_ss_warp(uint32_t d_tmem, uint64_t a_des
 
 // An item's query rows, scaled by powers of two to 2^7..2^8, as two e4m3 terms: of an element's 8 bits the first
 // holds 4 and the second what it leaves, exactly but for elements below 2^-9 of the row's largest, which are
-// rounded to 2^-17 of it.  256 threads, 8 channels each.
+// rounded to 2^-17 of it.  All softmax threads, 8 channels each.
 template <int HD>
 __device__ __forceinline__ void load_queries(const AttnDecodeParams &p, const Items &it, unsigned char *sq, int8_t *exps, int id) {
-    constexpr int PIECES = HD / 8, STEP = 256 / PIECES, HELD = 4;  // pieces of a row; rows of a pass; passes together
+    constexpr int PIECES = HD / 8, STEP = 32 * kSoftWarps / PIECES, HELD = 2;  // pieces of a row; rows of a pass; passes together
     const int piece = id % PIECES, rows = it.chunk.rows;
     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + (int64_t)it.chunk.tok0 * p.q_stride + (int64_t)it.head * p.G * HD + 8 * piece;
 #pragma unroll 1
@@ -275,12 +280,12 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
             mbar_init(&S.v_ready[i], kConvWarps);
             mbar_init(&S.v_free[i], 2);
             mbar_init(&S.s_full[i], 1);
-            mbar_init(&S.p_full[i], 4);
+            mbar_init(&S.p_full[i], kSoftWarps / 2);
             mbar_init(&S.drain[i], 1);
         }
-        mbar_init(&S.q_full, 8);
+        mbar_init(&S.q_full, kSoftWarps);
         mbar_init(&S.o_full, 2);
-        mbar_init(&S.o_free, 8);
+        mbar_init(&S.o_free, kSoftWarps);
         fence_barrier_init();
         S.abort_flag = 0;
         S.v_nan = 0;
@@ -300,9 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
     const uint32_t tm = S.tmem_base;
     constexpr int kO = 256;  // tensor memory column of tile 0's O; tile 1's 128 behind it; S at 0 and 128
 
-    // 96 registers a thread at launch: 256 x 128 + 384 x 72 <= 640 x 96
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // (72 registers a thread at launch)
+    if (warp >= kSoftWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kLoadWarp || warp == kLoadWarp + 1) {
             // ---------------- page look-ups and copies, of keys (a block at a time, swizzled rows that the products read as
             // they are) or of values (a page at a time, bytes that are converted)
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {  // 16 positions each; a page is one 128-byte-wide chunk of HD rows
                     constexpr uint64_t kChunk = HD * 128 >> 4, kStep = 32 >> 4;
-                    tc::mma_f16_ts_warp(to_o, to_s + 8 * ks, va + (ks >> 2) * kChunk + (ks & 3) * kStep, id_pv, ks == 0 ? begun : 1u);
+                    tc::mma_f16_ts_warp(to_o, to_s + 64 * (ks >> 2) + 8 * (ks & 3), va + (ks >> 2) * kChunk + (ks & 3) * kStep, id_pv, ks == 0 ? begun : 1u);
                 }
                 tc::commit_warp(&S.v_free[vb]);
                 if (p_narrow) tc::commit_warp(&S.v_free[vb]);
@@ -513,15 +518,22 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
-        // ---------------- softmax: thread = row
-        const int t = warp >> 2, quad = warp & 3, r = tid & 127;
-        const uint32_t s_addr = tc::lane_addr(tm, quad, 128 * t);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        // ---------------- softmax: thread = row and page of the block
+        const int t = warp >> 3, pg = (warp >> 2) & 1, quad = warp & 3, r = 32 * quad + lane;
+        const uint32_t s_addr = tc::lane_addr(tm, quad, 128 * t + 64 * pg);  // the page's scores, its weights over them
         const uint32_t o_addr = tc::lane_addr(tm, quad, kO + 128 * t);
-        auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); };
+        auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * t + quad) : "memory"); };  // a row's pages
+        auto quad_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(9 + quad) : "memory"); };         // and tiles
+        // The tiles take turns at the exponentials, in the order of the tasks: left to themselves both take them at once,
+        // and wait for the products at once.
+        auto my_turn = [&](int k) {
+            if (k > 0) asm volatile("bar.sync %0, %1;" ::"r"(13 + t), "n"(32 * kSoftWarps) : "memory");
+        };
+        auto other_turn = [&]() { asm volatile("bar.arrive %0, %1;" ::"r"(14 - t), "n"(32 * kSoftWarps) : "memory"); };
         bool ok = true;
         while (it.next(p)) {
-            // (after a wait gave up the loop runs on, on garbage: the two warps of a row meet at barriers)
+            // (after a wait gave up the loop runs on, on garbage: the warps of a row meet at barriers)
             // the query rows: the products of the item before are done (o_full)
             load_queries<HD>(p, it, sq, S.q_exp, tid);
             fence_proxy_async_smem();
@@ -533,63 +545,54 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
             const bool active = 128 * half + 32 * quad < it.chunk.rows;  // some row of this warp exists
             const int limit = valid ? limit_of(p, it.chunk, row) : 0;
             const int window0 = it.chunk.seen;
-            float m = -INFINITY, l = 0.f, qs = 0.f;
+            float m = -INFINITY, l = 0.f, qs = 0.f;  // l: of the thread's pages
             int unit = kNoUnit;  // the exponent that O is counted in
             bool first = true;
             for (int k = it.task0 + ((it.task0 ^ t) & 1); k < it.task0 + it.tasks; k += 2) {
                 if (!warp_wait(&S.s_full[t], k >> 1, abort_flag)) ok = false;
                 tc::fence_after_sync();
                 if (active) {
-                    const int b = (k - it.task0) >> (it.wide ? 1 : 0), page = it.page0 + 2 * b, pages = it.pages_of_block(b);
+                    const int b = (k - it.task0) >> (it.wide ? 1 : 0), page = it.page0 + 2 * b + pg, pages = it.pages_of_block(b);
                     // (rows that do not exist: scores of next to nothing)
                     if (first && valid) qs = __uint_as_float((uint32_t)(127 - 7 + S.q_exp[row]) << 23) * p.scale * kLog2e;
-                    float f[2];
-                    int vexp[2], end[2];
-                    bool has[2], masked = false;
-#pragma unroll
-                    for (int pg = 0; pg < 2; ++pg) {
-                        const PageMeta e = S.meta[(it.unit0 + 2 * b + pg) % kMetaRing];
-                        has[pg] = pg < pages && e.block >= 0;
-                        vexp[pg] = exponent_of(e.vs);
-                        f[pg] = has[pg] ? fmaxf(qs * e.ks, 1e-37f) : 1.f;  // positive, so that -inf stays -inf
-                        end[pg] = has[pg] ? limit - (page + pg) * kPage : 0;
-                        masked = masked || !has[pg] || (page + pg + 1) * kPage > window0;
-                    }
-                    float x[2][32];  // a page's scores: the second's are read for the maximum, and again for the weights
-                    auto scores = [&](int pg) {
-                        tc::ld32(s_addr + 64 * pg, x[0]);
-                        tc::ld32(s_addr + 64 * pg + 32, x[1]);
+                    const PageMeta e0 = S.meta[(it.unit0 + 2 * b + pg) % kMetaRing], e1 = S.meta[(it.unit0 + 2 * b + 1 - pg) % kMetaRing];
+                    const bool has = pg < pages && e0.block >= 0, other_has = 1 - pg < pages && e1.block >= 0;
+                    const int vexp = exponent_of(e0.vs);
+                    const float f = has ? fmaxf(qs * e0.ks, 1e-37f) : 1.f;  // positive, so that -inf stays -inf
+                    const int end = has ? limit - page * kPage : 0;
+                    const bool masked = !has || (page + 1) * kPage > window0;
+                    // (rolled loops: code that runs straight through is bound by its own fetching)
+                    float x[32];  // half of the page's scores: read for the maximum, and again for the weights
+                    auto scores = [&](int i) {
+                        tc::ld32(s_addr + 32 * i, x);
                         tc::wait_ld();
                         if (masked) {
                             asm volatile("" ::: "memory");  // (a branch, not predicates)
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                                for (int c = 0; c < 32; ++c)
-                                    if (32 * i + c >= end[pg]) x[i][c] = -INFINITY;
+                            for (int c = 0; c < 32; ++c)
+                                if (c >= end - 32 * i) x[c] = -INFINITY;
                         }
                     };
-                    float mx[2], raw[2];  // a page's largest score, and as it was read
+                    float best[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i) {
+                        scores(i);
 #pragma unroll
-                    for (int pg = 1; pg >= 0; --pg) {
-                        scores(pg);
-                        float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            best[c & 1] = max3(best[c & 1], x[0][2 * c], x[0][2 * c + 1]);
-                            best[2 + (c & 1)] = max3(best[2 + (c & 1)], x[1][2 * c], x[1][2 * c + 1]);
-                        }
-                        raw[pg] = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
-                        mx[pg] = __fmul_rn(raw[pg], f[pg]);  // (not to be fused with the differences below)
+                        for (int c = 0; c < 16; ++c) best[c & 1] = max3(best[c & 1], x[2 * c], x[2 * c + 1]);
                     }
-                    const float mnew = fmaxf(m, fmaxf(mx[0], mx[1])), before = m;
+                    const float raw = fmaxf(best[0], best[1]);
+                    const float mx = __fmul_rn(raw, f);  // (not to be fused with the differences below)
+                    // (the other thread has read what this one wrote a task ago: its weights came before these scores)
+                    S.met[t][pg][r] = mx;
+                    pair_sync();
+                    const float other = S.met[t][1 - pg][r];
+                    const float mnew = fmaxf(m, fmaxf(mx, other)), before = m;
                     const bool move = first || mnew - m > kLazy || (m == -INFINITY && mnew > m);
                     if (move) m = mnew;
                     const float use = m == -INFINITY ? 0.f : m;
                     int most = kNoUnit;  // the block's largest contribution
-#pragma unroll
-                    for (int pg = 0; pg < 2; ++pg)
-                        if (has[pg]) most = max(most, contribution(vexp[pg], mx[pg], use));
+                    if (has) most = contribution(vexp, mx, use);
+                    if (other_has) most = max(most, contribution(exponent_of(e1.vs), other, use));
                     int to = unit;
                     if (move) to += __float2int_ru(fmaxf(before - use, kFarBelow));
                     if (move || most > to + (int)kLazy) to = max(to, most);
@@ -600,10 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
                         fix = by.y;
                     }
                     unit = to;
-                    // (the last product of this tile came before these scores)
+                    // (the last product of this tile came before these scores); half of the channels each
                     if (__any_sync(~0u, !first && fix != 1.f)) {
 #pragma unroll 1
-                        for (int c = 0; c < HD; c += 16) {
+                        for (int c = pg * (HD / 2); c < (pg + 1) * (HD / 2); c += 16) {
                             float o[16];
                             tc::ld16(o_addr + c, o);
                             tc::wait_ld();
@@ -613,44 +616,44 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
                         }
                     }
                     first = false;
-#pragma unroll
-                    for (int pg = 0; pg < 2; ++pg) {
-                        if (pg == 1) scores(1);
-                        const int e = has[pg] ? kBias + vexp[pg] - unit : 0;
-                        const bool apart = e < kApart;  // these weights may vanish next to a larger value scale: their sum apart
-                        // scores are taken relative to the page's largest before they are scaled: however large they are,
-                        // that one's difference is 0
-                        const float top = raw[pg] == -INFINITY ? 0.f : -raw[pg], off = mx[pg] - use;
-                        const float unbias = pow2(-e);
-                        float own = 0.f;
-                        if (__any_sync(~0u, apart)) {  // (the whole warp: the stores below are the warp's)
+                    my_turn(k);
+                    const int e = has ? kBias + vexp - unit : 0;
+                    const bool apart = e < kApart;  // these weights may vanish next to a larger value scale: their sum apart
+                    // scores are taken relative to the page's largest before they are scaled: however large they are,
+                    // that one's difference is 0
+                    const float top = raw == -INFINITY ? 0.f : -raw, off = mx - use;
+                    float own = 0.f;
+                    const bool some_apart = __any_sync(~0u, apart);  // (the whole warp: the stores below are the warp's)
+                    const float z = off + (float)e;
+                    const float2 f2 = make_float2(f, f), z2 = make_float2(z, z), t2 = make_float2(top, top);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i) {
+                        scores(i);
+                        if (some_apart) {
                             asm volatile("" ::: "memory");
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                                for (int c = 0; c < 32; ++c) own += ex2(fmaf(x[i][c] + top, f[pg], off));
+                            for (int c = 0; c < 32; ++c) own += ex2(fmaf(x[c] + top, f, off));
                         }
                         __syncwarp();
-                        const float z = off + (float)e;
-                        const float2 f2 = make_float2(f[pg], f[pg]), z2 = make_float2(z, z), t2 = make_float2(top, top);
-                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        uint32_t pk[16];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) {
-                                float2 w = fma2(add2(make_float2(x[i][2 * c], x[i][2 * c + 1]), t2), f2, z2);
-                                w.x = ex2(w.x);
-                                w.y = ex2(w.y);
-                                sum[c & 1] = add2(sum[c & 1], w);
-                                pk[c] = pack_f16(w.x, w.y);
-                            }
-                            tc::st16u(s_addr + 32 * pg + 16 * i, pk);
+                        for (int c = 0; c < 16; ++c) {
+                            float2 w = fma2(add2(make_float2(x[2 * c], x[2 * c + 1]), t2), f2, z2);
+                            w.x = ex2(w.x);
+                            w.y = ex2(w.y);
+                            sum[c & 1] = add2(sum[c & 1], w);
+                            pk[c] = pack_f16(w.x, w.y);
                         }
-                        sum[0] = add2(sum[0], sum[1]);
-                        l += apart ? own : (sum[0].x + sum[0].y) * unbias;
+                        tc::st16u(s_addr + 16 * i, pk);
                     }
+                    other_turn();
+                    sum[0] = add2(sum[0], sum[1]);
+                    l += apart ? own : (sum[0].x + sum[0].y) * pow2(-e);
                     tc::wait_st();
+                } else {
+                    my_turn(k);
+                    other_turn();
                 }
                 tc::fence_before_sync();
                 __syncwarp();
@@ -665,30 +668,32 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
             const int64_t qrow = valid ? ((int64_t)it.chunk.tok0 + row / p.G) * p.Hq + it.head * p.G + row % p.G : 0;
             const bool rest = it.chunk_no >= plan.first_rest;
             float *out = whole ? (rest ? plan.rest_o : plan.prefix_o) + qrow * HD : part + plan.part_o + (slot * plan.rows + row) * HD;
-            float in[2] = {l == 0.f ? 0.f : pow2(unit) * (1.f / (float)(1 << kBias)), 0.f};  // of the tiles' O
-            bool writes = valid && ok;
-            if (!it.wide) {
-                // both tiles have the rows: tile 0's threads add up
-                if (t == 1) {
-                    S.other_m[r] = m;
-                    S.other_l[r] = l;
-                    S.other_unit[r] = (int16_t)unit;
-                }
-                pair_sync();
-                if (t == 0) {
-                    const float m1 = S.other_m[r], l1 = S.other_l[r];
-                    const float both = fmaxf(m, m1), use = both == -INFINITY ? 0.f : both;
-                    const float g0 = fmaxf(m - use, kFarBelow), g1 = fmaxf(m1 - use, kFarBelow);
-                    // (2^g in two steps: what it is multiplied with may be large)
-                    const float w0 = floorf(g0), w1 = floorf(g1), r0 = ex2(g0 - w0), r1 = ex2(g1 - w1);
-                    in[0] = l == 0.f ? 0.f : r0 * pow2((int)w0 + unit) * (1.f / (float)(1 << kBias));
-                    in[1] = l1 == 0.f ? 0.f : r1 * pow2((int)w1 + (int)S.other_unit[r]) * (1.f / (float)(1 << kBias));
-                    l = l * r0 * pow2((int)w0) + l1 * r1 * pow2((int)w1);
-                    m = both;
-                } else {
-                    writes = false;
-                }
+            // a row's sums: of both pages' threads, and in a narrow item of both tiles' (S.met once more: every product of
+            // the item is done, and so are the reads before them)
+            S.met[t][pg][r] = l;
+            pair_sync();
+            l += S.met[t][1 - pg][r];
+            float in[2] = {0.f, 0.f};  // of the tiles' O
+            if (it.wide) {
+                in[0] = l == 0.f ? 0.f : pow2(unit) * (1.f / (float)(1 << kBias));
+            } else {
+                quad_sync();
+                S.met[t][pg][r] = pg == 0 ? m : l;
+                quad_sync();
+                const float m0 = S.met[0][0][r], l0 = S.met[0][1][r], m1 = S.met[1][0][r], l1 = S.met[1][1][r];
+                quad_sync();
+                if (pg == 0) S.met[t][0][r] = __int_as_float(unit);
+                quad_sync();
+                m = fmaxf(m0, m1);
+                const float use = m == -INFINITY ? 0.f : m;
+                const float g0 = fmaxf(m0 - use, kFarBelow), g1 = fmaxf(m1 - use, kFarBelow);
+                // (2^g in two steps: what it is multiplied with may be large)
+                const float w0 = floorf(g0), w1 = floorf(g1), r0 = ex2(g0 - w0), r1 = ex2(g1 - w1);
+                in[0] = l0 == 0.f ? 0.f : r0 * pow2((int)w0 + __float_as_int(S.met[0][0][r])) * (1.f / (float)(1 << kBias));
+                in[1] = l1 == 0.f ? 0.f : r1 * pow2((int)w1 + __float_as_int(S.met[1][0][r])) * (1.f / (float)(1 << kBias));
+                l = l0 * r0 * pow2((int)w0) + l1 * r1 * pow2((int)w1);
             }
+            const bool writes = valid && ok && (it.wide || t == 0);
             const bool nan = S.v_nan != 0;
             if (active && (it.wide || t == 0)) {
                 float *row_out[4];  // of the quad's rows, this lane's columns
@@ -697,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
                 for (int k = 0; k < 4; ++k)
                     row_out[k] = reinterpret_cast<float *>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(out), (lane & 28) + k)) + 4 * (lane & 3);
 #pragma unroll 1
-                for (int c = 0; c < HD; c += 16) {
+                for (int c = pg * (HD / 2); c < (pg + 1) * (HD / 2); c += 16) {  // half of the channels each
                     float o[16];
                     tc::ld16(o_addr + c, o);
                     tc::wait_ld();
@@ -728,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
                         if ((row_writes >> k) & 1u) *reinterpret_cast<float4 *>(row_out[k] + c) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 }
             }
-            if (writes) {
+            if (writes && pg == 0) {
                 if (whole) {
                     (rest ? plan.rest_ml : plan.prefix_ml)[qrow] = make_float2(m, l);
                 } else {
