@@ -149,6 +149,12 @@ struct Items {
     __device__ __forceinline__ int pages_of_block(int b) const { return min(2, page1 - page0 - 2 * b); }
 };
 
+__device__ __forceinline__ void st8u(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {  // to nearest even
     uint16_t d;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
@@ -473,14 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
                     const unsigned char *src = ring + slot * C::kHalf + 16 * ct;
                     {
                         // 16 positions of a channel at a time: thread = channel ct / 4 + i ROWS
-                        constexpr int ROWS = 32, kTogether = HD / ROWS;
+                        constexpr int ROWS = 32, kTogether = 2;
                         const int r = ct >> 2, u = ct & 3;
                         unsigned char *dst = sv + buf * C::kOp + pg * HD * 128;
                         const uint32_t o0 = tc::sw128_off16(r, 16 * u, HD), o1 = tc::sw128_off16(r, 16 * u + 8, HD);
                         const bool have = there && S.v_there[(it.unit0 + 2 * b + pg) % kMetaRing] != 0;
                         const int pos0 = (it.page0 + 2 * b + pg) * kPage;
                         const bool tail = have && pos0 + kPage > window0;
-#pragma unroll
+#pragma unroll 1
                         for (int i0 = 0; i0 < HD / ROWS; i0 += kTogether) {
                             uint4 a[kTogether];
 #pragma unroll
@@ -562,23 +568,23 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
                     const int end = has ? limit - page * kPage : 0;
                     const bool masked = !has || (page + 1) * kPage > window0;
                     // (rolled loops: code that runs straight through is bound by its own fetching)
-                    float x[32];  // half of the page's scores: read for the maximum, and again for the weights
+                    float x[16];  // a quarter of the page's scores: read for the maximum, and again for the weights
                     auto scores = [&](int i) {
-                        tc::ld32(s_addr + 32 * i, x);
+                        tc::ld16(s_addr + 16 * i, x);
                         tc::wait_ld();
                         if (masked) {
                             asm volatile("" ::: "memory");  // (a branch, not predicates)
 #pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (c >= end - 32 * i) x[c] = -INFINITY;
+                            for (int c = 0; c < 16; ++c)
+                                if (c >= end - 16 * i) x[c] = -INFINITY;
                         }
                     };
                     float best[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int i = 0; i < 2; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         scores(i);
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) best[c & 1] = max3(best[c & 1], x[2 * c], x[2 * c + 1]);
+                        for (int c = 0; c < 8; ++c) best[c & 1] = max3(best[c & 1], x[2 * c], x[2 * c + 1]);
                     }
                     const float raw = fmaxf(best[0], best[1]);
                     const float mx = __fmul_rn(raw, f);  // (not to be fused with the differences below)
@@ -628,24 +634,24 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
                     const float2 f2 = make_float2(f, f), z2 = make_float2(z, z), t2 = make_float2(top, top);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-                    for (int i = 0; i < 2; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         scores(i);
                         if (some_apart) {
                             asm volatile("" ::: "memory");
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) own += ex2(fmaf(x[c] + top, f, off));
+                            for (int c = 0; c < 16; ++c) own += ex2(fmaf(x[c] + top, f, off));
                         }
                         __syncwarp();
-                        uint32_t pk[16];
+                        uint32_t pk[8];
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
+                        for (int c = 0; c < 8; ++c) {
                             float2 w = fma2(add2(make_float2(x[2 * c], x[2 * c + 1]), t2), f2, z2);
                             w.x = ex2(w.x);
                             w.y = ex2(w.y);
                             sum[c & 1] = add2(sum[c & 1], w);
                             pk[c] = pack_f16(w.x, w.y);
                         }
-                        tc::st16u(s_addr + 16 * i, pk);
+                        st8u(s_addr + 8 * i, pk);
                     }
                     other_turn();
                     sum[0] = add2(sum[0], sum[1]);
