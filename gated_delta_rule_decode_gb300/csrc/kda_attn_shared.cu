@@ -142,6 +142,31 @@ __device__ __forceinline__ int last_at_most(const int32_t *a, int n, int x) {
     return lo;
 }
 
+// What the threads before this one have of `mine`, and all together; by the whole block of 1024.
+template <typename T>
+__device__ __forceinline__ T scan(T mine, T *warp_sum, T &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T x = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    T sums = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T x = __shfl_up_sync(~0u, sums, o);
+        if (lane >= o) sums += x;
+    }
+    __syncthreads();  // (warp_sum is free again)
+    total = __shfl_sync(~0u, sums, 31);
+    const T before = __shfl_sync(~0u, sums, max(warp - 1, 0));
+    return (warp > 0 ? before : 0) + incl - mine;
+}
+static_assert(kPlanThreads == 1024, "a lane a warp");
+
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedParams p, const SharedLayout lay) {
     __shared__ int warp_sum[kPlanThreads / 32];
     __shared__ int sizes[kPlanCached];  // of the chunks: pages, and whether they are of more than 128 rows
@@ -162,21 +187,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
             const Group g = group_of(p, g0 + tid, true);
             if (g.pages > 0) mine = (g.count * D + lay.at[0].tokens - 1) / lay.at[0].tokens;
         }
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(~0u, incl, o);
-            if (lane >= o) incl += x;
-        }
-        if (lane == 31) warp_sum[warp] = incl;
-        __syncthreads();
-        int at = before + incl - mine;
-        for (int w = 0; w < kPlanThreads / 32; ++w) {
-            if (w < warp) at += warp_sum[w];
-            before += warp_sum[w];
-        }
+        int all;
+        const int at = before + scan(mine, warp_sum, all);
+        before += all;
         if (g0 + tid < p.groups) group_chunk[g0 + tid] = at;
-        __syncthreads();
     }
     const int used = (int)min((int64_t)before, lay.at[0].chunks);
 
@@ -206,8 +220,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
             if (c < kPlanCached) sizes[c] = size_of(out);
         }
     }
-    // the sequences, and the chunks of what follows their prefixes
-    for (int n = tid; n < p.call.batch; n += kPlanThreads) {
+    // the sequences, and the chunks of what follows their prefixes (from the last warps on: the first have the chunks above)
+    for (int n = kPlanThreads - 1 - tid; n < p.call.batch; n += kPlanThreads) {
         SeqPlan out{};
         const int len = capped_len(p.call, n), gi = last_at_most(p.group_start, p.groups, n);
         if (p.call.err_flag && p.call.seq_lens[n] > p.call.max_pages * kPage) atomicOr(p.call.err_flag, KDA_DEVERR_PAGE);
@@ -250,22 +264,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
     int64_t sum = 0;
     for (int c0 = 0; c0 < count; c0 += kPlanThreads) {
         const int64_t mine = c0 + tid < count ? (int64_t)item_cost(size(c0 + tid)) * Hkv : 0;
-        int64_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(~0u, incl, o);
-            if (lane >= o) incl += x;
-        }
-        if (lane == 31) warp_cost[warp] = incl;
-        __syncthreads();
-        int64_t at = sum + incl - mine;
-        for (int w = 0; w < kPlanThreads / 32; ++w) {
-            if (w < warp) at += warp_cost[w];
-            sum += warp_cost[w];
-        }
+        int64_t all;
+        const int64_t at = sum + scan(mine, warp_cost, all);
+        sum += all;
         if (c0 + tid < count) costs[c0 + tid] = at;  // before the chunk
-        __syncthreads();
     }
+    __syncthreads();
     // no more workers than have a block of their own (starts that differ), however the cuts are rounded
     const int W = (int)max((int64_t)1, min((int64_t)lay.workers, sum / (kItemCost + 4)));
     if (tid <= lay.workers) {
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
     __syncthreads();
     // the first and last worker of each item
     int2 *desc = reinterpret_cast<int2 *>(ws + lay.at[0].desc);  // (the rest's follow the prefixes')
-    for (int64_t i = tid; i < (int64_t)count * Hkv; i += kPlanThreads) {
+    for (uint32_t i = tid; i < (uint32_t)count * Hkv; i += kPlanThreads) {  // (query rows fit 31 bits)
         const int c = (int)(i / Hkv), h = (int)(i % Hkv), pages = size(c) >> 1;
         auto worker_of = [&](int page) {
             int lo = 0, hi = W;
