@@ -291,21 +291,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
         reinterpret_cast<int4 *>(ws + lay.starts)[tid] = start;
     }
     __syncthreads();
-    // the first and last worker of each item
-    int2 *desc = reinterpret_cast<int2 *>(ws + lay.at[0].desc);  // (the rest's follow the prefixes')
-    for (uint32_t i = tid; i < (uint32_t)count * Hkv; i += kPlanThreads) {  // (query rows fit 31 bits)
-        const int c = (int)(i / Hkv), h = (int)(i % Hkv), pages = size(c) >> 1;
-        auto worker_of = [&](int page) {
-            int lo = 0, hi = W;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                const int4 x = starts[mid];
-                if (x.x < c || (x.x == c && (x.y < h || (x.y == h && x.z <= page)))) lo = mid;
-                else hi = mid;
-            }
-            return lo;
-        };
-        desc[i] = pages > 0 ? make_int2(worker_of(0), worker_of(pages - 1)) : make_int2(0, -1);
+    // the first and last worker of each item, a thread each
+    int *desc = reinterpret_cast<int *>(ws + lay.at[0].desc);  // (the rest's follow the prefixes')
+    for (uint32_t i = tid >> 1; i < (uint32_t)count * Hkv; i += kPlanThreads / 2) {  // (query rows fit 31 bits)
+        const int c = (int)(i / Hkv), h = (int)(i % Hkv), pages = size(c) >> 1, page = tid & 1 ? pages - 1 : 0;
+        int lo = 0, hi = W;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            const int4 x = starts[mid];
+            if (x.x < c || (x.x == c && (x.y < h || (x.y == h && x.z <= page)))) lo = mid;
+            else hi = mid;
+        }
+        desc[2 * (int64_t)i + (tid & 1)] = pages > 0 ? lo : -(tid & 1);
     }
 }
 
