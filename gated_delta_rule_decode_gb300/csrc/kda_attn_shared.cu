@@ -33,9 +33,17 @@ struct SeqPlan {
 };
 
 // The tcgen05 workers' costs, in half blocks of 64 positions of up to 128 rows: a
-// page of a chunk of more rows is two, an item's start and end about kItemCost.
-constexpr int kItemCost = 6;
-constexpr int kFewRows = 16;       // of a kv head, up to which a sequence's rest is for the warps' kernel
+// page of a chunk of more rows is two, an item's start and end about kItemCost
+// (2, 6, 9, 12, 18: 40 sequences of 7 tokens in five groups, whose rests are short
+// items, 110, 70, 64, 64, 66 us; 64 of 8 tokens after one prefix 90, 85, 86, 88, 93).
+constexpr int kItemCost = 9;
+// On tcgen05 go prefixes of groups of more rows (of mean size, with all tokens
+// and heads of a kv head) than kFewShared, and sequences' rests of more rows than
+// kFewRows; the warps' kernel is quicker with few.  Prefixes of 32 pages and 64
+// sequences in groups of 4, 8, 16 and 32 rows: 149, 104, 81, 69 us there, 110, 85,
+// 83, 93 us with the warps' kernel.  Rests of 4 rows (32 sequences after 1600
+// pages) 121 us there, 104 with the warps' kernel; of 20 rows 106 and 257.
+constexpr int kFewShared = 8, kFewRows = 16;
 constexpr int kPlanCached = 2048;  // chunks whose costs fit the plan's shared memory
 
 // Where the parts of one of the two attentions are: an item's workers (first,
@@ -60,8 +68,9 @@ struct SharedLayout {
 SharedLayout shared_layout(int Hq, int Hkv, int d, int dtype, int64_t batch, int D, int64_t max_pages, int64_t groups) {
     const int G = Hq / Hkv;
     SharedLayout l{};
-    // on tcgen05: prefixes, and rests of more rows than a warp's tile (see lay_out)
-    l.tc[0] = dtype == KDA_DT_BF16 && d >= 64;
+    // the rows of a group of mean size
+    const int64_t mean = (batch + groups - 1) / std::max<int64_t>(groups, 1) * D * G;
+    l.tc[0] = dtype == KDA_DT_BF16 && d >= 64 && mean > kFewShared;
     l.tc[1] = l.tc[0] && D * G > kFewRows;
     l.workers = kSms;
     int64_t at = 0;
@@ -71,7 +80,6 @@ SharedLayout shared_layout(int Hq, int Hkv, int d, int dtype, int64_t batch, int
         return here;
     };
     // a chunk has the whole tokens that fit an item's rows: of a group of mean size, of a sequence
-    const int64_t mean = (batch + groups - 1) / std::max<int64_t>(groups, 1) * D * G;
     auto tokens = [&](int s, int64_t rows) {
         if (l.tc[s]) return kPartRows / G;
         return std::max(1, make_parts_layout(1, (int)std::min<int64_t>(rows, 4096), Hkv, d, dtype, max_pages).R / G);
