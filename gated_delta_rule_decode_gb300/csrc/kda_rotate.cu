@@ -15,6 +15,10 @@
 // integer product gives the turn's fraction to position * 2^-65, and only what
 // is left after taking out quarter turns becomes a float (2^-25 of at most an
 // eighth of a turn), whose sine and cosine are the first terms of their series.
+//
+// Measured: 16 384 tokens of 32 and 8 heads, d = 128, bf16, 60 us, 5.6 TB/s (82 %
+// of the copy's rate; the writes' share is half); 256 tokens 6.7 us, the launch
+// and one chain of reads.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -26,6 +30,9 @@
 namespace kda {
 namespace {
 
+// For 16 384 tokens of 40 heads: 1, 2, 4 rows a lane 59.8 (at 10 warps), 60.2, 113 us;
+// 16, 24, 32 warps an SM 66, 60, 96 (spills); 1, 2, 4, 8 tokens a barrier 61.6, 61.1,
+// 60.2, 62.2.
 constexpr int kMaxWarps = 6;     // of a block that hold rows
 constexpr int kRowsHeld = 2;     // rows of a lane
 constexpr int kWarpsPerSm = 24;  // by registers

@@ -23,12 +23,14 @@ def test_waits_give_up_and_the_context_stays_usable(variant, d):  # noqa: F811
     shared = torch.tensor([9, 4], dtype=torch.int32).cuda()
     index = torch.arange(15, dtype=torch.int32).expand(4, 2, 15).contiguous().cuda()
     flag = torch.zeros(1, dtype=torch.int32, device="cuda")
-    # 28 rows of a sequence and kv head: all on tcgen05, whose roles wait for one another; 4: the rests by warps
-    # that wait for copies which may have landed; fp32: all of it so
-    for D, dtype, flags in ((7, torch.bfloat16, (kda.KDA_DEVERR_TIMEOUT,)), (1, torch.bfloat16, (kda.KDA_DEVERR_TIMEOUT,)),
-                            (2, torch.float32, (0, kda.KDA_DEVERR_TIMEOUT))):
+    one, all4 = torch.tensor([0, 4], dtype=torch.int32).cuda(), torch.tensor([4], dtype=torch.int32).cuda()
+    gave_up, either = (kda.KDA_DEVERR_TIMEOUT,), (0, kda.KDA_DEVERR_TIMEOUT)
+    # 28 rows of a sequence and kv head: all on tcgen05, whose roles wait for one another; 4 rows, prefixes of groups
+    # of 8, fp32: by warps that wait for copies which may have landed; a group of 16 rows: its prefix on tcgen05
+    for D, dtype, groups, flags in ((7, torch.bfloat16, (start, shared), gave_up), (1, torch.bfloat16, (start, shared), either),
+                                    (2, torch.float32, (start, shared), either), (1, torch.bfloat16, (one, all4), gave_up)):
         q = randn(g, 4, D, 8, d).to(dtype).cuda()
-        call = lambda: attn.decode_shared(q, cache, lens, table, start, shared, return_lse=True, err_flag=flag)  # noqa: E731,B023
+        call = lambda: attn.decode_shared(q, cache, lens, table, *groups, return_lse=True, err_flag=flag)  # noqa: E731,B023
         flag.zero_()
         want = call()
         assert flag.item() == 0

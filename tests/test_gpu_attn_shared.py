@@ -269,3 +269,51 @@ def test_queries_that_are_no_numbers_stay_in_their_rows(dtype, D, d):
     rows[0, 0, 1] = rows[2, D - 1, 6] = rows[3, 0, 0] = True
     assert out[rows].isnan().all()
     assert torch.equal(out[~rows], want[~rows]) and torch.equal(lse[~rows], want_lse[~rows])
+
+
+def _serve_step(a, c, table, held, rot, w, row, cu, one, start, shared):
+    """A token of each sequence: norm and rotation, into the cache, attention; (q, lengths, out, lse)."""
+    q, k, v = row[:, :8], row[:, 8:10], row[:, 10:]
+    q, k = a.norm_rotate(q, k, held, rot, q_weight=w, k_weight=w)
+    a.append(c, k, v, cu, held, table)
+    now = held + one
+    return (q, now) + a.decode_shared(q[:, None], c, now, table, start, shared, return_lse=True)
+
+
+def test_a_course_with_a_system_prompt():
+    """A prefix goes into the cache once; three sequences of a group and one by itself go on from there."""
+    a, g = _attn(), gen(51)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    c = a.alloc_cache(40, 2, 128)
+    pages = torch.randperm(40, generator=g).int()
+    table = torch.stack([torch.cat([pages[:4], pages[4 + 3 * n:7 + 3 * n]]) for n in range(3)] + [pages[20:27]]).cuda()
+    rot, w = a.rotary(a.rotary_frequencies(128)), (1 + 0.1 * randn(g, 128)).cuda()
+    start, shared = i32([0, 3, 4]), i32([4, 0])
+    # the prefix, through the first sequence's row, and the other sequence's prompt
+    row = randn(g, 256 + 70, 12, 128).bfloat16().cuda()
+    pos = torch.cat([torch.arange(256), torch.arange(70)]).int().cuda()
+    _, k = a.norm_rotate(row[:, :8], row[:, 8:10], pos, rot, q_weight=w, k_weight=w)
+    a.append(c, k, row[:, 10:], i32([0, 256, 326]), i32([0, 0]), table[[0, 3]].contiguous())
+    # what the sequences of the group ask, behind the prefix
+    row = randn(g, 100 + 1 + 64, 12, 128).bfloat16().cuda()
+    pos = torch.cat([256 + torch.arange(n) for n in (100, 1, 64)]).int().cuda()
+    _, k = a.norm_rotate(row[:, :8], row[:, 8:10], pos, rot, q_weight=w, k_weight=w)
+    a.append(c, k, row[:, 10:], i32([0, 100, 101, 165]), i32([256] * 3), table[:3].contiguous())
+    held, one, cu = i32([356, 257, 320, 70]), i32([1] * 4), i32([0, 1, 2, 3, 4])
+    row = randn(g, 4, 12, 128).bfloat16().cuda()
+    saved = [x.clone() for x in c]
+    q, now, out, lse = _serve_step(a, c, table, held, rot, w, row, cu, one, start, shared)
+    kp, vp = (x.view(torch.uint8).cpu() for x in (c.k_pages, c.v_pages))
+    case = ((kp, vp, c.k_scale.cpu(), c.v_scale.cpu()), now.cpu(), table.cpu(), None, None)
+    want, want_lse, tol, tol_lse = _want(case, q[:, None], BF)
+    check(out, want, tol, "out")
+    check(lse, want_lse, tol_lse, "lse")
+    # the same step captured, replayed from the same state
+    for x, y in zip(c, saved):
+        x.view(torch.uint8).copy_(y.view(torch.uint8)) if x.element_size() == 1 else x.copy_(y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _serve_step(a, c, table, held, rot, w, row, cu, one, start, shared)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[2], out) and torch.equal(got[3], lse)
