@@ -204,7 +204,8 @@ KDA_API int kda_norm_rotate(const kda_attn_dims *dims, int64_t total_tokens, con
  * are read from the row of the group's first sequence, once for all of them.
  * The results are those of kda_attn_decode (the shared pages are full; a
  * sequence that ends inside them sees them as far as it goes).  Sequences of
- * no group share nothing.
+ * no group share nothing.  Kernels are chosen by batch / num_groups, the mean
+ * size of a group: many empty groups cost time, not results.
  *
  *   group_start  i32 [num_groups + 1], not decreasing, in 0..batch; offsets
  *                that are not set KDA_DEVERR_SEQLENS, and the outputs of the
