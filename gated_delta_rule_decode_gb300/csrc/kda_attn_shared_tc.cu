@@ -3,7 +3,8 @@
 //
 // The formulas and the counting of outputs are those of kda_attn_decode_tc.cu
 // (value scales in the exponents of fp16 weights, values turned into fp16).  Keys
-// are multiplied as the bytes that they are, with queries as two e4m3 terms: they
+// are multiplied as the bytes that they are, with queries as an e4m3 and an e5m2
+// term (and what these leave in fp32, where it counts: see load_queries): they
 // need no conversion and half the room, so that four blocks are in flight.  And
 // two tiles of 128 rows are.  A chunk of more than 128 rows is two tiles, and a block of 128
 // positions is read, turned into fp16 and used for both.  A chunk of up to 128
@@ -67,6 +68,9 @@ constexpr float kLazy = 8.f;
 constexpr int kSoftRegs = 80, kOtherRegs = 56;
 static_assert(32 * kSoftWarps * kSoftRegs + (kThreads - 32 * kSoftWarps) * kOtherRegs <= kThreads * 72, "registers of a launched CTA");
 constexpr int kBias = 7;  // log2 of the weights' fp16 scale
+// What the queries' two terms may leave out of a score (base 2) before it is added in fp32.  A weight is rounded
+// by 2^-11 next to it.  Rows of normal elements leave less than this until their scores reach thousands.
+constexpr float kLeftOut = 0x1p-14f;
 
 template <int HD>
 struct Cfg {
@@ -90,6 +94,7 @@ struct Small {
     int abort_flag;
     volatile int v_nan;  // a NaN was set aside among the values that not every row sees
     int8_t q_exp[256];
+    float q_left[2][4];  // of items in turn and groups of 64 rows: the sum of |what two terms leave|
     float met[2][2][128];         // by tile, page and row: what the threads of a row tell each other
     PageMeta meta[kMetaRing];     // by the keys' warp
     int8_t v_there[kMetaRing];    // by the values' warp: the page is in the cache
@@ -189,8 +194,14 @@ __device__ __forceinline__ uint64_t desc_keys(uint32_t saddr) {
            (C::kSwizzle << 61);
 }
 
-// kind::f8f6f4 with e4m3 operands and fp32 accumulation; a step is 32 channels.
-__device__ __forceinline__ void mma_e4m3_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {  // to nearest even
+    uint16_t d;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// kind::f8f6f4 with 8-bit operands and fp32 accumulation; a step is 32 channels.
+__device__ __forceinline__ void mma_f8_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
@@ -198,11 +209,33 @@ __device__ __forceinline__ void mma_e4m3_ss_warp(uint32_t d_tmem, uint64_t a_des
         : "memory");
 }
 
-// An item's query rows, scaled by powers of two to 2^7..2^8, as two e4m3 terms: of an element's 8 bits the first
-// holds 4 and the second what it leaves, exactly but for elements below 2^-9 of the row's largest, which are
-// rounded to 2^-17 of it.  All softmax threads, 8 channels each.
+// Pairs of a query's elements, scaled (see load_queries): their first term, of e4m3, their second, of e5m2, and what
+// the two leave.
+struct Terms {
+    uint32_t first, second;
+    float2 left;
+};
+__device__ __forceinline__ Terms terms_of(float x0, float x1) {
+    Terms t;
+    // (an infinite query makes its row NaN, as its scores would)
+    t.first = to_e4m3x2(x0 - x0 == 0.f ? x0 : NAN, x1 - x1 == 0.f ? x1 : NAN);
+    uint32_t u, unused;
+    e4m3x4_to_f16(t.first, u, unused);
+    const float2 first = unpack_f16(u);
+    t.second = to_e5m2x2(x0 - first.x, x1 - first.y);
+    const float2 second = unpack_f16((t.second & 0xffu) << 8 | (t.second & 0xff00u) << 16);  // (e5m2 is fp16's upper byte)
+    t.left = make_float2((x0 - first.x) - second.x, (x1 - first.y) - second.y);
+    return t;
+}
+__device__ __forceinline__ float row_scale(int ex) { return __uint_as_float((uint32_t)(127 + 7 - ex) << 23); }
+
+// An item's query rows, scaled by powers of two to 2^7..2^8, as an e4m3 and an e5m2 term.  Of an element's 8 bits the
+// first holds 4 and leaves at most half of the last of these: 3 bits, which the second holds exactly down to elements
+// of 2^-6, 2^-13 of the row's largest.  Of those below it leaves up to 2^-14, 2^-21 of the largest, and the softmax
+// adds that in fp32 where it may count (add_left).  All softmax threads, 8 channels each.
 template <int HD>
-__device__ __forceinline__ void load_queries(const AttnDecodeParams &p, const Items &it, unsigned char *sq, int8_t *exps, int id) {
+__device__ __forceinline__ void load_queries(const AttnDecodeParams &p, const Items &it, unsigned char *sq, int8_t *exps, float *lefts,
+                                             int id) {
     constexpr int PIECES = HD / 8, STEP = 32 * kSoftWarps / PIECES, HELD = 2;  // pieces of a row; rows of a pass; passes together
     const int piece = id % PIECES, rows = it.chunk.rows;
     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + (int64_t)it.chunk.tok0 * p.q_stride + (int64_t)it.head * p.G * HD + 8 * piece;
@@ -219,34 +252,94 @@ __device__ __forceinline__ void load_queries(const AttnDecodeParams &p, const It
         for (int i = 0; i < HELD; ++i) {
             const int row = r0 + i * STEP + id / PIECES;
             const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-            float amax = 0.f;
+            float amax = 0.f, amin = INFINITY;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+            for (int e = 0; e < 4; ++e) {
+                const float x0 = fabsf(__uint_as_float(w[e] << 16)), x1 = fabsf(__uint_as_float(w[e] & 0xffff0000u));
+                amax = fmaxf(amax, fmaxf(x0, x1));
+                amin = fminf(amin, fminf(x0, x1));
+            }
 #pragma unroll
             for (int o = 1; o < PIECES; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-            if (row < rows) {
-                int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-                ex = ex < -100 ? -100 : ex > 126 ? 126 : ex;
-                const float mul = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
-                if (piece == 0) exps[row] = (int8_t)ex;
-                uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+            int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+            ex = ex < -100 ? -100 : ex > 126 ? 126 : ex;
+            const float mul = row_scale(ex);
+            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Terms t = terms_of(__uint_as_float(w[e] << 16) * mul, __uint_as_float(w[e] & 0xffff0000u) * mul);
+                hi[e >> 1] |= t.first << (16 * (e & 1));
+                lo[e >> 1] |= t.second << (16 * (e & 1));
+            }
+            if (row < rows && amin * mul < 0x1p-6f) {  // (two of a thousand lanes, of normal elements)
+                float left = 0.f;
+                uint4 v = raw[i];
+#pragma unroll 1
                 for (int e = 0; e < 4; ++e) {
-                    const float x0 = __uint_as_float(w[e] << 16) * mul, x1 = __uint_as_float(w[e] & 0xffff0000u) * mul;
-                    // (an infinite query makes its row NaN, as its scores would)
-                    const uint32_t h = to_e4m3x2(x0 - x0 == 0.f ? x0 : NAN, x1 - x1 == 0.f ? x1 : NAN);
-                    uint32_t u, unused;
-                    e4m3x4_to_f16(h, u, unused);
-                    const float2 first = unpack_f16(u);
-                    hi[e >> 1] |= h << (16 * (e & 1));
-                    lo[e >> 1] |= to_e4m3x2(x0 - first.x, x1 - first.y) << (16 * (e & 1));
+                    const float2 x = terms_of(__uint_as_float(v.x << 16) * mul, __uint_as_float(v.x & 0xffff0000u) * mul).left;
+                    left += fabsf(x.x) + fabsf(x.y);
+                    v.x = v.y; v.y = v.z; v.z = v.w;
                 }
+                if (left > 0.f) atomicAdd(&lefts[row >> 6], left * __uint_as_float((uint32_t)(127 - 7 + ex) << 23));
+            }
+            if (row < rows) {
+                if (piece == 0) exps[row] = (int8_t)ex;
                 // 8 bytes of the row, in its swizzled units of 16
                 unsigned char *dst = sq + (row >> 7) * 2 * Cfg<HD>::kKeys + key_off<HD>(row & 127, 8 * piece);
                 *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
                 *reinterpret_cast<uint2 *>(dst + Cfg<HD>::kKeys) = make_uint2(lo[0], lo[1]);
             }
+        }
+    }
+}
+
+// Adds what the terms of the thread's row (-1: none) leave of its scores to the 64 of a page (if it is in the cache), in
+// tensor memory at s_addr.  By whole warps, in those rows alone where it may be more than kLeftOut: a row's result does
+// not depend on others.  A call, and little code rather than quick code: the rows that come here are rare, and inlined
+// it cost the others 6 us of a document's 104 (as it is, 2: the check).
+template <int HD>
+__device__ __noinline__ void add_left(const AttnDecodeParams &p, const Items &it, uint32_t s_addr, int row, const PageMeta *at,
+                                      const int8_t *exps) {
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q);
+    const PageMeta page = *at;
+    if (page.block < 0) return;
+    float mul = 0.f, bound = 0.f;
+    if (row >= 0) {
+        q += ((int64_t)it.chunk.tok0 + row / p.G) * p.q_stride + (int64_t)(it.head * p.G + row % p.G) * HD;
+        mul = row_scale(exps[row]);
+        bound = kLeftOut * mul / (p.scale * kLog2e * page.ks * 448.f);
+    }
+    auto left_of = [&](int c) {
+        const uint32_t w = row >= 0 ? *reinterpret_cast<const uint32_t *>(q + c) : 0u;
+        return terms_of(__uint_as_float(w << 16) * mul, __uint_as_float(w & 0xffff0000u) * mul).left;
+    };
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < HD; c += 2) {
+        const float2 x = left_of(c);
+        sum += fabsf(x.x) + fabsf(x.y);
+    }
+    if (!(sum > bound)) row = -1;  // (NaN: its scores are NaN already)
+    __syncwarp();
+#pragma unroll 1
+    for (int c = 0; c < HD; c += 2) {
+        const float2 x = left_of(c);
+        if (!__any_sync(~0u, x.x != 0.f || x.y != 0.f)) continue;
+        const unsigned char *key = p.k_pages + (int64_t)page.block * Cfg<HD>::kHalf + c;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i, key += 16 * HD) {
+            float s[16];
+            tc::ld16(s_addr + 16 * i, s);
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                uint32_t u, unused;
+                e4m3x4_to_f16(*reinterpret_cast<const uint16_t *>(key + e * HD), u, unused);
+                const float2 k = unpack_f16(u);
+                s[e] = fmaf(x.x, k.x, fmaf(x.y, k.y, s[e]));
+            }
+            tc::st16(s_addr + 16 * i, s);
+            tc::wait_st();
         }
     }
 }
@@ -304,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
         mbar_init(&S.o_full, 2);
         mbar_init(&S.o_free, kSoftWarps);
         fence_barrier_init();
+        for (int i = 0; i < 8; ++i) S.q_left[i >> 2][i & 3] = 0;
         S.abort_flag = 0;
         S.v_nan = 0;
     }
@@ -406,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
             // was the tile's too, and between items all meet (q_full).  What frees a block counts two: one of a narrow
             // item is freed twice by its tile's warp.
             const uint32_t id_qk = tc::idesc_f16(128, 128), id_pv = tc::idesc_f16(128, HD);  // (e4m3 has fp16's code, 0)
+            constexpr uint32_t kE5m2 = 1u << 7;  // of the first operand
             const int t = warp - kMmaWarp;
             const uint32_t to_s = tm + 128 * t, to_o = tm + kO + 128 * t;
             int block0 = 0;  // blocks before the item
@@ -457,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
                     for (int ks = 0; ks < HD / 16; ++ks) {
                         constexpr int STEPS = HD / 32;  // of a term
                         const uint64_t step = (ks % STEPS) * (32 >> 4);
-                        mma_e4m3_ss_warp(to_s, qa + (ks / STEPS) * (C::kKeys >> 4) + step, ka + step, id_qk, ks > 0);
+                        mma_f8_ss_warp(to_s, qa + (ks / STEPS) * (C::kKeys >> 4) + step, ka + step, ks < STEPS ? id_qk : id_qk | kE5m2, ks > 0);
                     }
                     tc::commit_warp(&S.s_full[t]);
                     tc::commit_warp(&S.k_free[kb]);
@@ -552,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
         while (it.next(p)) {
             // (after a wait gave up the loop runs on, on garbage: the warps of a row meet at barriers)
             // the query rows: the products of the item before are done (o_full)
-            load_queries<HD>(p, it, sq, S.q_exp, tid);
+            load_queries<HD>(p, it, sq, S.q_exp, S.q_left[it.item & 1], tid);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.q_full);
@@ -564,15 +659,27 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
             const int window0 = it.chunk.seen;
             float m = -INFINITY, l = 0.f, qs = 0.f;  // l: of the thread's pages
             int unit = kNoUnit;  // the exponent that O is counted in
+            float left = 0.f;  // twice what the queries' terms may leave of a score, by the page's key scale
             bool first = true;
             for (int k = it.task0 + ((it.task0 ^ t) & 1); k < it.task0 + it.tasks; k += 2) {
                 if (!warp_wait(&S.s_full[t], k >> 1, abort_flag)) ok = false;
                 tc::fence_after_sync();
                 if (active) {
                     const int b = (k - it.task0) >> (it.wide ? 1 : 0), page = it.page0 + 2 * b + pg, pages = it.pages_of_block(b);
-                    // (rows that do not exist: scores of next to nothing)
-                    if (first && valid) qs = __uint_as_float((uint32_t)(127 - 7 + S.q_exp[row]) << 23) * p.scale * kLog2e;
-                    const PageMeta e0 = S.meta[(it.unit0 + 2 * b + pg) % kMetaRing], e1 = S.meta[(it.unit0 + 2 * b + 1 - pg) % kMetaRing];
+                    if (first) {
+                        // (the sum of a group of rows, its order left open, so half of the bound: add_left looks at the row's own)
+                        if (valid) qs = __uint_as_float((uint32_t)(127 - 7 + S.q_exp[row]) << 23) * p.scale * kLog2e;  // (rows that do not exist: scores of next to nothing)
+                        left = S.q_left[it.item & 1][(128 * half + 32 * quad) >> 6] * (2.f * 448.f * kLog2e) * p.scale;
+                    }
+                    const int meta0 = (it.unit0 + 2 * b + pg) % kMetaRing;
+                    // (a page that a wait which gave up has left unknown is not read)
+                    if (__any_sync(~0u, S.meta[meta0].ks * left > kLeftOut && pg < pages && ok)) {
+                        int mine = row;
+                        asm volatile("" : "+r"(mine)::"memory");  // (nothing of the call is kept in registers beside it)
+                        add_left<HD>(p, it, s_addr, mine < it.chunk.rows ? mine : -1, &S.meta[meta0], S.q_exp);
+                        asm volatile("" ::: "memory");
+                    }
+                    const PageMeta e0 = S.meta[meta0], e1 = S.meta[(it.unit0 + 2 * b + 1 - pg) % kMetaRing];
                     const bool has = pg < pages && e0.block >= 0, other_has = 1 - pg < pages && e1.block >= 0;
                     const int vexp = exponent_of(e0.vs);
                     const float f = has ? fmaxf(qs * e0.ks, 1e-37f) : 1.f;  // positive, so that -inf stays -inf
@@ -680,6 +787,8 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
             // ---------------- the item's end
             if (!warp_wait(&S.o_full, it.item, abort_flag)) ok = false;
             tc::fence_after_sync();
+            // (every warp has read them; they are written again for the item after the next, once this warp is in that one)
+            if (tid < 4) S.q_left[it.item & 1][tid] = 0;
             const bool whole = it.page0 == 0 && it.page1 == it.pages;
             const int64_t slot = 2 * (int64_t)blockIdx.x + (it.page0 == 0 ? 1 : 0);
             const int64_t qrow = valid ? ((int64_t)it.chunk.tok0 + row / p.G) * p.Hq + it.head * p.G + row % p.G : 0;

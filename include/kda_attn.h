@@ -203,7 +203,10 @@ KDA_API int kda_norm_rotate(const kda_attn_dims *dims, int64_t total_tokens, con
  * shared_pages[g] entries of their block table rows name the same pages, which
  * are read from the row of the group's first sequence, once for all of them.
  * The results are those of kda_attn_decode (the shared pages are full; a
- * sequence that ends inside them sees them as far as it goes).  Sequences of
+ * sequence that ends inside them sees them as far as it goes).  In bf16, where
+ * many rows meet a page, queries are multiplied as two 8-bit terms, and what
+ * these leave is added where it could come to more than 2^-14 of a score (in
+ * units of log 2): the weights' own rounding is 2^-11.  Sequences of
  * no group share nothing.  Kernels are chosen by batch / num_groups, the mean
  * size of a group: many empty groups cost time, not results.
  *
