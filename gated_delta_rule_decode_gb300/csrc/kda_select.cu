@@ -8,9 +8,11 @@
 //
 // about the most that a key of the page can give the row.  Sums of 128 products
 // of whole numbers stay below 2^24, so every order of adding gives the same
-// bits, and a selection is a matter of the inputs alone.
+// bits, and a selection is a matter of the inputs alone: of units of any size too,
+// since scores are compared without leaving whole numbers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include "kda_attn_decode.cuh"
@@ -153,9 +155,14 @@ struct ScoreSmem {
     static int bytes(int rows) { return kScoreWarps * kTile + (rows < kScoreRows ? rows : kScoreRows) * 2 * HD; }
 };
 
-__device__ __forceinline__ uint32_t ordered(float x) {
-    const uint32_t b = __float_as_uint(x == 0.f ? 0.f : x);  // -0 as 0
-    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+// Scores as whole numbers of the same order.  A sum of 128 products is below 2^21, so as fp32 it has 20 bits behind
+// the first and 3 that are 0; what its row's and its page's units add to the exponent, up to 2^248 and 2^252, would leave
+// fp32's range, and is added where those 3 bits make room for it.
+constexpr int kScoreBits = 20;  // of a score's fraction
+__device__ __forceinline__ int unit_step(int e) { return (e + 126) << kScoreBits; }  // of a unit 2^e, e = -126..126
+__device__ __forceinline__ int score_of(int sum, int step) {
+    const int mag = (int)(__float_as_uint(fabsf((float)sum)) >> (23 - kScoreBits)) + step;
+    return sum > 0 ? mag : sum < 0 ? -mag : 0;
 }
 
 // Four neighbouring elements.
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const CacheSele
     using S = ScoreSmem<HD>;
     constexpr int W = HD / 4;  // words of a bound, and of a row's part
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float x_unit[kScoreRows];
+    __shared__ int x_step[kScoreRows];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int item = (int)(blockIdx.x / (unsigned)splits), split = (int)(blockIdx.x % (unsigned)splits);
     const int n = item / p.Hkv, h = item % p.Hkv;
@@ -257,7 +264,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const CacheSele
                 xs[r * 2 * W + lane] = up;
                 xs[r * 2 * W + W + lane] = down;
             }
-            if (lane == 0) x_unit[r] = exp2i(e);
+            if (lane == 0) x_step[r] = unit_step(e);
         }
         __syncthreads();
         for (int page = first; page < P; page += step) {
@@ -275,7 +282,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const CacheSele
             if (page + step < P) copy(next);
             const float next_unit = unit_of(next);
             const int after = id_of(page + 2 * step + lane, r0 == 0);
-            float best = -INFINITY;
+            int best = INT_MIN;
 #pragma unroll 1
             for (int r = 0; r < here; ++r) {
                 int sum[4] = {0, 0, 0, 0};
@@ -289,12 +296,13 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const CacheSele
                         sum[2] = __dp4a((int)u.z, (int)b[i][j + 2], sum[2]);
                         sum[3] = __dp4a((int)u.w, (int)b[i][j + 3], sum[3]);
                     }
-                best = fmaxf(best, (float)((sum[0] + sum[1]) + (sum[2] + sum[3])) * x_unit[r]);
+                best = max(best, score_of((sum[0] + sum[1]) + (sum[2] + sum[3]), x_step[r]));
             }
             if (page + lane < P) {
                 const bool good = now >= 0 && power_of_two(unit);
                 if (now >= 0 && !good && r0 == 0 && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_SCALE);
-                uint32_t key = ordered(good ? best * unit : -INFINITY);
+                const int step = good ? unit_step((int)(__float_as_uint(unit) >> 23) - 127) : 0;
+                uint32_t key = good ? 0x80000000u + (uint32_t)(best + (best > 0 ? step : best < 0 ? -step : 0)) : 0;
                 if (r0 > 0) key = max(key, keys[page + lane]);
                 keys[page + lane] = key;
             }
