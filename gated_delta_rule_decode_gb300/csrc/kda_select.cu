@@ -351,8 +351,13 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const CacheSelec
     }
     if (P <= p.budget) {
         for (int i = tid; i < p.budget; i += kSelectThreads) {
-            p.block_table_out[to + i] = i < P ? table[i] : -1;
+            const int id = i < P ? table[i] : -1;
+            p.block_table_out[to + i] = id;
             p.index_out[to + i] = i < P ? i : -1;
+            if (i < P && p.err_flag) {  // (no scores, but errors as with them)
+                if (id < 0 || id >= p.num_pages) atomicOr(p.err_flag, KDA_DEVERR_PAGE);
+                else if (!power_of_two(p.unit[(int64_t)id * p.Hkv + item % p.Hkv])) atomicOr(p.err_flag, KDA_DEVERR_SCALE);
+            }
         }
         return;
     }

@@ -1,9 +1,9 @@
-"""Page selection: windows of many rows, scores of any size."""
+"""Page selection: windows of many rows, scores of any size, errors whatever the budget."""
 import pytest
 import torch
 
 from attn_testutil import gen, randn
-from test_gpu_select import BF, F32, _i32, _random_summary, _selects
+from test_gpu_select import BF, F32, _attn, _i32, _random_summary, _selects
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,25 @@ def test_rows_of_units_far_apart():
     q[0, 0, 2, 4:] = 2.0 ** -120 * torch.rand(28, generator=g)
     for dtype in (BF, F32):
         _selects(q.to(dtype), b, u, _i32([70 * 64]), torch.arange(70, dtype=torch.int32)[None], 9, 0, 1)
+
+
+@pytest.mark.parametrize("width", [6, 30])
+def test_errors_of_sequences_that_keep_all_their_pages(width):
+    """Entries outside the cache and units that are no powers of two are flagged for them as for others."""
+    g, a = gen(8), _attn()
+    b, u = _random_summary(g, 20, 2, 32)
+    q = randn(g, 2, 1, 4, 32)
+    base = torch.full((2, width), -1, dtype=torch.int32)
+    base[:, :4] = torch.arange(8, dtype=torch.int32).view(2, 4)
+    lens = _i32([4 * 64 - 3, 4 * 64])
+    _selects(q, b, u, lens, base, 8, 1, 2)  # (entries past the last page are not looked at)
+    for bad in (-1, 20, 1 << 30):
+        table = base.clone()
+        table[1, 2] = bad
+        _selects(q, b, u, lens, table, 8, 1, 2, a.KDA_DEVERR_PAGE)
+    for bad in (3.0, 0.0, float("nan"), -1.0, 2.0 ** 127):
+        odd = u.clone()
+        odd[5, 1] = bad
+        _selects(q, b, odd, lens, base, 8, 1, 2, a.KDA_DEVERR_SCALE)
+        odd[5, 1], odd[9, 0] = u[5, 1], bad  # of a page that no row names
+        _selects(q, b, odd, lens, base, 8, 1, 2)
