@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
     }
     const int used = (int)min((int64_t)before, lay.at[0].chunks);
 
-    // the prefixes' chunks, a warp each: a lane a sequence
+    // the prefixes' chunks, a warp each: a lane a sequence.  A chunk goes as far as its longest sequence, whose row of
+    // the table names its pages: what lies behind a sequence's last page is not read.
     __syncthreads();
     for (int c = warp; c < lay.at[0].chunks; c += kPlanThreads / 32) {
         AttnChunk out{};
@@ -217,15 +218,24 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
             const Group g = group_of(p, gi, false);
             const int t0 = (c - group_chunk[gi]) * lay.at[0].tokens, tokens = min(lay.at[0].tokens, g.count * D - t0);
             if (tokens > 0) {
-                out.table = (int64_t)g.first * p.call.max_pages;
                 out.tok0 = g.first * D + t0;
                 out.rows = tokens * p.call.G;
-                out.len = out.seen = g.pages * kPage;
+                out.seen = g.pages * kPage;
                 out.limit = AttnChunk::kManySequences;
+                int longest = out.tok0 / D;
                 for (int n = out.tok0 / D + lane; n <= (out.tok0 + tokens - 1) / D; n += 32) {
                     const int len = capped_len(p.call, n);
                     if (len > 0) out.seen = min(out.seen, max(1, len - D + 1));
+                    if (len > out.len) {
+                        out.len = len;
+                        longest = n;
+                    }
                 }
+                const int most = __reduce_max_sync(~0u, out.len);
+                longest = __shfl_sync(~0u, longest, __ffs(__ballot_sync(~0u, out.len == most)) - 1);
+                out.len = min(most, g.pages * kPage);
+                out.seen = min(out.seen, out.len);
+                out.table = (int64_t)longest * p.call.max_pages;
             }
         }
         out.seen = __reduce_min_sync(~0u, out.seen);

@@ -200,8 +200,9 @@ KDA_API int kda_norm_rotate(const kda_attn_dims *dims, int64_t total_tokens, con
 /*
  * kda_attn_decode_shared: kda_attn_decode for sequences that share prefixes.
  * The sequences group_start[g]..group_start[g+1]-1 are a group: the first
- * shared_pages[g] entries of their block table rows name the same pages, which
- * are read from the row of the group's first sequence, once for all of them.
+ * shared_pages[g] entries of their block table rows name the same pages (as far
+ * as a sequence goes), which are read once for all of them, from the row of a
+ * sequence that goes as far as any of those that are computed together.
  * The results are those of kda_attn_decode (the shared pages are full; a
  * sequence that ends inside them sees them as far as it goes).  In bf16, where
  * many rows meet a page, queries are multiplied as two 8-bit terms, and what
