@@ -156,7 +156,11 @@ __device__ __forceinline__ int last_at_most(const int32_t *a, int n, int x) {
     return lo;
 }
 
-// What the threads before this one have of `mine`, and all together; by the whole block of 1024.
+// Sums of counts that may leave 31 bits stay at the most that these hold.
+__device__ __forceinline__ int add(int a, int b) { return (int)min((unsigned)a + (unsigned)b, 0x7fffffffu); }
+__device__ __forceinline__ int64_t add(int64_t a, int64_t b) { return a + b; }
+
+// What the threads before this one have of `mine` (not negative), and all together; by the whole block of 1024.
 template <typename T>
 __device__ __forceinline__ T scan(T mine, T *warp_sum, T &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -164,20 +168,21 @@ __device__ __forceinline__ T scan(T mine, T *warp_sum, T &total) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const T x = __shfl_up_sync(~0u, incl, o);
-        if (lane >= o) incl += x;
+        if (lane >= o) incl = add(incl, x);
     }
     if (lane == 31) warp_sum[warp] = incl;
+    const T excl = __shfl_up_sync(~0u, incl, 1);
     __syncthreads();
     T sums = warp_sum[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const T x = __shfl_up_sync(~0u, sums, o);
-        if (lane >= o) sums += x;
+        if (lane >= o) sums = add(sums, x);
     }
     __syncthreads();  // (warp_sum is free again)
     total = __shfl_sync(~0u, sums, 31);
     const T before = __shfl_sync(~0u, sums, max(warp - 1, 0));
-    return (warp > 0 ? before : 0) + incl - mine;
+    return add(warp > 0 ? before : 0, lane > 0 ? excl : 0);
 }
 static_assert(kPlanThreads == 1024, "a lane a warp");
 
@@ -193,18 +198,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = p.call.D;
 
-    // the groups' first chunks
+    // the groups' first chunks.  Groups of wrong offsets may overlap, so that there are more than their sequences can
+    // have, in all more than 31 bits hold: those that have no place here start at the end, and are no one's.
     int before = 0;
     for (int g0 = 0; g0 < p.groups; g0 += kPlanThreads) {
         int mine = 0;
         if (g0 + tid < p.groups) {
             const Group g = group_of(p, g0 + tid, true);
-            if (g.pages > 0) mine = (g.count * D + lay.at[0].tokens - 1) / lay.at[0].tokens;
+            if (g.pages > 0) mine = add(g.count * D, lay.at[0].tokens - 1) / lay.at[0].tokens;
         }
         int all;
-        const int at = before + scan(mine, warp_sum, all);
-        before += all;
-        if (g0 + tid < p.groups) group_chunk[g0 + tid] = at;
+        const int at = add(before, scan(mine, warp_sum, all));
+        before = add(before, all);
+        if (g0 + tid < p.groups) group_chunk[g0 + tid] = (int32_t)min((int64_t)at, lay.at[0].chunks);
     }
     const int used = (int)min((int64_t)before, lay.at[0].chunks);
 
