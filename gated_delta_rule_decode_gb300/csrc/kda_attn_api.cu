@@ -235,7 +235,8 @@ int kda_norm_rotate(const kda_attn_dims *dims, int64_t total_tokens, const void 
                     int32_t interleaved, float factor, const float *q_weight, const float *k_weight, float eps,
                     void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream) {
     if (const int st = check_dims(dims)) return st;
-    if (total_tokens < 0 || total_tokens > kMaxI32 || rotary_dim < 0 || rotary_dim > dims->head_dim || rotary_dim % 2 != 0)
+    // (blocks count tokens in 31 bits, and ask for those of their next round first: less than 2^14 further)
+    if (total_tokens < 0 || total_tokens > kMaxI32 - (1 << 14) || rotary_dim < 0 || rotary_dim > dims->head_dim || rotary_dim % 2 != 0)
         return KDA_ERR_INVALID_ARG;
     if (!(eps >= 0.f) || isinf(eps) || isnan(factor) || isinf(factor)) return KDA_ERR_INVALID_ARG;
     if (total_tokens == 0) return KDA_OK;

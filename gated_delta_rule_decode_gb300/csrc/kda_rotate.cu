@@ -296,6 +296,7 @@ cudaError_t launch_dim(const NormRotateParams &p, cudaStream_t st) {
     const int64_t most = std::max(1, 152 * (32 * kWarpsPerSm / threads) / parts);
     const int per = (int)std::min<int64_t>(kTokens, (p.total_tokens + most - 1) / most);
     const int64_t blocks = std::min<int64_t>((p.total_tokens + per - 1) / per, most);
+    static_assert(kTokens * 152 * kWarpsPerSm / 2 < 1 << 14, "a round's tokens behind the last: what the entry point leaves of 31 bits");
     if (parts > 65535) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)blocks, (unsigned)parts);
     if (p.interleaved) norm_rotate_kernel<T, HD, kPairs><<<grid, threads, 0, st>>>(p, warps, per);

@@ -186,7 +186,7 @@ KDA_API int kda_cache_evict(int32_t batch, int32_t max_pages, int32_t budget, in
  *   q, k         dtype [total_tokens][Hq or Hkv][d], tokens q_stride, k_stride apart
  *   q_out, k_out the same, tokens q_out_stride, k_out_stride apart; each may be
  *                its input (with its stride)
- *   positions    i32 [total_tokens], any value
+ *   positions    i32 [total_tokens], any value; total_tokens < 2^31 - 2^14
  *   turns        u64 [rotary_dim / 2]
  *   q_weight, k_weight  f32 [d], 16-byte aligned; NULL: no norm
  * dims->scale is not used.  rotary_dim even, 0..d (0: norm alone).
