@@ -219,10 +219,10 @@ int kda_attn_decode_shared(const kda_attn_dims *dims, const kda_kv_cache *cache,
     if (batch == 0) return KDA_OK;
     if (const int st = check_decode_pointers(dims, q, q_stride, seq_lens, block_table, max_pages, out, lse)) return st;
     if (num_groups > 0 && !ok4({group_start, shared_pages})) return KDA_ERR_INVALID_ARG;
-    if (!workspace_ok(workspace, workspace_bytes,
-                      kda::attn_shared_workspace_bytes(dims->q_heads, dims->kv_heads, dims->head_dim, dims->dtype, batch,
-                                                       draft_len, max_pages, num_groups)))
-        return KDA_ERR_WORKSPACE;
+    const size_t need = kda::attn_shared_workspace_bytes(dims->q_heads, dims->kv_heads, dims->head_dim, dims->dtype, batch,
+                                                         draft_len, max_pages, num_groups);
+    if (need == 0) return KDA_ERR_INVALID_ARG;  // (more rows or chunks than the kernels count)
+    if (!workspace_ok(workspace, workspace_bytes, need)) return KDA_ERR_WORKSPACE;
     kda::AttnSharedParams p{};
     p.call = decode_params(dims, cache, batch, draft_len, q, q_stride, seq_lens, block_table, max_pages, out, lse,
                            workspace, err_flag);

@@ -62,7 +62,7 @@ struct PartsAt {
     int32_t whole;                   // no item is cut
 };
 
-// The workspace, in bytes: the plan, the results of whole items, and the parts.
+// The workspace, in bytes: the plan, the results of whole items, and the parts.  total 0: a call that is too large.
 struct SharedLayout {
     int64_t group_chunk, seqs, chunks, costs, starts, total;
     PartsAt at[2];  // of the prefixes, of the rest
@@ -96,6 +96,7 @@ SharedLayout shared_layout(int Hq, int Hkv, int d, int dtype, int64_t batch, int
     l.at[0].chunks = groups > 0 ? batch * D / l.at[0].tokens + groups : 0;
     l.at[1].chunks = batch * l.at[1].per;
     const int64_t count = l.at[0].chunks + l.at[1].chunks, q = batch * D * Hq;
+    if (count * Hkv > 0xfffff000ll || q > 0x7fffffff) return l;  // (the kernels count these in 32 and 31 bits)
     l.group_chunk = take(groups * 4);
     l.seqs = take(batch * (int64_t)sizeof(SeqPlan));
     l.chunks = take(count * (int64_t)sizeof(AttnChunk));
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
     __syncthreads();
     // the first and last worker of each item, a thread each
     int *desc = reinterpret_cast<int *>(ws + lay.at[0].desc);  // (the rest's follow the prefixes')
-    for (uint32_t i = tid >> 1; i < (uint32_t)count * Hkv; i += kPlanThreads / 2) {  // (query rows fit 31 bits)
+    for (uint32_t i = tid >> 1; i < (uint32_t)count * Hkv; i += kPlanThreads / 2) {  // (shared_layout)
         const int c = (int)(i / Hkv), h = (int)(i % Hkv), pages = size(c) >> 1, page = tid & 1 ? pages - 1 : 0;
         int lo = 0, hi = W;
         while (hi - lo > 1) {
@@ -444,7 +445,7 @@ size_t attn_shared_workspace_bytes(int Hq, int Hkv, int d, int dtype, int64_t ba
 cudaError_t launch_attn_shared(const AttnSharedParams &p, int d, int dtype, cudaStream_t st) {
     const AttnDecodeParams &c = p.call;
     const SharedLayout lay = shared_layout(c.Hq, c.Hkv, d, dtype, c.batch, c.D, c.max_pages, p.groups);
-    if ((int64_t)c.batch * c.D * c.Hq > 0x7fffffff || lay.at[0].chunks + lay.at[1].chunks > 0x7fffffff) return cudaErrorInvalidValue;
+    if (lay.total == 0) return cudaErrorInvalidValue;
     unsigned char *ws = static_cast<unsigned char *>(c.workspace);
     plan_kernel<<<1, kPlanThreads, 0, st>>>(p, lay);
     cudaError_t e = cudaGetLastError();

@@ -227,7 +227,10 @@ KDA_API int kda_attn_decode_shared(const kda_attn_dims *dims, const kda_kv_cache
                                    const int32_t *group_start, const int32_t *shared_pages, void *out, float *lse,
                                    void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream);
 
-/* Workspace of kda_attn_decode_shared; 0 for invalid arguments. */
+/*
+ * Workspace of kda_attn_decode_shared; 0 for invalid arguments, and for calls of
+ * more than 2^31 - 1 query rows, or of nearly 2^32 groups times kv heads.
+ */
 KDA_API size_t kda_attn_decode_shared_workspace_bytes(const kda_attn_dims *dims, int32_t batch, int32_t draft_len,
                                                       int32_t max_pages, int32_t num_groups);
 
