@@ -493,8 +493,9 @@ def decode_shared(q, cache: KVCache, seq_lens, block_table, group_start, shared_
     group_start: [groups + 1] int32: sequences group_start[g] to
     group_start[g + 1] - 1 are a group; shared_pages: [groups] int32: so many
     entries of their block table rows, from the first, name the same pages.
-    Kernels are chosen by the groups' mean size, so leave out empty groups where
-    time counts.  Returns out [B, D, Hq, d], then with ``return_lse`` lse [B, D, Hq] fp32.
+    How many rows read a prefix together goes by the groups' mean size (see
+    ``include/kda_attn.h``): leave out empty groups and groups of one where time
+    counts.  Returns out [B, D, Hq, d], then with ``return_lse`` lse [B, D, Hq] fp32.
     """
     width, groups = block_table.shape[1], shared_pages.shape[0]
     dev, c, dims, qs, out, lse = _decode_args(q, cache, seq_lens, block_table, lambda B, Hkv: (B, width), out, lse,

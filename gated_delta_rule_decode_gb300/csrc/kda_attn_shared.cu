@@ -5,11 +5,12 @@
 //
 // plan_kernel lays the batch out as chunks: up to R query rows of one group and
 // its prefix; a sequence's rows and the rest of it.  The chunks are attended as
-// items of a kernel whose results stay apart as (o, m, l): on tcgen05 (bf16,
-// d = 64 and 128; kda_attn_shared_tc.cu) all in one launch, whose workers' ranges
-// the plan cuts by cost; otherwise by the kernels of kda_attn_decode_rows.cuh,
-// the prefixes' chunks and then the others'.  merge_kernel adds up all parts of
-// a row in a fixed order.
+// items of kernels whose results stay apart as (o, m, l): on tcgen05 (bf16,
+// d = 64 and 128; kda_attn_shared_tc.cu) in one launch, whose workers' ranges the
+// plan cuts by cost, or by the kernels of kda_attn_decode_rows.cuh, the prefixes'
+// chunks and then the others'.  Where groups are small in the mean, their prefixes
+// have a launch for few rows, and groups that are large all the same one of their
+// own.  merge_kernel adds up all parts of a row in a fixed order.
 //
 // Measured (bf16, d = 128, 32 heads over 8): 64 sequences of up to 2048 positions
 // after a prefix of 8192: 96 us, of which the plan 6, the prefix 24, the rests 55 and
@@ -33,9 +34,10 @@ using namespace dec;
 constexpr int kPlanThreads = 1024;
 
 // Where a sequence's parts lie: base: positions of its prefix; first: the first
-// chunk of its group's; token: its first token within the group's.
+// chunk of its group's (few: among those of small groups); token: its first token
+// within the group's.
 struct SeqPlan {
-    int32_t base, first, token, pad;
+    int32_t base, first, token, few;
 };
 
 // The tcgen05 workers' costs, in half blocks of 64 positions of up to 128 rows: a
@@ -50,9 +52,16 @@ constexpr int kItemCost = 9;
 // 83, 93 us with the warps' kernel.  Rests of 4 rows (32 sequences after 1600
 // pages) 121 us there, 104 with the warps' kernel; of 20 rows 106 and 257.
 constexpr int kFewShared = 8, kFewRows = 16;
+// Among groups of kFewShared rows in the mean, those of more than kLargeGroup are read apart, once for up to 256 rows
+// on tcgen05 and for up to 64 elsewhere instead of once for 8.  That launch costs 4 us where there are none, so it is
+// left out where it could not save much: where no more than kLongReads pages of a kv head could be read for chunks of 8
+// rows.  One group of 64 sequences among 63 of one (32 heads over 8, d = 128): prefixes of 1600 pages 922 us without
+// and 228 with it, of 128 pages 194 and 202; 16, 32 and 64 groups of 64 sequences, 32 pages, 55, 74, 82 and 60, 80, 87.
+constexpr int kLargeGroup = 32;
+constexpr double kLongReads = 1 << 16;
 constexpr int kPlanCached = 2048;  // chunks whose costs fit the plan's shared memory
 
-// Where the parts of one of the two attentions are: an item's workers (first,
+// Where the parts of one of the attentions are: an item's workers (first,
 // last) in desc, two slots a worker of PR rows each, RB items a chunk and kv head
 // of R rows.
 struct PartsAt {
@@ -65,19 +74,23 @@ struct PartsAt {
 // The workspace, in bytes: the plan, the results of whole items, and the parts.  total 0: a call that is too large.
 struct SharedLayout {
     int64_t group_chunk, seqs, chunks, costs, starts, total;
-    PartsAt at[2];  // of the prefixes, of the rest
-    int64_t ws[2];  // off tcgen05: workspaces of the two launches
-    Layout lay[2];
-    int32_t tc[2], workers;
+    PartsAt at[3];  // of the prefixes, of the rests, of the prefixes of small groups; their chunks follow one another
+    int64_t ws[3];  // off tcgen05: workspaces of the launches
+    Layout lay[3];
+    int32_t tc[3], workers;
+    int32_t few;  // where groups are small in the mean, the most rows of one that counts as small, else 0
+    int32_t on_tc;
 };
 
 SharedLayout shared_layout(int Hq, int Hkv, int d, int dtype, int64_t batch, int D, int64_t max_pages, int64_t groups) {
     const int G = Hq / Hkv;
     SharedLayout l{};
+    l.tc[0] = dtype == KDA_DT_BF16 && d >= 64;
+    l.tc[1] = l.tc[0] && D * G > kFewRows;
     // the rows of a group of mean size
     const int64_t mean = (batch + groups - 1) / std::max<int64_t>(groups, 1) * D * G;
-    l.tc[0] = dtype == KDA_DT_BF16 && d >= 64 && mean > kFewShared;
-    l.tc[1] = l.tc[0] && D * G > kFewRows;
+    const double reads = (double)batch * D * G / kFewShared * max_pages * Hkv;
+    l.few = groups == 0 || mean > kFewShared ? 0 : reads > kLongReads ? kLargeGroup : 0x7fffffff;
     l.workers = kSms;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -85,26 +98,33 @@ SharedLayout shared_layout(int Hq, int Hkv, int d, int dtype, int64_t batch, int
         at += (bytes + 255) / 256 * 256;
         return here;
     };
-    // a chunk has the whole tokens that fit an item's rows: of a group of mean size, of a sequence
+    // a chunk has the whole tokens that fit an item's rows
     auto tokens = [&](int s, int64_t rows) {
         if (l.tc[s]) return kPartRows / G;
         return std::max(1, make_parts_layout(1, (int)std::min<int64_t>(rows, 4096), Hkv, d, dtype, max_pages).R / G);
     };
-    l.at[0].tokens = tokens(0, std::max<int64_t>(mean, G));
+    l.at[0].tokens = tokens(0, l.few > 0 ? kPartRows : std::max<int64_t>(mean, G));
     l.at[1].tokens = std::min(D, tokens(1, (int64_t)D * G));
     l.at[1].per = (D + l.at[1].tokens - 1) / l.at[1].tokens;
-    l.at[0].chunks = groups > 0 ? batch * D / l.at[0].tokens + groups : 0;
+    l.at[0].chunks = groups > 0 && batch * D * G > l.few ? batch * D / l.at[0].tokens + groups : 0;
     l.at[1].chunks = batch * l.at[1].per;
-    const int64_t count = l.at[0].chunks + l.at[1].chunks, q = batch * D * Hq;
+    if (l.few > 0) {
+        l.at[2].tokens = kFewShared / G;  // (a sequence has no more rows)
+        l.at[2].chunks = batch * D / l.at[2].tokens + groups;
+    }
+    l.on_tc = (l.tc[0] && l.at[0].chunks > 0) || l.tc[1];
+    const int64_t count = l.at[0].chunks + l.at[1].chunks + l.at[2].chunks, q = batch * D * Hq;
     if (count * Hkv > 0xfffff000ll || q > 0x7fffffff) return l;  // (the kernels count these in 32 and 31 bits)
-    l.group_chunk = take(groups * 4);
+    l.group_chunk = take(2 * groups * 4);
     l.seqs = take(batch * (int64_t)sizeof(SeqPlan));
     l.chunks = take(count * (int64_t)sizeof(AttnChunk));
     for (int s = 0; s < 2; ++s) {
         l.at[s].ml = take(q * 8);
         l.at[s].o = take(q * d * 4);
     }
-    if (l.tc[0]) {
+    l.at[2].ml = l.at[0].ml;  // (a row has one prefix)
+    l.at[2].o = l.at[0].o;
+    if (l.on_tc) {
         l.costs = take(count * 8);
         l.starts = take((l.workers + 1) * (int64_t)sizeof(int4));
         const int64_t rows = 2 * (int64_t)l.workers * kPartRows;
@@ -116,8 +136,8 @@ SharedLayout shared_layout(int Hq, int Hkv, int d, int dtype, int64_t batch, int
             a.workers = l.workers; a.R = a.PR = kPartRows; a.RB = 1;
         }
     }
-    for (int s = 0; s < 2; ++s) {
-        if (l.tc[s]) continue;
+    for (int s = 0; s < 3; ++s) {
+        if (l.tc[s] || l.at[s].chunks == 0) continue;
         PartsAt &a = l.at[s];
         const Layout y = make_parts_layout(a.chunks, a.tokens * G, Hkv, d, dtype, max_pages);
         const int64_t ws = take(y.total * 4);
@@ -144,6 +164,13 @@ __device__ __forceinline__ Group group_of(const AttnSharedParams &p, int g, bool
         if (s < 0 || s > p.call.max_pages) atomicOr(p.call.err_flag, KDA_DEVERR_PAGE);
     }
     return Group{a, bad ? 0 : b - a, s < 0 ? 0 : min(s, p.call.max_pages)};
+}
+
+// How a group's prefix is attended: not at all, among those of small groups, among the others.
+enum Sharing { kNone, kFew, kMany };
+__device__ __forceinline__ Sharing sharing_of(const AttnSharedParams &p, const SharedLayout &lay, const Group &g) {
+    if (g.pages == 0 || g.count == 0) return kNone;
+    return (int64_t)g.count * p.call.D * p.call.G <= lay.few ? kFew : kMany;
 }
 
 // The last of a[0..n-1] that is <= x, -1 for none.
@@ -195,35 +222,46 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
     int32_t *group_chunk = reinterpret_cast<int32_t *>(ws + lay.group_chunk);
     SeqPlan *seqs = reinterpret_cast<SeqPlan *>(ws + lay.seqs);
     AttnChunk *prefix = reinterpret_cast<AttnChunk *>(ws + lay.chunks), *rest = prefix + lay.at[0].chunks;
+    AttnChunk *few_prefix = rest + lay.at[1].chunks;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = p.call.D;
 
-    // the groups' first chunks.  Groups of wrong offsets may overlap, so that there are more than their sequences can
-    // have, in all more than 31 bits hold: those that have no place here start at the end, and are no one's.
-    int before = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += kPlanThreads) {
-        int mine = 0;
-        if (g0 + tid < p.groups) {
-            const Group g = group_of(p, g0 + tid, true);
-            if (g.pages > 0) mine = add(g.count * D, lay.at[0].tokens - 1) / lay.at[0].tokens;
+    // the groups' first chunks, of `cap` in all.  Groups of wrong offsets may overlap, so that there are more than their
+    // sequences can have, in all more than 31 bits hold: those that have no place here start at the end, and are no one's.
+    const int64_t many = lay.at[0].chunks, few = lay.at[2].chunks;
+    auto first_chunks = [&](int32_t *first, Sharing which, int tokens, int64_t cap) {
+        int before = 0;
+        for (int g0 = 0; g0 < p.groups; g0 += kPlanThreads) {
+            int mine = 0;
+            if (g0 + tid < p.groups) {
+                const Group g = group_of(p, g0 + tid, which == kMany || many == 0);
+                if (sharing_of(p, lay, g) == which) mine = add(g.count * D, tokens - 1) / tokens;
+            }
+            int all;
+            const int at = add(before, scan(mine, warp_sum, all));
+            before = add(before, all);
+            if (g0 + tid < p.groups) first[g0 + tid] = (int32_t)min((int64_t)at, cap);
         }
-        int all;
-        const int at = add(before, scan(mine, warp_sum, all));
-        before = add(before, all);
-        if (g0 + tid < p.groups) group_chunk[g0 + tid] = (int32_t)min((int64_t)at, lay.at[0].chunks);
-    }
-    const int used = (int)min((int64_t)before, lay.at[0].chunks);
+        return min((int64_t)before, cap);
+    };
+    int32_t *few_chunk = group_chunk + p.groups;
+    const int64_t used = many > 0 ? first_chunks(group_chunk, kMany, lay.at[0].tokens, many) : 0;
+    const int64_t few_used = few > 0 ? first_chunks(few_chunk, kFew, lay.at[2].tokens, few) : 0;
 
     // the prefixes' chunks, a warp each: a lane a sequence.  A chunk goes as far as its longest sequence, whose row of
     // the table names its pages: what lies behind a sequence's last page is not read.
     __syncthreads();
-    for (int c = warp; c < lay.at[0].chunks; c += kPlanThreads / 32) {
+    // (where there are none on tcgen05, no chunk is looked at there)
+    for (int64_t c = warp + (used == 0 && lay.tc[0] && !lay.tc[1] ? many : 0); c < many + few; c += kPlanThreads / 32) {
         AttnChunk out{};
-        if (c < used) {
-            const int gi = last_at_most(group_chunk, p.groups, c);
+        const bool is_few = c >= many;
+        const int at = (int)(is_few ? c - many : c);
+        if (at < (is_few ? few_used : used)) {
+            const int32_t *first = is_few ? few_chunk : group_chunk;
+            const int gi = last_at_most(first, p.groups, at), most = lay.at[is_few ? 2 : 0].tokens;
             const Group g = group_of(p, gi, false);
-            const int t0 = (c - group_chunk[gi]) * lay.at[0].tokens, tokens = min(lay.at[0].tokens, g.count * D - t0);
+            const int t0 = (at - first[gi]) * most, tokens = min(most, g.count * D - t0);
             if (tokens > 0) {
                 out.tok0 = g.first * D + t0;
                 out.rows = tokens * p.call.G;
@@ -238,17 +276,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
                         longest = n;
                     }
                 }
-                const int most = __reduce_max_sync(~0u, out.len);
-                longest = __shfl_sync(~0u, longest, __ffs(__ballot_sync(~0u, out.len == most)) - 1);
-                out.len = min(most, g.pages * kPage);
+                const int len = __reduce_max_sync(~0u, out.len);
+                longest = __shfl_sync(~0u, longest, __ffs(__ballot_sync(~0u, out.len == len)) - 1);
+                out.len = min(len, g.pages * kPage);
                 out.seen = min(out.seen, out.len);
                 out.table = (int64_t)longest * p.call.max_pages;
             }
         }
         out.seen = __reduce_min_sync(~0u, out.seen);
         if (lane == 0) {
-            prefix[c] = out;
-            if (c < kPlanCached) sizes[c] = size_of(out);
+            (is_few ? few_prefix : prefix)[at] = out;
+            if (!is_few && at < kPlanCached) sizes[at] = size_of(out);
         }
     }
     // the sequences, and the chunks of what follows their prefixes (from the last warps on: the first have the chunks above)
@@ -258,9 +296,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
         if (p.call.err_flag && p.call.seq_lens[n] > p.call.max_pages * kPage) atomicOr(p.call.err_flag, KDA_DEVERR_PAGE);
         if (gi >= 0) {
             const Group g = group_of(p, gi, false);
-            if (n >= g.first && n < g.first + g.count) {
+            const Sharing how = sharing_of(p, lay, g);
+            if (how != kNone && n >= g.first && n < g.first + g.count) {
                 out.base = g.pages * kPage;
-                out.first = group_chunk[gi];
+                out.few = how == kFew;
+                out.first = how == kFew ? few_chunk[gi] : group_chunk[gi];
                 out.token = (n - g.first) * D;
             }
         }
@@ -280,7 +320,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
             if (at < kPlanCached) sizes[at] = size_of(c);
         }
     }
-    if (!lay.tc[0]) return;
+    if (!lay.on_tc) return;
 
     // ---- the workers' ranges: the chunks' costs laid end to end, cut evenly
     __shared__ int64_t cached[kPlanCached];
@@ -288,6 +328,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnSharedPara
     __shared__ int4 starts[kSms + 1];
     const int count = (int)(lay.at[0].chunks + (lay.tc[1] ? lay.at[1].chunks : 0)), Hkv = p.call.Hkv;
     int64_t *costs = count <= kPlanCached ? cached : reinterpret_cast<int64_t *>(ws + lay.costs);
+    if (used == 0 && !lay.tc[1]) {  // small groups alone
+        if (tid <= lay.workers) reinterpret_cast<int4 *>(ws + lay.starts)[tid] = make_int4(count, 0, 0, 0);
+        return;
+    }
     __syncthreads();  // (the chunks are written)
     auto size = [&](int c) { return c < kPlanCached ? sizes[c] : size_of(prefix[c]); };
     auto weight = [](int size) { return 1 + (size & 1); };
@@ -362,7 +406,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const AttnSharedPa
     int count[2], first[2], row[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const PartsAt &a = lay.at[s];
+        const bool few = s == 0 && sp.few;
+        const PartsAt &a = lay.at[few ? 2 : s];
         const int local = s == 0 ? sp.token + t : t;
         const int64_t chunk = (s == 0 ? (int64_t)sp.first : (int64_t)n * a.per) + local / a.tokens;
         const int r = (local % a.tokens) * c.G + gi, rb = r / a.R;
@@ -380,7 +425,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const AttnSharedPa
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const PartsAt &a = lay.at[s];
+        const PartsAt &a = lay.at[s == 0 && sp.few ? 2 : s];
         const float *part_m = reinterpret_cast<const float *>(ws + a.part_m), *part_l = reinterpret_cast<const float *>(ws + a.part_l);
         const float *part_o = reinterpret_cast<const float *>(ws + a.part_o);
         constexpr int BATCH = 4;
@@ -391,10 +436,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const AttnSharedPa
             for (int b = 0; b < BATCH; ++b) {
                 const int x = min(x0 + b, count[s] - 1);
                 if (count[s] == 1) {
-                    const float2 ml = reinterpret_cast<const float2 *>(ws + a.ml)[qrow];
+                    const float2 ml = reinterpret_cast<const float2 *>(ws + lay.at[s].ml)[qrow];
                     pm[b] = ml.x;
                     pl[b] = ml.y;
-                    v[b] = reinterpret_cast<const float4 *>(ws + a.o)[qrow * TPR + c4];
+                    v[b] = reinterpret_cast<const float4 *>(ws + lay.at[s].o)[qrow * TPR + c4];
                 } else {  // part x lies in slot 2 (w + x), the first in slot 2 w + 1
                     const int64_t k = (2 * ((int64_t)first[s] + x) + (x == 0 ? 1 : 0)) * a.PR + row[s];
                     pm[b] = part_m[k];
@@ -452,7 +497,7 @@ cudaError_t launch_attn_shared(const AttnSharedParams &p, int d, int dtype, cuda
     if (e != cudaSuccess) return e;
     const AttnChunk *chunks = reinterpret_cast<const AttnChunk *>(ws + lay.chunks);
     auto floats = [&](int64_t at) { return reinterpret_cast<float *>(ws + at); };
-    if (lay.tc[0] && c.max_pages > 0) {
+    auto attend_tc = [&] {
         AttnDecodeParams q = c;
         q.chunks = chunks;
         PartsPlan plan{};
@@ -464,20 +509,23 @@ cudaError_t launch_attn_shared(const AttnSharedParams &p, int d, int dtype, cuda
         plan.rest_ml = reinterpret_cast<float2 *>(ws + lay.at[1].ml);
         plan.first_rest = (int32_t)lay.at[0].chunks;
         plan.rows = kPartRows;
-        e = launch_parts_tc(q, plan, lay.workers, d, st);
-        if (e != cudaSuccess) return e;
-    }
-    for (int s = 0; s < 2; ++s) {
-        if (lay.tc[s] || c.max_pages == 0 || lay.at[s].chunks == 0) continue;
+        return launch_parts_tc(q, plan, lay.workers, d, st);
+    };
+    auto attend = [&](int s) {
+        if (lay.tc[s] || lay.at[s].chunks == 0) return cudaSuccess;
         AttnDecodeParams q = c;
-        q.chunks = chunks + (s == 0 ? 0 : lay.at[0].chunks);
+        q.chunks = chunks + (s == 0 ? 0 : lay.at[0].chunks + (s == 1 ? 0 : lay.at[1].chunks));
         q.part_ml = reinterpret_cast<float2 *>(ws + lay.at[s].ml);
         q.out = ws + lay.at[s].o;
         q.lse = nullptr;
         q.workspace = ws + lay.ws[s];
         q.batch = (int32_t)lay.at[s].chunks;
-        e = launch_parts(q, lay.lay[s], d, dtype, st);
-        if (e != cudaSuccess) return e;
+        return launch_parts(q, lay.lay[s], d, dtype, st);
+    };
+    if (c.max_pages > 0) {
+        if (lay.on_tc && (e = attend_tc()) != cudaSuccess) return e;
+        for (int s : {0, 2, 1})
+            if ((e = attend(s)) != cudaSuccess) return e;
     }
     return dtype == KDA_DT_BF16 ? launch_merge<__nv_bfloat16>(p, lay, d, st) : launch_merge<float>(p, lay, d, st);
 }

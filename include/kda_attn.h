@@ -208,8 +208,15 @@ KDA_API int kda_norm_rotate(const kda_attn_dims *dims, int64_t total_tokens, con
  * many rows meet a page, queries are multiplied as two 8-bit terms, and what
  * these leave is added where it could come to more than 2^-14 of a score (in
  * units of log 2): the weights' own rounding is 2^-11.  Sequences of
- * no group share nothing.  Kernels are chosen by batch / num_groups, the mean
- * size of a group: many empty groups cost time, not results.
+ * no group share nothing.
+ *
+ * "Once" is for up to 256 query rows of a kv head (a group's tokens times G); in
+ * fp32 and at d = 32 for up to 64.  Where groups have up to 8 rows in the mean
+ * (of ceil(batch / num_groups) sequences), it is for 8, which is quicker, and
+ * groups of more than 32 rows are read apart where the block table is long; in
+ * fp32 and at d = 32 a mean of up to 16 or 32 rows is for as many.  Empty groups,
+ * groups of one and sequences of no group count in the mean: that can cost time,
+ * never results.
  *
  *   group_start  i32 [num_groups + 1], not decreasing, in 0..batch; offsets
  *                that are not set KDA_DEVERR_SEQLENS, and the outputs of the

@@ -41,3 +41,50 @@ def test_wrong_offsets_whose_groups_sum_past_31_bits():
     flag.zero_()
     out = a.decode_shared(q, c, lens, table, _i32([0, B]).cuda(), _i32([1]).cuda(), err_flag=flag)
     assert flag.item() == 0 and (out == 0).all()  # (the cache's values)
+
+
+WIDE = 2000  # columns of a table in which reading a large group's prefix for few rows at a time would cost
+
+
+def _mixed(g, big, small, hkv, d, width=WIDE):
+    """One large group among small ones, of one, two and five sequences, of none, and sequences of no group."""
+    groups = [(0, [70])] + [(2, [130 + i]) for i in range(small)] + [(3, [200 + 3 * i for i in range(big)])]
+    groups += [(1, [100, 65]), (4, [300] * 5), (2, []), (3, [])] + [(1, [64 + i]) for i in range(small)]
+    return _case(g, groups, hkv, d, width=width)
+
+
+@pytest.mark.parametrize("width", [0, WIDE])
+@pytest.mark.parametrize("dtype,D,hq,hkv,d", [(BF, 1, 8, 2, 128), (BF, 2, 3, 1, 64), (F32, 1, 8, 2, 64), (BF, 1, 8, 2, 32), (F32, 3, 4, 2, 128),
+                                              (BF, 1, 32, 2, 128), (BF, 1, 1, 1, 64)])
+def test_a_large_group_among_small_ones(dtype, D, hq, hkv, d, width):
+    g = gen(d + D + hq)
+    case = _mixed(g, 37, 20, hkv, d, width)
+    _compare(case, (2 * randn(g, case[1].shape[0], D, hq, d)).to(dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype,d,together", [(BF, 128, 64), (BF, 64, 64), (F32, 64, 16)])
+def test_a_large_groups_prefix_is_read_for_many_rows_together(dtype, d, together):
+    """The pages are named by one row of the table for as many sequences as are computed together: 256 rows of queries,
+    64 where the tensor cores do not compute them."""
+    g = gen(d)
+    groups = [(1, [80 + i]) for i in range(70)] + [(3, [193 + i % 50 + (60 if i % together == 7 else 0) for i in range(64)])]
+    case = list(_case(g, groups, 2, d, width=WIDE))
+    q = randn(g, 134, 1, 8, d).to(dtype)
+    want, want_lse, tol, tol_lse = _want(case, q, dtype)
+    case[2] = case[2].clone()
+    for i in range(64):
+        if i % together != 7:  # (not the longest of them)
+            case[2][70 + i, :3] = -1
+    out, lse, flag = _run(tuple(case), q)
+    assert flag == 0
+    check(out, want, tol, "out")
+    check(lse, want_lse, tol_lse, "lse")
+
+
+@pytest.mark.parametrize("B", [1, 3])
+def test_windows_of_no_group(B):
+    """No prefixes at all: the sequences' own rows choose how they are attended."""
+    g = gen(B)
+    case = list(_case(g, [(0, [900, 130, 16][:B])], 2, 128))
+    case[3], case[4] = _i32([0]), torch.zeros(0, dtype=torch.int32)
+    _compare(tuple(case), (2 * randn(g, B, 16, 16, 128)).to(BF), BF)
