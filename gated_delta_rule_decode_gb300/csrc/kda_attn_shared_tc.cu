@@ -262,7 +262,7 @@ __device__ __forceinline__ void load_queries(const AttnDecodeParams &p, const It
 #pragma unroll
             for (int o = 1; o < PIECES; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
             int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-            ex = ex < -100 ? -100 : ex > 126 ? 126 : ex;
+            ex = ex < -100 ? -100 : ex > 127 ? 127 : ex;  // (128: infinities and NaN stay what they are)
             const float mul = row_scale(ex);
             uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
@@ -307,7 +307,7 @@ __device__ __noinline__ void add_left(const AttnDecodeParams &p, const Items &it
     if (row >= 0) {
         q += ((int64_t)it.chunk.tok0 + row / p.G) * p.q_stride + (int64_t)(it.head * p.G + row % p.G) * HD;
         mul = row_scale(exps[row]);
-        bound = kLeftOut * mul / (p.scale * kLog2e * page.ks * 448.f);
+        bound = kLeftOut / (448.f * kLog2e) * mul / page.ks / p.scale;  // (in this order within fp32's range)
     }
     auto left_of = [&](int c) {
         const uint32_t w = row >= 0 ? *reinterpret_cast<const uint32_t *>(q + c) : 0u;

@@ -1,4 +1,4 @@
-"""Page selection: windows of many rows, scores of any size, errors whatever the budget."""
+"""Page selection: windows of many rows, rows of many pages, scores of any size, errors whatever the budget."""
 import pytest
 import torch
 
@@ -69,3 +69,11 @@ def test_errors_of_sequences_that_keep_all_their_pages(width):
         _selects(q, b, odd, lens, base, 8, 1, 2, a.KDA_DEVERR_SCALE)
         odd[5, 1], odd[9, 0] = u[5, 1], bad  # of a page that no row names
         _selects(q, b, odd, lens, base, 8, 1, 2)
+
+
+@pytest.mark.parametrize("P,budget", [(50001, 300), (52000, 51990)])
+def test_rows_whose_scores_do_not_fit_shared_memory(P, budget):
+    g = gen(P)
+    b, u = _random_summary(g, 900, 1, 32)  # (pages repeat, and so do scores)
+    table = torch.randint(0, 900, (1, P), generator=g, dtype=torch.int32)
+    _selects(randn(g, 1, 1, 1, 32).to(BF), b, u, _i32([P * 64 - 9]), table, budget, 1, 2)
