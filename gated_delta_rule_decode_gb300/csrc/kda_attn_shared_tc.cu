@@ -68,9 +68,10 @@ constexpr float kLazy = 8.f;
 constexpr int kSoftRegs = 80, kOtherRegs = 56;
 static_assert(32 * kSoftWarps * kSoftRegs + (kThreads - 32 * kSoftWarps) * kOtherRegs <= kThreads * 72, "registers of a launched CTA");
 constexpr int kBias = 7;  // log2 of the weights' fp16 scale
-// What the queries' two terms may leave out of a score (base 2) before it is added in fp32.  A weight is rounded
-// by 2^-11 next to it.  Rows of normal elements leave less than this until their scores reach thousands.
-constexpr float kLeftOut = 0x1p-14f;
+// What the queries' two terms may leave out of a score (base 2) before it is added in fp32: as much as a weight is
+// rounded by.  It is compared with the sum of what is left times the largest key that a page's scale can hold, so rows
+// of normal elements leave less until their scores reach thousands.
+constexpr float kLeftOut = 0x1p-11f;
 
 template <int HD>
 struct Cfg {
@@ -309,22 +310,35 @@ __device__ __noinline__ void add_left(const AttnDecodeParams &p, const Items &it
         mul = row_scale(exps[row]);
         bound = kLeftOut / (448.f * kLog2e) * mul / page.ks / p.scale;  // (in this order within fp32's range)
     }
-    auto left_of = [&](int c) {
-        const uint32_t w = row >= 0 ? *reinterpret_cast<const uint32_t *>(q + c) : 0u;
-        return terms_of(__uint_as_float(w << 16) * mul, __uint_as_float(w & 0xffff0000u) * mul).left;
-    };
+    auto left_of = [&](uint32_t w) { return terms_of(__uint_as_float(w << 16) * mul, __uint_as_float(w & 0xffff0000u) * mul).left; };
+    // the row's pairs of channels of which something is left, and how much of all
+    uint64_t pairs = 0;
     float sum = 0.f;
 #pragma unroll 1
-    for (int c = 0; c < HD; c += 2) {
-        const float2 x = left_of(c);
-        sum += fabsf(x.x) + fabsf(x.y);
-    }
-    if (!(sum > bound)) row = -1;  // (NaN: its scores are NaN already)
-    __syncwarp();
+    for (int c = 0; row >= 0 && c < HD; c += 8) {
+        uint4 v = *reinterpret_cast<const uint4 *>(q + c);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float amin = INFINITY;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            amin = fminf(amin, fminf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+        if (!(amin * mul < 0x1p-6f)) continue;
 #pragma unroll 1
-    for (int c = 0; c < HD; c += 2) {
-        const float2 x = left_of(c);
-        if (!__any_sync(~0u, x.x != 0.f || x.y != 0.f)) continue;
+        for (int e = 0; e < 4; ++e) {
+            const float2 x = left_of(v.x);
+            sum += fabsf(x.x) + fabsf(x.y);
+            if (x.x != 0.f || x.y != 0.f) pairs |= (uint64_t)1 << (c / 2 + e);
+            v.x = v.y; v.y = v.z; v.z = v.w;
+        }
+    }
+    if (!(sum > bound)) pairs = 0;  // (NaN: its scores are NaN already)
+    // each row its own pairs, one at a time: the lanes' bytes are of one key's row
+    while (__any_sync(~0u, pairs != 0)) {
+        const int c = pairs != 0 ? 2 * (__ffsll(pairs) - 1) : 0;
+        float2 x = make_float2(0.f, 0.f);
+        if (pairs != 0) x = left_of(*reinterpret_cast<const uint32_t *>(q + c));
+        pairs &= pairs - 1;
+        __syncwarp();
         const unsigned char *key = p.k_pages + (int64_t)page.block * Cfg<HD>::kHalf + c;
 #pragma unroll 1
         for (int i = 0; i < 4; ++i, key += 16 * HD) {

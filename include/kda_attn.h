@@ -206,9 +206,9 @@ KDA_API int kda_norm_rotate(const kda_attn_dims *dims, int64_t total_tokens, con
  * The results are those of kda_attn_decode (the shared pages are full; a
  * sequence that ends inside them sees them as far as it goes).  In bf16, where
  * many rows meet a page, queries are multiplied as two 8-bit terms, and what
- * these leave is added where it could come to more than 2^-14 of a score (in
- * units of log 2): the weights' own rounding is 2^-11.  Sequences of
- * no group share nothing.
+ * these leave is added where it could come to more than 2^-11 of a score (in
+ * units of log 2), which is the weights' own rounding.  Sequences of no group
+ * share nothing.
  *
  * "Once" is for up to 256 query rows of a kv head (a group's tokens times G); in
  * fp32 and at d = 32 for up to 64.  Where groups have up to 8 rows in the mean

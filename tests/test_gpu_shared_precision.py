@@ -3,9 +3,9 @@
 There a query row is scaled so that its largest element is in 2^7..2^8 and multiplied as an e4m3 term and an e5m2
 term of what the first leaves.  With x an element of 2^e.., 8 bits, steps of 2^(e-7): the first term leaves at most
 half its step, max(2^(e-4), 2^-10), in steps of 2^(e-7).  Down to e = -6 that is a sum of 3 bits, which e5m2 holds
-exactly (its smallest step is 2^-16).  Where the terms leave more than 2^-14 / log2(e) of a score (sum of |what is
-left| times the largest key), the scores get it in fp32: a score is off by at most 2^-14, besides what `bounds`
-counts for every kernel."""
+exactly (its smallest step is 2^-16).  Where what the terms leave (the sum of its magnitudes times the largest key that
+the page's scale can hold) may be more than 2^-11 of a score in units of log 2, the scores get it in fp32: a score is off
+by at most 2^-11 ln 2, as much as a weight's rounding moves it, besides what `bounds` counts for every kernel."""
 import numpy as np
 import pytest
 import torch
@@ -16,7 +16,7 @@ from oracle import attention as ref
 from test_gpu_attn_shared import _case, _run
 
 BF = torch.bfloat16
-OFF = 2.0 ** -14
+OFF = 2.0 ** -11 * np.log(2)
 
 
 def _compare(case, q):
