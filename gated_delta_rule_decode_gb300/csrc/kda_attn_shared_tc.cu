@@ -72,6 +72,7 @@ constexpr int kBias = 7;  // log2 of the weights' fp16 scale
 // rounded by.  It is compared with the sum of what is left times the largest key that a page's scale can hold, so rows
 // of normal elements leave less until their scores reach thousands.
 constexpr float kLeftOut = 0x1p-11f;
+constexpr float kLeastQuery = 0x1p-6f, kMostQuery = 448.f;  // scaled elements between these are held by the two terms
 
 template <int HD>
 struct Cfg {
@@ -211,7 +212,7 @@ __device__ __forceinline__ void mma_f8_ss_warp(uint32_t d_tmem, uint64_t a_desc,
 }
 
 // Pairs of a query's elements, scaled (see load_queries): their first term, of e4m3, their second, of e5m2, and what
-// the two leave.
+// the two leave: all of an element that is too large for e4m3.
 struct Terms {
     uint32_t first, second;
     float2 left;
@@ -219,11 +220,12 @@ struct Terms {
 __device__ __forceinline__ Terms terms_of(float x0, float x1) {
     Terms t;
     // (an infinite query makes its row NaN, as its scores would)
-    t.first = to_e4m3x2(x0 - x0 == 0.f ? x0 : NAN, x1 - x1 == 0.f ? x1 : NAN);
+    const float y0 = fabsf(x0) <= kMostQuery ? x0 : x0 - x0, y1 = fabsf(x1) <= kMostQuery ? x1 : x1 - x1;
+    t.first = to_e4m3x2(y0, y1);
     uint32_t u, unused;
     e4m3x4_to_f16(t.first, u, unused);
     const float2 first = unpack_f16(u);
-    t.second = to_e5m2x2(x0 - first.x, x1 - first.y);
+    t.second = to_e5m2x2(y0 - first.x, y1 - first.y);
     const float2 second = unpack_f16((t.second & 0xffu) << 8 | (t.second & 0xff00u) << 16);  // (e5m2 is fp16's upper byte)
     t.left = make_float2((x0 - first.x) - second.x, (x1 - first.y) - second.y);
     return t;
@@ -233,7 +235,10 @@ __device__ __forceinline__ float row_scale(int ex) { return __uint_as_float((uin
 // An item's query rows, scaled by powers of two to 2^7..2^8, as an e4m3 and an e5m2 term.  Of an element's 8 bits the
 // first holds 4 and leaves at most half of the last of these: 3 bits, which the second holds exactly down to elements
 // of 2^-6, 2^-13 of the row's largest.  Of those below it leaves up to 2^-14, 2^-21 of the largest, and the softmax
-// adds that in fp32 where it may count (add_left).  All softmax threads, 8 channels each.
+// adds that in fp32 where it may count (add_left).  A row with a few elements of more than 2^7 times the others is
+// scaled by the others, and these few are left whole: it is one or two channels then that the softmax adds, not all
+// (64 sequences after 128 pages, every row with a channel of 2^10, 2^14, 2^20 times the others: 137, 120, 116 us instead
+// of 265, 916, 1068; without one 63).  All softmax threads, 8 channels each.
 template <int HD>
 __device__ __forceinline__ void load_queries(const AttnDecodeParams &p, const Items &it, unsigned char *sq, int8_t *exps, float *lefts,
                                              int id) {
@@ -260,11 +265,12 @@ __device__ __forceinline__ void load_queries(const AttnDecodeParams &p, const It
                 amax = fmaxf(amax, fmaxf(x0, x1));
                 amin = fminf(amin, fminf(x0, x1));
             }
+            const float mine = amax;
 #pragma unroll
             for (int o = 1; o < PIECES; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
             int ex = (int)(__float_as_uint(amax) >> 23) - 127;
             ex = ex < -100 ? -100 : ex > 127 ? 127 : ex;  // (128: infinities and NaN stay what they are)
-            const float mul = row_scale(ex);
+            float mul = row_scale(ex);
             uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -272,16 +278,31 @@ __device__ __forceinline__ void load_queries(const AttnDecodeParams &p, const It
                 hi[e >> 1] |= t.first << (16 * (e & 1));
                 lo[e >> 1] |= t.second << (16 * (e & 1));
             }
-            if (row < rows && amin * mul < 0x1p-6f) {  // (two of a thousand lanes, of normal elements)
+            if (__any_sync(~0u, row < rows && amin * mul < kLeastQuery)) {  // (one warp in twenty, of normal elements)
+                // pieces of the row with large elements: where they are few, the others' largest is the row's scale,
+                // but within 2^100 of the row's, which has to stay finite
+                const bool large = mine > 0x1p-7f * amax;
+                const int pieces = __popc(__ballot_sync(~0u, large) >> ((id & 31) / PIECES * PIECES) & ((1u << PIECES) - 1));
+                float most = large ? 0.f : mine;
+#pragma unroll
+                for (int o = 1; o < PIECES; o <<= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+                if (pieces <= PIECES / 8 && most > 0.f && amax <= 3.402823466e38f)
+                    ex = max(max((int)(__float_as_uint(most) >> 23) - 127, ex - 100), -100);
+                mul = row_scale(ex);
+                uint64_t first = 0, second = 0;
                 float left = 0.f;
                 uint4 v = raw[i];
 #pragma unroll 1
-                for (int e = 0; e < 4; ++e) {
-                    const float2 x = terms_of(__uint_as_float(v.x << 16) * mul, __uint_as_float(v.x & 0xffff0000u) * mul).left;
-                    left += fabsf(x.x) + fabsf(x.y);
+                for (int e = 0; e < 64; e += 16) {
+                    const Terms t = terms_of(__uint_as_float(v.x << 16) * mul, __uint_as_float(v.x & 0xffff0000u) * mul);
+                    first |= (uint64_t)t.first << e;
+                    second |= (uint64_t)t.second << e;
+                    left += fabsf(t.left.x) + fabsf(t.left.y);
                     v.x = v.y; v.y = v.z; v.z = v.w;
                 }
-                if (left > 0.f) atomicAdd(&lefts[row >> 6], left * __uint_as_float((uint32_t)(127 - 7 + ex) << 23));
+                hi[0] = (uint32_t)first; hi[1] = (uint32_t)(first >> 32);
+                lo[0] = (uint32_t)second; lo[1] = (uint32_t)(second >> 32);
+                if (row < rows && left > 0.f) atomicAdd(&lefts[row >> 6], left * __uint_as_float((uint32_t)(127 - 7 + ex) << 23));
             }
             if (row < rows) {
                 if (piece == 0) exps[row] = (int8_t)ex;
@@ -318,11 +339,14 @@ __device__ __noinline__ void add_left(const AttnDecodeParams &p, const Items &it
     for (int c = 0; row >= 0 && c < HD; c += 8) {
         uint4 v = *reinterpret_cast<const uint4 *>(q + c);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        float amin = INFINITY;
+        float amin = INFINITY, amax = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            amin = fminf(amin, fminf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
-        if (!(amin * mul < 0x1p-6f)) continue;
+        for (int e = 0; e < 4; ++e) {
+            const float x0 = fabsf(__uint_as_float(w[e] << 16)), x1 = fabsf(__uint_as_float(w[e] & 0xffff0000u));
+            amin = fminf(amin, fminf(x0, x1));
+            amax = fmaxf(amax, fmaxf(x0, x1));
+        }
+        if (!(amin * mul < kLeastQuery || amax * mul > kMostQuery)) continue;
 #pragma unroll 1
         for (int e = 0; e < 4; ++e) {
             const float2 x = left_of(v.x);

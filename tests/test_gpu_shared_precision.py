@@ -81,3 +81,30 @@ def test_a_row_does_not_change_others():
     rest = torch.ones(3, 2, 10, dtype=torch.bool)
     rest[1, 1, 4] = False
     assert flag == 0 and torch.equal(out[rest], want[rest]) and torch.equal(lse[rest], want_lse[rest])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [[5], [5, 6, 7], [0, 63], [3, 20, 40], [1, 9, 17, 25, 33, 41, 49, 57]])
+@pytest.mark.parametrize("D,hq", [(1, 12), (8, 24)])
+def test_large_channels_that_meet_small_keys(d, at, D, hq):
+    """Channels of 2^4 to 2^14 times the others, in one piece of a row and in all, whose keys are as much smaller."""
+    g = gen(len(at) + D)
+    case = _case(g, [(20, [1400, 1290, 1300])], 1, d)
+    q = 2 * randn(g, 3, D, hq, d)
+    q[..., at] *= torch.exp2(torch.randint(4, 15, (3, D, hq, 1), generator=g).float())
+    case[0][0][..., at] = 0x01 + 0x80 * torch.randint(0, 2, case[0][0][..., at].shape, generator=g, dtype=torch.uint8)
+    _compare(case, q.bfloat16())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("power", [95, 120])
+def test_elements_further_apart_than_a_score_holds(power):
+    """A channel 2^95 and 2^120 times the others, whose keys are zero.  (Windows of 24 rows, all of them on tcgen05: the
+    warps' kernel rounds what is below 2^-28 of a row's largest.)"""
+    g = gen(power)
+    case = _case(g, [(20, [1400, 1290, 1300])], 1, 128)
+    case[0][0][..., 9] = 0
+    q = randn(g, 3, 2, 12, 128)
+    q[:, :, 1::2, 9] = 2.0 ** power
+    _compare(case, q.bfloat16())
