@@ -13,8 +13,8 @@
 // own.  merge_kernel adds up all parts of a row in a fixed order.
 //
 // Measured (bf16, d = 128, 32 heads over 8): 64 sequences of up to 2048 positions
-// after a prefix of 8192: 96 us, of which the plan 6, the prefix 24, the rests 55 and
-// the sum 11 (each cold and by itself); 32 of up to 512 after 102 400: 104 us (6, 73,
+// after a prefix of 8192: 98 us, of which the plan 7, the prefix 26, the rests 55 and
+// the sum 11 (each cold and by itself); 32 of up to 512 after 102 400: 106 us (6, 75,
 // 17, 10).  The plan and the sum are chains of dependent reads; the rests, a few
 // pages a worker, are the start and end of their items.
 #include <cuda_bf16.h>

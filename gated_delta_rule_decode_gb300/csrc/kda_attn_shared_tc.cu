@@ -29,13 +29,19 @@
 // O of both, 4 x 128 columns.  Rows of a tile that do not exist stay garbage in
 // lanes of their own.
 //
+// Weights are one fp16 term (11 bits), as in the kernels of whole sequences in bf16.
+// Outputs are added up in tensor memory over a worker's whole share of an item,
+// 16 positions at a time, by tensor cores that truncate (the warps' kernel adds
+// page by page to nearest): after 102 400 positions the error against 64 bits is
+// 0.00169 where fp32 sums have 0.00168, the outputs' own rounding.
+//
 // What bounds it: the chain scores - softmax - outputs of a tile, about 2 700
 // cycles a block, of which the tensor pipe has 1 024; every role's code runs in
 // short loops, because code that runs straight through is bound by its own
 // fetching (3 to 5 cycles an instruction).  Measured (d = 128): 32 sequences after
-// one prefix of 102 400 positions, 128 rows, 74 us cold, 2.9 TB/s, tensor pipe 30 %;
+// one prefix of 102 400 positions, 128 rows, 75 us cold, 2.8 TB/s of pages, tensor pipe 29 %;
 // 40 sequences of 7 tokens, 32 heads over 4, after five prefixes of up to 160 pages
-// 52 us, 20 %.  In whole calls the steps were (these two cases): 126 and 109 us with one
+// 54 us, 19 %.  In whole calls the steps were (these two cases): 126 and 109 us with one
 // thread a row; 106 and 81 with two threads a row and rolled loops of 32 columns
 // (straight-line code 138 and 89; without turns 110 and 80); 107 and 74 with loops
 // of 16; the rest is the plan's (kda_attn_shared.cu).
@@ -917,8 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1) parts_tc_kernel(const AttnDecodeP
     if (tid == 0 && S.abort_flag && p.err_flag) atomicOr(p.err_flag, KDA_DEVERR_TIMEOUT);
 }
 
-// The keys: rows of d bytes, 64 of a page and kv head, all of these (a row's number
-// can pass 32 bits).
+// The keys: rows of d bytes, 64 of a page and kv head, all of these.
 template <int HD>
 bool make_map(CUtensorMap *map, const AttnDecodeParams &p) {
     const cuuint64_t dims[3] = {(cuuint64_t)HD, (cuuint64_t)kPage, (cuuint64_t)(p.num_pages * p.Hkv)};

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) summarise_kernel(const CacheSu
             if (p.err_flag && lane == 0) atomicOr(p.err_flag, KDA_DEVERR_SCALE);
             continue;
         }
-        const float f = amax > 0.f ? exp2i(ke - ue) : 0.f;  // (2^9 at most: 448 f <= 127)
+        const float f = amax > 0.f ? exp2i(ke - ue) : 0.f;  // (2^15 at most, for an amax of 2^-9: amax f <= 127)
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -140,7 +140,7 @@ cudaError_t launch_summarise(const CacheSummariseParams &p, cudaStream_t st) {
 // the next group's are asked for as soon as this one's are in registers (their
 // ids and units one group earlier).  A page's 2 d bytes are scored for every row,
 // so with few rows it is bound by HBM, in reads of 256 bytes: 64 sequences of up to
-// 102 400 positions, 8 heads of 4 rows, d = 128, about 30 us of 42, 3.6 TB/s.
+// 102 400 positions, 8 heads of 4 rows, d = 128, about 30 us of 41, 3.6 TB/s.
 // Two buffers a warp at 12 warps an SM took 38.
 constexpr int kScoreWarps = 4;
 // Blocks that a call has at least, where it has the pages: 1, 2, 4, 8 times 152 x 3 take 43.9, 41.9, 41.9, 43.9 us

@@ -181,7 +181,8 @@ KDA_API int kda_cache_evict(int32_t batch, int32_t max_pages, int32_t budget, in
  * (a, b) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) where interleaved; the
  * other channels are y.  t = 2 pi positions[token] turns[i] / 2^64: a table of
  * turns per position in units of 2^-64, modulo one, so that angles are exact to
- * 2^-24 at every position.  fp32 throughout, rounded once.
+ * 2^-24 at every position.  fp32 throughout, rounded once (a row whose sum of
+ * squares leaves fp32's range gives 0).
  *
  *   q, k         dtype [total_tokens][Hq or Hkv][d], tokens q_stride, k_stride apart
  *   q_out, k_out the same, tokens q_out_stride, k_out_stride apart; each may be
